@@ -477,6 +477,189 @@ ra_status ra_seed_signals(ra_handle h, uint64_t signal_value, uint64_t shadow_va
  * RA_ERR_UNSUPPORTED in other builds. */
 ra_status ra_debug_bounds_report(unsigned long long* count, unsigned long long* first_address, int reset);
 
+/* ------------------------------------------------------------------------
+ * Model operators: what a tensor-parallel language model computes around its
+ * sums over ranks, each in one pass over the R rank buffers instead of a
+ * collective and a chain of elementwise passes.
+ *
+ *   ra_norm_*   the end of a block: the R partial products summed,
+ *               normalised, gated, added to the residual stream and
+ *               normalised for the next block; and its gradient
+ *   ra_vocab_*  the vocabulary-parallel head on R column shards of the
+ *               logits: log probabilities of given tokens with entropy and
+ *               top alternatives, distillation from a teacher's top logits,
+ *               and the gradients of both
+ *
+ * Buffers are as above the caller's device memory, addressed by rows: a
+ * stride is the number of elements between rows (at least the row's width;
+ * not looked at for one row or none).  Any start that is a multiple of the element's size
+ * and any stride will do; rows that start on 16-byte boundaries and hold
+ * whole 16-byte vectors are fastest.  An output may not overlap another
+ * buffer of the call, except where a call says so; buffers with the same
+ * stride whose columns are disjoint (column slices of one matrix) do not
+ * overlap.  Calls with no rows return RA_OK.  The types are RA_F32, RA_BF16 and RA_F16 (others:
+ * RA_ERR_UNSUPPORTED); sums, statistics and log probabilities are held in
+ * binary32 and every output is rounded once (the sum over ranks runs in rank
+ * order in binary32, not in the ring's order with its rounding at every hop).
+ * Results are the same on every run.  Calls are asynchronous on `stream` and
+ * may be captured into CUDA graphs, except the first ra_norm_backward of a
+ * handle, which allocates its workspace.  A handle is used by one host thread
+ * at a time; ra_norm_backward calls of one handle must be ordered (they share
+ * that workspace), all other calls may overlap. */
+typedef struct ra_norm_ctx* ra_norm_handle;
+typedef struct ra_vocab_ctx* ra_vocab_handle;
+
+/* Block ends of R ranks and `dim` columns, 1..16384 (more:
+ * RA_ERR_UNSUPPORTED).  The residual stream is RA_F32 or `dtype`, weights and
+ * gate are RA_F32 or `dtype`.  eps >= 0 is added to the mean square, scale
+ * multiplies the block's contribution to the residual stream. */
+ra_status ra_norm_create(int R, int dim, ra_dtype dtype, ra_dtype residual_dtype, ra_dtype param_dtype, float eps,
+                         float scale, ra_norm_handle* out);
+/* Free the handle after synchronising the device.  NULL is a no-op. */
+ra_status ra_norm_destroy(ra_norm_handle h);
+
+/* S = sum_r in[r];  y = S r1 post_weight, r1 = 1 / sqrt(mean S^2 + eps), or
+ * y = S without post_weight;  residual_out = residual + scale * gate * y;
+ * out = residual_out r2 weight, r2 = 1 / sqrt(mean residual_out^2 + eps)
+ * (of the unrounded residual_out).  residual_out == residual (same stride) and
+ * out[q] == in[q] (same stride) are allowed. */
+typedef struct ra_norm_forward_args {
+  size_t rows;
+  const void* const* in;       /* R buffers [rows][dim] of dtype */
+  size_t in_stride;
+  const void* residual;        /* [rows][dim] of residual_dtype */
+  size_t residual_stride;
+  const void* weight;          /* [dim] of param_dtype */
+  const void* post_weight;     /* [dim] of param_dtype, or NULL: no norm before the gate */
+  const void* gate;            /* [gate_rows][dim] of param_dtype, or NULL */
+  size_t gate_rows;            /* divides rows; row t has gate row t / (rows / gate_rows) */
+  void* const* out;            /* `outs` buffers [rows][dim] of dtype, each gets the same */
+  size_t out_stride;
+  int outs;                    /* 1 or R */
+  void* residual_out;          /* [rows][dim] of residual_dtype */
+  size_t residual_out_stride;
+  void* total;                 /* S [rows][dim] of dtype, kept for backward, or NULL */
+  size_t total_stride;
+  float* rstd;                 /* [2][rows], kept for backward, or NULL: r1 (0 without post_weight), r2 */
+} ra_norm_forward_args;
+ra_status ra_norm_forward(ra_norm_handle h, const ra_norm_forward_args* args, void* stream);
+
+/* The gradient.  grad_out are the partial gradients of `out` that the ranks'
+ * next projections give (`grads` of them, summed here), grad_residual_out that
+ * of residual_out.  grad_residual == grad_residual_out (same stride) and
+ * grad_in[q] == grad_out[q] (same stride) are allowed.  Weight and gate
+ * gradients are binary32 sums over the rows, in a fixed order; each may be NULL. */
+typedef struct ra_norm_backward_args {
+  size_t rows;
+  const void* const* grad_out;     /* `grads` buffers [rows][dim] of dtype */
+  size_t grad_out_stride;
+  int grads;                       /* 1 or R */
+  const void* grad_residual_out;   /* [rows][dim] of residual_dtype, or NULL: zero */
+  size_t grad_residual_out_stride;
+  const void* residual_out;        /* what forward wrote */
+  size_t residual_out_stride;
+  const void* total;               /* what forward wrote; may be NULL without post_weight and grad_gate */
+  size_t total_stride;
+  const float* rstd;               /* what forward wrote */
+  const void* weight;
+  const void* post_weight;
+  const void* gate;
+  size_t gate_rows;
+  void* const* grad_in;            /* `outs` buffers [rows][dim] of dtype: the gradient of every rank's partial */
+  size_t grad_in_stride;
+  int outs;                        /* 1 or R */
+  void* grad_residual;             /* [rows][dim] of residual_dtype */
+  size_t grad_residual_stride;
+  float* grad_weight;              /* [dim] */
+  float* grad_post_weight;         /* [dim]; only with post_weight */
+  float* grad_gate;                /* [gate_rows][dim]; only with gate */
+} ra_norm_backward_args;
+ra_status ra_norm_backward(ra_norm_handle h, const ra_norm_backward_args* args, void* stream);
+
+/* A head of V columns (1..2^30) held as R shards: shard r has the columns of
+ * chunk r of ra_chunk_plan(R, V), [r C, min((r+1) C, V)), C = ceil(V / R); the
+ * pointers of empty shards are not looked at.  The logits are divided by
+ * temperature > 0 in every call. */
+ra_status ra_vocab_create(int R, size_t V, ra_dtype dtype, float temperature, ra_vocab_handle* out);
+ra_status ra_vocab_destroy(ra_vocab_handle h);
+
+/* Per row: lse = log sum_j e^{x_j}, x = logits / temperature; logprob =
+ * x_target - lse (0 where the target is negative, NaN where it is no column);
+ * entropy = -sum_j p_j log p_j; the `top` largest logits' columns in falling
+ * order (equal ones: the lower column first; -0 equals +0, NaN is largest)
+ * and their log probabilities.  A row of nothing but -inf has lse -inf, log
+ * probabilities -inf and entropy 0; a row with +inf or NaN has NaN. */
+typedef struct ra_vocab_logprobs_args {
+  size_t rows;
+  const void* const* shards;     /* R buffers */
+  const size_t* strides;         /* R */
+  const int64_t* targets;        /* [rows] */
+  float* logprob;                /* [rows] */
+  float* lse;                    /* [rows] */
+  float* entropy;                /* [rows], or NULL */
+  int top;                       /* 0..32, at most V */
+  int64_t* top_ids;              /* [rows][top] */
+  float* top_logprobs;           /* [rows][top] */
+} ra_vocab_logprobs_args;
+ra_status ra_vocab_logprobs(ra_vocab_handle h, const ra_vocab_logprobs_args* args, void* stream);
+
+/* grads = the gradient of sum_t (grad_logprob_t logprob_t + grad_entropy_t
+ * entropy_t) with respect to the logits; lse and entropy are what forward
+ * wrote.  Zero in a row that a mask leaves nothing of: lse below -1e30 (-inf
+ * everywhere, or the lowest value of RA_F32 or RA_BF16).  grads[r] == shards[r] (same
+ * stride) is allowed. */
+typedef struct ra_vocab_logprobs_backward_args {
+  size_t rows;
+  const void* const* shards;
+  const size_t* strides;
+  const int64_t* targets;
+  const float* lse;
+  const float* entropy;          /* NULL only when grad_entropy is */
+  const float* grad_logprob;     /* [rows] */
+  const float* grad_entropy;     /* [rows], or NULL: zero */
+  void* const* grads;            /* R buffers of dtype */
+  const size_t* grad_strides;
+} ra_vocab_logprobs_backward_args;
+ra_status ra_vocab_logprobs_backward(ra_vocab_handle h, const ra_vocab_logprobs_backward_args* args, void* stream);
+
+/* Distillation from the K largest logits of a teacher, per row: q = softmax
+ * of teacher_logits / temperature over the row's teacher tokens; loss =
+ * temperature^2 sum_k q_k (log q_k - log p_{id_k}).  A token with an id that
+ * is no column, or a teacher logit of -inf, is absent; a row without tokens
+ * has loss 0.  A token may occur twice.  Student logits of -inf give a loss
+ * of +inf where q > 0. */
+typedef struct ra_vocab_distill_args {
+  size_t rows;
+  const void* const* shards;
+  const size_t* strides;
+  int teacher_k;                 /* 1..256 */
+  const int64_t* teacher_ids;    /* [rows][teacher_k] */
+  const void* teacher_logits;    /* [rows][teacher_k] of teacher_dtype */
+  ra_dtype teacher_dtype;        /* RA_F32 or the logits' type */
+  float* loss;                   /* [rows] */
+  float* lse;                    /* [rows] */
+} ra_vocab_distill_args;
+ra_status ra_vocab_distill(ra_vocab_handle h, const ra_vocab_distill_args* args, void* stream);
+
+/* grads = the gradient of sum_t grad_loss_t loss_t with respect to the
+ * student's logits, grad_loss_t temperature (p - q); lse is what forward
+ * wrote.  Zero in a row without teacher tokens and in one with lse below -1e30.
+ * grads[r] == shards[r] (same stride) is allowed. */
+typedef struct ra_vocab_distill_backward_args {
+  size_t rows;
+  const void* const* shards;
+  const size_t* strides;
+  int teacher_k;
+  const int64_t* teacher_ids;
+  const void* teacher_logits;
+  ra_dtype teacher_dtype;
+  const float* lse;
+  const float* grad_loss;        /* [rows] */
+  void* const* grads;
+  const size_t* grad_strides;
+} ra_vocab_distill_backward_args;
+ra_status ra_vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distill_backward_args* args, void* stream);
+
 /* Text of the calling thread's last error ("" if none). */
 const char* ra_last_error(void);
 

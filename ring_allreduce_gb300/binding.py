@@ -129,6 +129,18 @@ EXPORTED = {
     "ra_seed_signals": (_ST, [_P, ctypes.c_uint64, ctypes.c_uint64]),
     "ra_debug_bounds_report": (_ST, [ctypes.POINTER(ctypes.c_ulonglong), ctypes.POINTER(ctypes.c_ulonglong),
                                      ctypes.c_int]),
+    # model operators: the argument blocks are the structures of operators.py
+    "ra_norm_create": (_ST, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                             ctypes.c_float, ctypes.c_float, ctypes.POINTER(_P)]),
+    "ra_norm_destroy": (_ST, [_P]),
+    "ra_norm_forward": (_ST, [_P, _P, _P]),
+    "ra_norm_backward": (_ST, [_P, _P, _P]),
+    "ra_vocab_create": (_ST, [ctypes.c_int, _SZ, ctypes.c_int, ctypes.c_float, ctypes.POINTER(_P)]),
+    "ra_vocab_destroy": (_ST, [_P]),
+    "ra_vocab_logprobs": (_ST, [_P, _P, _P]),
+    "ra_vocab_logprobs_backward": (_ST, [_P, _P, _P]),
+    "ra_vocab_distill": (_ST, [_P, _P, _P]),
+    "ra_vocab_distill_backward": (_ST, [_P, _P, _P]),
     "ra_last_error": (ctypes.c_char_p, []),
     "ra_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }

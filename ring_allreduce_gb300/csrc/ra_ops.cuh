@@ -1,0 +1,89 @@
+// ra_ops.cuh -- device building blocks of the model operators: conversions
+// between the activations' types and binary32, groups of a row's columns, and
+// sums over a block.
+#pragma once
+
+#include <float.h>
+#include <math.h>
+
+#include "ra_device.cuh"
+#include "ra_ops.h"
+
+namespace ra {
+
+template <class D> __device__ __forceinline__ float widen(typename D::T v);
+template <> __device__ __forceinline__ float widen<DF32>(float v) { return v; }
+template <> __device__ __forceinline__ float widen<DBF16>(uint16_t v) { return bf16_widen(v); }
+template <> __device__ __forceinline__ float widen<DF16>(uint16_t v) {
+  return __half2float(__ushort_as_half(v));
+}
+
+// One rounding to the activations' type, to nearest even.
+template <class D> __device__ __forceinline__ typename D::T narrow(float v);
+template <> __device__ __forceinline__ float narrow<DF32>(float v) { return v; }
+template <> __device__ __forceinline__ uint16_t narrow<DBF16>(float v) { return bf16_round(v); }
+template <> __device__ __forceinline__ uint16_t narrow<DF16>(float v) {
+  return __half_as_ushort(__float2half_rn(v));
+}
+
+// The elements of one 16-byte vector as binary32, and back.
+template <class D> __device__ __forceinline__ void unpack(uint4 v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (sizeof(typename D::T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = widen<D>((typename D::T)(w[i] & 0xFFFFu));
+      x[2 * i + 1] = widen<D>((typename D::T)(w[i] >> 16));
+    }
+  }
+}
+
+template <class D> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<DBF16>(float lo, float hi) {
+  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&p);
+}
+template <> __device__ __forceinline__ uint32_t pack2<DF16>(float lo, float hi) {
+  __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&p);
+}
+template <> __device__ __forceinline__ uint32_t pack2<DF32>(float lo, float) { return __float_as_uint(lo); }
+
+template <class D> __device__ __forceinline__ uint4 pack(const float* x) {
+  if (sizeof(typename D::T) == 4)
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  return make_uint4(pack2<D>(x[0], x[1]), pack2<D>(x[2], x[3]), pack2<D>(x[4 % D::kVec], x[5 % D::kVec]),
+                    pack2<D>(x[6 % D::kVec], x[7 % D::kVec]));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
+  return v;
+}
+
+// The larger value; NaN when either is (a masked place that holds NaN must
+// not vanish from a maximum).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, s));
+  return v;
+}
+
+// 2^x, to about 2 ulp (ex2.approx: 0 for arguments below the subnormals).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+}  // namespace ra
