@@ -33,8 +33,12 @@ SOURCES = ["ra_host.cpp", "ra_direct.cu", "ra_round.cu", "ra_persistent.cu", "ra
 # (source, object stem, preprocessor definitions): ra_direct_inst.cu is
 # compiled once per dtype so its instantiations build in parallel
 DTYPES = ["RA_F32", "RA_BF16", "RA_I32", "RA_F16", "RA_F64", "RA_I64"]
+# ... and ra_norm_inst.cu per pair of activations' and residual stream's types
+NORM_TYPES = [("DF32", "DF32"), ("DBF16", "DBF16"), ("DBF16", "DF32"), ("DF16", "DF16"), ("DF16", "DF32")]
 UNITS = ([(src, os.path.splitext(src)[0], {}) for src in SOURCES] +
-         [("ra_direct_inst.cu", "ra_direct_" + dt[3:].lower(), {"RA_INST_DTYPE": dt}) for dt in DTYPES])
+         [("ra_direct_inst.cu", "ra_direct_" + dt[3:].lower(), {"RA_INST_DTYPE": dt}) for dt in DTYPES] +
+         [("ra_norm_inst.cu", f"ra_norm_{d}_{rd}".lower(), {"RA_INST_D": d, "RA_INST_RD": rd})
+          for d, rd in NORM_TYPES])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # IEEE arithmetic throughout: no fast-math, no flush to zero, no contraction.
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-ftz=false",
@@ -65,7 +69,7 @@ KERNEL_SOURCES = {
     "bcast": ["ra_bcast.cu", "ra_device.cuh", "ra_internal.h"],
     "local": ["ra_local.cu", "ra_device.cuh", "ra_internal.h"],
     "ll": ["ra_ll.cu", "ra_ll.h", "ra_device.cuh", "ra_internal.h"],
-    "norm": ["ra_norm.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
+    "norm": ["ra_norm.cu", "ra_norm.cuh", "ra_norm_inst.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
     "vocab": ["ra_vocab.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
 }
 

@@ -59,6 +59,12 @@ template <class D> __device__ __forceinline__ uint4 pack(const float* x) {
                     pack2<D>(x[6 % D::kVec], x[7 % D::kVec]));
 }
 
+// A vector that many rows read: cached.
+__device__ __forceinline__ uint4 ld_plain(const uint4* p) {
+  if (!RA_ACCESS_OK(p, 16u, 1u)) return make_uint4(0u, 0u, 0u, 0u);
+  return *p;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);

@@ -19,17 +19,20 @@ ValueError, what the library refuses raises RAError; nothing is launched then.
 """
 
 import ctypes
+from array import array
 
 import torch
 
 from . import binding
-from .binding import RAError, Status, _lib, _ST, _SZ, _P
+from .binding import RAError, _lib, _ST, _SZ, _P
 
 __all__ = ["BlockNorm", "VocabHead"]
 
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 _CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 3}
 _CODE_OF = {k: _CODE[v] for k, v in _TORCH.items()}
+_byref = ctypes.byref
+_current_stream = torch._C._cuda_getCurrentRawStream   # the raw handle of torch's current stream on a device
 
 
 class _NormForward(ctypes.Structure):
@@ -86,52 +89,65 @@ class _Handle:
         self.dtype = _TORCH[dtype]
         self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
 
+    # A call's checks run before every launch, for a few microseconds in all: a
+    # decode step is hardly longer.  So the common case (a contiguous tensor)
+    # is asked for first, and texts are made only for an error.
+
     def _flat(self, name, t, shape, dtype):
         """Address of a contiguous tensor."""
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-                and t.get_device() == self.device):
-            _fail(name, t, f"a contiguous {dtype} {tuple(shape)} on cuda:{self.device}")
-        return t.data_ptr()
+        if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+                and t.get_device() == self.device:
+            return t.data_ptr()
+        _fail(name, t, f"a contiguous {dtype} {tuple(shape)} on cuda:{self.device}")
 
     def _rows(self, name, t, shape, dtype):
         """Address and row stride of a tensor [rows, width] whose rows are contiguous."""
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-                and t.get_device() == self.device):
-            _fail(name, t, f"{dtype} {tuple(shape)} on cuda:{self.device}")
-        st = t.stride()
-        if st[1] != 1 and shape[1] > 1:
-            _fail(name, t, "a contiguous last axis")
-        return t.data_ptr(), st[0]
+        if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == self.device:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1]
+            step, one = t.stride()
+            if one == 1 or shape[1] <= 1:
+                return t.data_ptr(), step
+        _fail(name, t, f"{dtype} {tuple(shape)}, its last axis contiguous, on cuda:{self.device}")
 
-    def _ranks(self, name, t, counts, shape, dtype):
-        """C array of rank buffers [rows, width], their common row stride and
-        their number (one of `counts`)."""
+    def _ranks(self, name, t, shape, dtype, only=None):
+        """The addresses of rank buffers [rows, width] as a C array (which has
+        to stay referenced until the call has returned) and where it is, their
+        common row stride and their number: R, or also 1 where `only` is not R."""
+        n, rows, width = len(t), *shape
+        if n != self.R and (n != 1 or only == self.R):
+            raise ValueError(f"{name}: {'' if only == self.R else '1 or '}{self.R} rank buffers are expected, got {n}")
         if isinstance(t, torch.Tensor):
-            if t.dim() != 3 or t.shape[0] not in counts:
-                _fail(name, t, f"{' or '.join(map(str, counts))} rank buffers {tuple(shape)}")
-            n = t.shape[0]
-            step = t.stride(0) * t.element_size() if n > 1 else 0
-            base, stride = self._rows(name, t[0], shape, dtype)
-            return (_P * n)(*[base + r * step for r in range(n)]), stride, n
-        if len(t) not in counts:
-            raise ValueError(f"{name}: {' or '.join(map(str, counts))} rank buffers are expected, got {len(t)}")
-        got = [self._rows(f"{name}[{r}]", x, shape, dtype) for r, x in enumerate(t)]
-        if shape[0] > 1 and any(s != got[0][1] for _, s in got):
-            raise ValueError(f"{name}: the rank buffers' rows have different strides")
-        return (_P * len(got))(*[p for p, _ in got]), got[0][1], len(got)
+            if t.dtype is dtype and t.shape == (n, rows, width) and t.get_device() == self.device:
+                base, rank, stride = t.data_ptr(), rows * width, width
+                if not t.is_contiguous():
+                    rank, stride, one = t.stride()
+                    if one != 1 and width > 1:
+                        _fail(name, t, "a contiguous last axis")
+                step = rank * dtype.itemsize
+                ptrs = array("Q", range(base, base + n * step, step) if step else [base] * n)
+                return ptrs, ptrs.buffer_info()[0], stride, n
+            _fail(name, t, f"{n} x {dtype} {tuple(shape)} on cuda:{self.device}")
+        got = [self._rows(name, x, shape, dtype) for x in t]
+        stride = got[0][1]
+        if rows > 1:
+            for _, s in got:
+                if s != stride:
+                    raise ValueError(f"{name}: the rank buffers' rows have different strides")
+        ptrs = array("Q", [p for p, _ in got])
+        return ptrs, ptrs.buffer_info()[0], stride, n
 
     def _call(self, fn, args, stream, tensors):
         if self._h is None:
             raise ValueError("the handle is closed")
         if stream is None:
-            # the raw handle of torch's current stream on the handle's device
-            raw = torch.cuda.current_stream(self.device).cuda_stream
+            raw = _current_stream(self.device)
         else:
             raw = binding._stream(stream)
             _keep(tensors, stream, self.device)
-        st = fn(self._h, ctypes.addressof(args), raw)
-        if st != Status.OK:
-            raise RAError(st, binding.ra_last_error())
+        status = fn(self._h, _byref(args), raw)
+        if status:
+            raise RAError(status, binding.ra_last_error())
 
     def close(self):
         if self._h is not None:
@@ -190,14 +206,12 @@ class BlockNorm(_Handle):
                                            _CODE_OF[param_dtype], self.eps, self.scale, ctypes.byref(h)))
         self._h = h
 
-    def _params(self, a, rows, weight, post_weight, gate):
-        one = (self.dim,)
-        a.weight = self._flat("weight", weight, one, self.param_dtype)
-        if post_weight is not None:
-            a.post_weight = self._flat("post_weight", post_weight, one, self.param_dtype)
-        if gate is not None:
-            a.gate_rows = gate.shape[0] if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 0
-            a.gate = self._flat("gate", gate, (a.gate_rows, self.dim), self.param_dtype)
+    def _gate(self, gate):
+        """Address and rows of the gate (0, 0 without one)."""
+        if gate is None:
+            return None, 0
+        rows = gate.shape[0] if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 0
+        return self._flat("gate", gate, (rows, self.dim), self.param_dtype), rows
 
     def forward(self, parts, residual, weight, outs, residual_out, post_weight=None, gate=None, total=None,
                 rstd=None, stream=None):
@@ -211,22 +225,20 @@ class BlockNorm(_Handle):
         [2, T] (float32) keep what backward reads: S, and the two norms' factors."""
         if not isinstance(residual, torch.Tensor) or residual.dim() != 2:
             raise ValueError(f"residual: a tensor [rows, {self.dim}] is expected")
-        T = residual.shape[0]
+        T, one, dt, rdt = residual.shape[0], (self.dim,), self.dtype, self.residual_dtype
         shape = (T, self.dim)
-        a = _NormForward(rows=T)
-        # the arrays stay referenced until the call has returned
-        ins, a.in_stride, _ = self._ranks("parts", parts, (self.R,), shape, self.dtype)
-        to, a.out_stride, a.outs = self._ranks("outs", outs, (1, self.R), shape, self.dtype)
-        a.in_, a.out = ctypes.addressof(ins), ctypes.addressof(to)
-        a.residual, a.residual_stride = self._rows("residual", residual, shape, self.residual_dtype)
-        a.residual_out, a.residual_out_stride = self._rows("residual_out", residual_out, shape, self.residual_dtype)
-        self._params(a, T, weight, post_weight, gate)
-        if total is not None:
-            a.total, a.total_stride = self._rows("total", total, shape, self.dtype)
-        if rstd is not None:
-            a.rstd = self._flat("rstd", rstd, (2, T), torch.float32)
-        self._call(_lib.ra_norm_forward, a, stream,
-                   (parts, residual, weight, outs, residual_out, post_weight, gate, total, rstd))
+        ins, ins_at, in_stride, _ = self._ranks("parts", parts, shape, dt, self.R)
+        to, to_at, out_stride, n = self._ranks("outs", outs, shape, dt)
+        res, res_stride = self._rows("residual", residual, shape, rdt)
+        res_out, res_out_stride = self._rows("residual_out", residual_out, shape, rdt)
+        g, gate_rows = self._gate(gate)
+        tot, tot_stride = (None, 0) if total is None else self._rows("total", total, shape, dt)
+        self._call(_lib.ra_norm_forward, _NormForward(
+            T, ins_at, in_stride, res, res_stride, self._flat("weight", weight, one, self.param_dtype),
+            None if post_weight is None else self._flat("post_weight", post_weight, one, self.param_dtype),
+            g, gate_rows, to_at, out_stride, n, res_out, res_out_stride, tot, tot_stride,
+            None if rstd is None else self._flat("rstd", rstd, (2, T), torch.float32)), stream,
+            (parts, residual, weight, outs, residual_out, post_weight, gate, total, rstd))
 
     def backward(self, grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins, grad_residual,
                  grad_weight=None, post_weight=None, gate=None, total=None, grad_post_weight=None, grad_gate=None,
@@ -243,31 +255,26 @@ class BlockNorm(_Handle):
         grad_ins may be grad_outs."""
         if not isinstance(residual_out, torch.Tensor) or residual_out.dim() != 2:
             raise ValueError(f"residual_out: a tensor [rows, {self.dim}] is expected")
-        T = residual_out.shape[0]
-        shape, one = (T, self.dim), (self.dim,)
-        a = _NormBackward(rows=T)
-        ins, a.grad_out_stride, a.grads = self._ranks("grad_outs", grad_outs, (1, self.R), shape, self.dtype)
-        to, a.grad_in_stride, a.outs = self._ranks("grad_ins", grad_ins, (1, self.R), shape, self.dtype)
-        a.grad_out, a.grad_in = ctypes.addressof(ins), ctypes.addressof(to)
-        if grad_residual_out is not None:
-            a.grad_residual_out, a.grad_residual_out_stride = self._rows(
-                "grad_residual_out", grad_residual_out, shape, self.residual_dtype)
-        a.residual_out, a.residual_out_stride = self._rows("residual_out", residual_out, shape, self.residual_dtype)
-        a.grad_residual, a.grad_residual_stride = self._rows("grad_residual", grad_residual, shape,
-                                                             self.residual_dtype)
-        self._params(a, T, weight, post_weight, gate)
-        if total is not None:
-            a.total, a.total_stride = self._rows("total", total, shape, self.dtype)
-        a.rstd = self._flat("rstd", rstd, (2, T), torch.float32)
-        if grad_weight is not None:
-            a.grad_weight = self._flat("grad_weight", grad_weight, one, torch.float32)
-        if grad_post_weight is not None:
-            a.grad_post_weight = self._flat("grad_post_weight", grad_post_weight, one, torch.float32)
-        if grad_gate is not None:
-            a.grad_gate = self._flat("grad_gate", grad_gate, (a.gate_rows, self.dim), torch.float32)
-        self._call(_lib.ra_norm_backward, a, stream,
-                   (grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins, grad_residual, grad_weight,
-                    post_weight, gate, total, grad_post_weight, grad_gate))
+        T, one, dt, rdt, f32 = residual_out.shape[0], (self.dim,), self.dtype, self.residual_dtype, torch.float32
+        shape = (T, self.dim)
+        ins, ins_at, in_stride, grads = self._ranks("grad_outs", grad_outs, shape, dt)
+        to, to_at, out_stride, n = self._ranks("grad_ins", grad_ins, shape, dt)
+        gro, gro_stride = (None, 0) if grad_residual_out is None else \
+            self._rows("grad_residual_out", grad_residual_out, shape, rdt)
+        ro, ro_stride = self._rows("residual_out", residual_out, shape, rdt)
+        gr, gr_stride = self._rows("grad_residual", grad_residual, shape, rdt)
+        g, gate_rows = self._gate(gate)
+        tot, tot_stride = (None, 0) if total is None else self._rows("total", total, shape, dt)
+        self._call(_lib.ra_norm_backward, _NormBackward(
+            T, ins_at, in_stride, grads, gro, gro_stride, ro, ro_stride, tot, tot_stride,
+            self._flat("rstd", rstd, (2, T), f32), self._flat("weight", weight, one, self.param_dtype),
+            None if post_weight is None else self._flat("post_weight", post_weight, one, self.param_dtype),
+            g, gate_rows, to_at, out_stride, n, gr, gr_stride,
+            None if grad_weight is None else self._flat("grad_weight", grad_weight, one, f32),
+            None if grad_post_weight is None else self._flat("grad_post_weight", grad_post_weight, one, f32),
+            None if grad_gate is None else self._flat("grad_gate", grad_gate, (gate_rows, self.dim), f32)), stream,
+            (grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins, grad_residual, grad_weight,
+             post_weight, gate, total, grad_post_weight, grad_gate))
 
 
 class VocabHead(_Handle):
@@ -285,20 +292,25 @@ class VocabHead(_Handle):
         self._h = h
         #: columns of each rank's shard
         self.widths = [n for _, n in binding.ra_chunk_plan(self.R, self.vocab)]
+        self._widths = array("Q", [0] * self.R + self.widths)   # addresses and strides of contiguous shards
 
     def _shards(self, name, t, T):
-        """C arrays of the shards' addresses and row strides."""
-        if len(t) != self.R:
-            raise ValueError(f"{name}: {self.R} shards are expected, got {len(t)}")
-        ptrs, strides = [], []
-        for r, (x, w) in enumerate(zip(t, self.widths)):
-            if w:
-                p, s = self._rows(f"{name}[{r}]", x, (T, w), self.dtype)
-            else:
-                p, s = None, 0      # a shard without columns: nothing to look at
-            ptrs.append(p)
-            strides.append(s)
-        return (_P * self.R)(*ptrs), (_SZ * self.R)(*strides)
+        """C array of the shards' addresses, then of their row strides, and
+        where the two are."""
+        R, dt, device = self.R, self.dtype, self.device
+        if len(t) != R:
+            raise ValueError(f"{name}: {R} shards are expected, got {len(t)}")
+        both = array("Q", self._widths)
+        for r, x in enumerate(t):
+            shape = (T, self.widths[r])
+            if shape[1]:      # a shard without columns is not looked at
+                if isinstance(x, torch.Tensor) and x.dtype is dt and x.shape == shape and x.is_contiguous() \
+                        and x.get_device() == device:
+                    both[r] = x.data_ptr()
+                else:
+                    both[r], both[R + r] = self._rows(name, x, shape, dt)
+        at = both.buffer_info()[0]
+        return both, at, at + 8 * R
 
     @staticmethod
     def _count(name, t):
@@ -311,58 +323,47 @@ class VocabHead(_Handle):
         negative, NaN where beyond the vocabulary), lse = log sum exp, entropy,
         and the K = top_ids.shape[1] largest logits' columns (int64, equal ones
         lowest first) with their log probabilities, K at most 32."""
-        T = self._count("targets", targets)
-        one = (T,)
-        a = _Logprobs(rows=T)
-        p, s = self._shards("shards", shards, T)
-        a.shards, a.strides = ctypes.addressof(p), ctypes.addressof(s)
-        a.targets = self._flat("targets", targets, one, torch.int64)
-        a.logprob = self._flat("logprob", logprob, one, torch.float32)
-        a.lse = self._flat("lse", lse, one, torch.float32)
-        if entropy is not None:
-            a.entropy = self._flat("entropy", entropy, one, torch.float32)
+        T, f32 = self._count("targets", targets), torch.float32
+        one, K, ti, tl = (T,), 0, None, None
+        x, x_at, x_strides = self._shards("shards", shards, T)
         if (top_ids is None) != (top_logprobs is None):
             raise ValueError("top_ids and top_logprobs go together")
         if top_ids is not None:
             K = top_ids.shape[1] if isinstance(top_ids, torch.Tensor) and top_ids.dim() == 2 else 0
-            a.top = K
-            a.top_ids = self._flat("top_ids", top_ids, (T, K), torch.int64)
-            a.top_logprobs = self._flat("top_logprobs", top_logprobs, (T, K), torch.float32)
-        self._call(_lib.ra_vocab_logprobs, a, stream,
-                   (shards, targets, logprob, lse, entropy, top_ids, top_logprobs))
+            ti = self._flat("top_ids", top_ids, (T, K), torch.int64)
+            tl = self._flat("top_logprobs", top_logprobs, (T, K), f32)
+        self._call(_lib.ra_vocab_logprobs, _Logprobs(
+            T, x_at, x_strides, self._flat("targets", targets, one, torch.int64),
+            self._flat("logprob", logprob, one, f32), self._flat("lse", lse, one, f32),
+            None if entropy is None else self._flat("entropy", entropy, one, f32), K, ti, tl), stream,
+            (shards, targets, logprob, lse, entropy, top_ids, top_logprobs))
 
     def logprobs_backward(self, shards, targets, lse, grad_logprob, grads, entropy=None, grad_entropy=None,
                           stream=None):
         """grads (R shards, may be the logits' own) = the logits' gradient of
         sum(grad_logprob * logprob) + sum(grad_entropy * entropy); lse and
         entropy are what logprobs wrote."""
-        T = self._count("targets", targets)
-        one = (T,)
-        a = _LogprobsBackward(rows=T)
-        p, s = self._shards("shards", shards, T)
-        gp, gs = self._shards("grads", grads, T)
-        a.shards, a.strides = ctypes.addressof(p), ctypes.addressof(s)
-        a.grads, a.grad_strides = ctypes.addressof(gp), ctypes.addressof(gs)
-        a.targets = self._flat("targets", targets, one, torch.int64)
-        a.lse = self._flat("lse", lse, one, torch.float32)
-        a.grad_logprob = self._flat("grad_logprob", grad_logprob, one, torch.float32)
+        T, f32 = self._count("targets", targets), torch.float32
+        one, H, gh = (T,), None, None
+        x, x_at, x_strides = self._shards("shards", shards, T)
+        g, g_at, g_strides = self._shards("grads", grads, T)
         if grad_entropy is not None:
-            a.grad_entropy = self._flat("grad_entropy", grad_entropy, one, torch.float32)
-            a.entropy = self._flat("entropy", entropy, one, torch.float32)
-        self._call(_lib.ra_vocab_logprobs_backward, a, stream,
-                   (shards, targets, lse, grad_logprob, grads, entropy, grad_entropy))
+            gh = self._flat("grad_entropy", grad_entropy, one, f32)
+            H = self._flat("entropy", entropy, one, f32)
+        self._call(_lib.ra_vocab_logprobs_backward, _LogprobsBackward(
+            T, x_at, x_strides, self._flat("targets", targets, one, torch.int64),
+            self._flat("lse", lse, one, f32), H, self._flat("grad_logprob", grad_logprob, one, f32), gh,
+            g_at, g_strides), stream,
+            (shards, targets, lse, grad_logprob, grads, entropy, grad_entropy))
 
-    def _teacher(self, a, teacher_ids, teacher_logits):
+    def _teacher(self, teacher_ids, teacher_logits):
+        """Rows, tokens per row, the two addresses and the type's code."""
         if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2:
             raise ValueError("teacher_ids: a tensor [rows, K] is expected")
-        T, K = teacher_ids.shape
-        a.rows, a.teacher_k = T, K
-        a.teacher_ids = self._flat("teacher_ids", teacher_ids, (T, K), torch.int64)
-        dt = torch.float32 if isinstance(teacher_logits, torch.Tensor) and teacher_logits.dtype is torch.float32 \
-            else self.dtype
-        a.teacher_logits = self._flat("teacher_logits", teacher_logits, (T, K), dt)
-        a.teacher_dtype = _CODE[dt]
-        return T
+        shape = teacher_ids.shape
+        dt = torch.float32 if getattr(teacher_logits, "dtype", None) is torch.float32 else self.dtype
+        return (*shape, self._flat("teacher_ids", teacher_ids, shape, torch.int64),
+                self._flat("teacher_logits", teacher_logits, shape, dt), _CODE[dt])
 
     def distill(self, shards, teacher_ids, teacher_logits, loss, lse, stream=None):
         """Per row: q = softmax(teacher_logits / temperature) over the row's K
@@ -370,24 +371,19 @@ class VocabHead(_Handle):
         loss = temperature^2 sum q (log q - log p), lse = log sum exp of the
         student's logits / temperature.  teacher_ids: int64 [T, K];
         teacher_logits: float32 or the logits' type."""
-        a = _Distill()
-        T = self._teacher(a, teacher_ids, teacher_logits)
-        p, s = self._shards("shards", shards, T)
-        a.shards, a.strides = ctypes.addressof(p), ctypes.addressof(s)
-        a.loss = self._flat("loss", loss, (T,), torch.float32)
-        a.lse = self._flat("lse", lse, (T,), torch.float32)
-        self._call(_lib.ra_vocab_distill, a, stream, (shards, teacher_ids, teacher_logits, loss, lse))
+        T, K, ids, logits, code = self._teacher(teacher_ids, teacher_logits)
+        x, x_at, x_strides = self._shards("shards", shards, T)
+        self._call(_lib.ra_vocab_distill, _Distill(
+            T, x_at, x_strides, K, ids, logits, code, self._flat("loss", loss, (T,), torch.float32),
+            self._flat("lse", lse, (T,), torch.float32)), stream, (shards, teacher_ids, teacher_logits, loss, lse))
 
     def distill_backward(self, shards, teacher_ids, teacher_logits, lse, grad_loss, grads, stream=None):
         """grads (R shards, may be the logits' own) = the logits' gradient of
         sum(grad_loss * loss); lse is what distill wrote."""
-        a = _DistillBackward()
-        T = self._teacher(a, teacher_ids, teacher_logits)
-        p, s = self._shards("shards", shards, T)
-        gp, gs = self._shards("grads", grads, T)
-        a.shards, a.strides = ctypes.addressof(p), ctypes.addressof(s)
-        a.grads, a.grad_strides = ctypes.addressof(gp), ctypes.addressof(gs)
-        a.lse = self._flat("lse", lse, (T,), torch.float32)
-        a.grad_loss = self._flat("grad_loss", grad_loss, (T,), torch.float32)
-        self._call(_lib.ra_vocab_distill_backward, a, stream,
-                   (shards, teacher_ids, teacher_logits, lse, grad_loss, grads))
+        T, K, ids, logits, code = self._teacher(teacher_ids, teacher_logits)
+        x, x_at, x_strides = self._shards("shards", shards, T)
+        g, g_at, g_strides = self._shards("grads", grads, T)
+        self._call(_lib.ra_vocab_distill_backward, _DistillBackward(
+            T, x_at, x_strides, K, ids, logits, code, self._flat("lse", lse, (T,), torch.float32),
+            self._flat("grad_loss", grad_loss, (T,), torch.float32), g_at, g_strides), stream,
+            (shards, teacher_ids, teacher_logits, lse, grad_loss, grads))
