@@ -6,8 +6,8 @@ namespace ra {
 namespace norm {
 
 #define RA_NORM_EXTERN(D, RD)                                                                                      \
-  extern template cudaError_t run_forward<D, RD>(const Shape&, int, const NormForward&, unsigned, cudaStream_t);   \
-  extern template cudaError_t run_backward<D, RD>(const Shape&, int, const NormBackward&, const Deal&, unsigned,   \
+  extern template cudaError_t run_forward<D, RD>(const Shape&, bool, const NormForward&, unsigned, cudaStream_t);   \
+  extern template cudaError_t run_backward<D, RD>(const Shape&, bool, const NormBackward&, const Deal&, unsigned,   \
                                                   cudaStream_t);
 RA_NORM_EXTERN(DF32, DF32)
 RA_NORM_EXTERN(DBF16, DBF16)
@@ -90,21 +90,21 @@ size_t norm_workspace_floats(int dim, int sms) {
   return 4 * most * (size_t)dim;
 }
 
-cudaError_t launch_norm_forward(int dtype, int rdtype, int grain, const NormForward& a, int sms, cudaStream_t st) {
+cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormForward& a, int sms, cudaStream_t st) {
   const Shape s = forward_shape(a.dim, vec_of(dtype));
   const int64_t want = (a.rows + s.rows - 1) / s.rows, most = most_ctas(s, sms);
   const unsigned grid = (unsigned)(want < most ? want : most);
   return with_types(dtype, rdtype, [&](auto d, auto r) {
-    return run_forward<decltype(d), decltype(r)>(s, grain, a, grid, st);
+    return run_forward<decltype(d), decltype(r)>(s, aligned, a, grid, st);
   });
 }
 
-cudaError_t launch_norm_backward(int dtype, int rdtype, int grain, const NormBackward& a, int sms, cudaStream_t st) {
+cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const NormBackward& a, int sms, cudaStream_t st) {
   const Shape s = backward_shape(a.dim, vec_of(dtype));
   const Deal dl = make_deal(a, s, sms);
   const unsigned grid = (unsigned)(dl.workers / s.rows);
   cudaError_t e = with_types(dtype, rdtype, [&](auto d, auto r) {
-    return run_backward<decltype(d), decltype(r)>(s, grain, a, dl, grid, st);
+    return run_backward<decltype(d), decltype(r)>(s, aligned, a, dl, grid, st);
   });
   if (e != cudaSuccess) return e;
   const bool gates = a.grad_gate && dl.parts > 1;

@@ -18,10 +18,13 @@
 // rows by the latency of two sums over a block.
 //
 // The rows reach the registers through a ring of kDepth slots in shared
-// memory: a slot holds one tensor's part of a row, every thread copies its own
-// columns into it (cp.async) kDepth - 1 slots ahead and reads them back
-// itself, so the copies need no barrier and run on through the sums over the
-// block and into the next row.
+// memory: a slot holds one tensor's part of a row, every warp copies its own
+// columns into its part of it (cp.async) kDepth - 1 slots ahead and reads them
+// back itself, so the copies need no barrier of the block and run on through
+// the sums over it and into the next row.  What binds next is the
+// instructions per column: arithmetic is done on pairs of columns
+// (fma.rn.f32x2 and its like), and a warp's columns lie side by side, so that
+// all addresses within a row are constants away from the warp's first one.
 #pragma once
 
 #include "ra_ops.cuh"
@@ -46,283 +49,345 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
   return warp_sum(lane < warps ? buf[lane] : 0.0f);
 }
 
-__device__ __forceinline__ void copy_async(uint32_t smem, const void* p, int bytes) {
-  if (!RA_ACCESS_OK(p, (unsigned)bytes, 1u)) return;
-  if (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(p) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t smem, const char* p) {
+  if (!RA_ACCESS_OK(p, 16u, 1u)) return;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(p) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The columns of one thread, for rows of type D: kEach of them in pieces of U
-// neighbouring columns, a row's threads side by side.  GRAIN is what every
-// row of every buffer of the call is aligned to, and whole multiples of:
-//   16 bytes  pieces of one 16-byte vector
-//   4 bytes   pieces of 4 bytes (two columns of a 16-bit type)
-//   2 bytes   single columns of a 16-bit type, loaded without the ring
-//             (cp.async copies no less than 4 bytes)
-template <class D, int VPT, int GRAIN, int MAXT> struct Cols {
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// The columns of one thread, for rows of type D: kEach of them (as pairs), of
+// a warp's 32 kEach neighbouring columns.
+//   AL   every row of every buffer of the call starts on a 16-byte boundary
+//        and holds whole 16-byte vectors: a thread has whole vectors, the
+//        warp's side by side.
+//   else rows may start on any element: a thread has every 32nd column, and a
+//        slot holds the 16-byte vectors that cover the warp's columns, shifted
+//        as they lie in memory (bytes of the neighbouring rows come along and
+//        are not used).
+template <class D, int VPT, bool AL, int MAXT> struct Cols {
   using T = typename D::T;
-  static constexpr int kEach = D::kVec * VPT;
-  static constexpr int U = GRAIN / (int)sizeof(T);
-  static constexpr int kPieces = kEach / U;
-  static constexpr bool kRing = GRAIN >= 4;
-  static constexpr int kSlotBytes = kEach * (int)sizeof(T);   // per thread
-  // slots of the ring: 8, or what 192 KB hold for a row of MAXT threads
-  static constexpr int kDepth = 192 * 1024 / (MAXT * kSlotBytes) < 8 ? 192 * 1024 / (MAXT * kSlotBytes) : 8;
+  static constexpr int V = D::kVec;
+  static constexpr int kEach = V * VPT, kPairs = kEach / 2;
+  static constexpr int kWarpBytes = 32 * kEach * (int)sizeof(T) + (AL ? 0 : 16);   // of a slot
+  // slots of the ring: 8, or what 192 KB hold for MAXT threads
+  static constexpr int kFit = 192 * 1024 / (MAXT / 32 * kWarpBytes);
+  static constexpr int kDepth = kFit < 8 ? kFit : 8;
 
-  static __device__ __forceinline__ int column(int k) { return (k * (int)blockDim.x + (int)threadIdx.x) * U; }
+  int lane, base;   // base: the warp's first column
+  int left;         // columns of the row from the thread's first on
+  int dim;
+  __device__ __forceinline__ explicit Cols(int columns) : dim(columns) {
+    lane = threadIdx.x & 31;
+    base = (int)(threadIdx.x >> 5) * 32 * kEach;
+    left = dim - base - (AL ? lane * V : lane);
+  }
+  // pieces: AL a vector, else a column
+  static constexpr int kPieces = AL ? VPT : kEach;
+  static constexpr int kStep = AL ? 32 * V : 32;   // columns from a thread's piece to its next
+  __device__ __forceinline__ bool has(int k) const { return k * kStep < left; }
+  __device__ __forceinline__ int first() const { return base + (AL ? lane * V : lane); }
 
-  // `half` of E's elements of each piece (a residual stream of binary32 beside
-  // a 16-bit type takes two slots)
-  template <class E>
-  static __device__ __forceinline__ void fetch(uint32_t slot, const void* base, int64_t at, int half, int dim) {
-    const char* row = static_cast<const char*>(base) + at * (int64_t)sizeof(typename E::T);
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int c = column(k);
-      if (c < dim)
-        copy_async(slot + (uint32_t)((k * blockDim.x + threadIdx.x) * GRAIN),
-                   row + (int64_t)c * (int)sizeof(typename E::T) + half * GRAIN, GRAIN);
-    }
+  // Buffers are addressed by a row's offset in elements; the warp's (else) or
+  // the thread's (AL) first column of that row:
+  template <class E> __device__ __forceinline__ int64_t offset(int64_t elements) const {
+    return (elements + (AL ? first() : base)) * (int64_t)sizeof(typename E::T);
   }
 
-  // a slot's columns (of E; the half of each piece that it holds)
+  // Copies of E take sizeof(E) / sizeof(D) slots: `half` of each vector of
+  // columns (AL) or of the warp's columns (else).
+  template <class E> static __host__ __device__ constexpr int halves() { return (int)(sizeof(typename E::T) / sizeof(T)); }
+
+  // p: offset()'s place; lo, span: where the buffer begins and its bytes
   template <class E>
-  static __device__ __forceinline__ void read(uint32_t slot, int half, int dim, float (&x)[kEach]) {
-    constexpr int n = GRAIN / (int)sizeof(typename E::T);   // elements of a piece that one slot holds
+  __device__ __forceinline__ void fetch(uint32_t slot, const char* p, int half, const char* lo, int64_t span) const {
+    constexpr int es = (int)sizeof(typename E::T);
+    if constexpr (AL) {
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      float v[n];
-      const uint32_t at = slot + (uint32_t)((k * blockDim.x + threadIdx.x) * GRAIN);
-      if (GRAIN == 16) {
-        uint4 w;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at));
-        float u[E::kVec];
-        unpack<E>(w, u);
+      for (int k = 0; k < VPT; ++k)
+        if (has(k)) copy_async(slot + k * 512 + lane * 16, p + half * 16 + k * kStep * es);
+    } else {
+      constexpr int most = 32 * kEach / halves<E>();   // columns in a slot
+      p += half * most * es;
+      const int columns = min(most, dim - base - half * most);
+      if (columns <= 0) return;
+      const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+      const char* v0 = p - shift;
+      const int vectors = (shift + columns * es + 15) >> 4;
+      const bool whole = v0 >= lo && v0 + 16 * vectors <= lo + span;   // nothing outside the buffer is read
 #pragma unroll
-        for (int e = 0; e < n; ++e) v[e] = u[e];
-      } else {
-        uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at));
-        if (sizeof(typename E::T) == 4) {
-          v[0] = __uint_as_float(w);
+      for (int i = 0; i < (most * es / 16 + 1 + 31) / 32; ++i) {
+        const int v = lane + 32 * i;
+        if (v >= vectors) break;
+        if (whole || (v > 0 && v < vectors - 1)) {
+          copy_async(slot + v * 16, v0 + v * 16);
         } else {
-          v[0] = widen<E>((typename E::T)(w & 0xFFFFu));
-          v[n - 1] = widen<E>((typename E::T)(w >> 16));
+          for (int e = 0; e < 16 / es; ++e) {
+            const int c = (v * 16 - shift) / es + e;   // 16 and shift are multiples of the element's size
+            if (c < 0 || c >= columns) continue;
+            const typename E::T x = ld_g(reinterpret_cast<const typename E::T*>(p) + c);
+            if constexpr (es == 4)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + shift + c * es), "f"(x) : "memory");
+            else
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot + shift + c * es), "h"(x) : "memory");
+          }
         }
       }
-      const bool some = column(k) < dim;
-#pragma unroll
-      for (int e = 0; e < n; ++e) x[k * U + half * n + e] = some ? v[e] : 0.0f;
     }
   }
 
-  // straight from memory: weights and gates, which every row reads, and rows without the ring
+  // A slot's columns of E; p as in fetch.  Columns past the row come back as
+  // anything (AL: 0), see clear().
   template <class E>
-  static __device__ __forceinline__ void load_piece(const void* base, int64_t at, int k, int dim, float (&x)[U]) {
-    const typename E::T* row = static_cast<const typename E::T*>(base) + at;
-    const int c = column(k);
-    if (c >= dim) {
+  __device__ __forceinline__ void read(uint32_t slot, const char* p, int half, float2 (&x)[kPairs]) const {
+    constexpr int es = (int)sizeof(typename E::T), n = halves<E>();
+    if constexpr (AL) {
 #pragma unroll
-      for (int e = 0; e < U; ++e) x[e] = 0.0f;
-      return;
-    }
-    if constexpr (GRAIN == 16) {
-#pragma unroll
-      for (int q = 0; q < U / E::kVec; ++q)
-        unpack<E>(ld_plain(reinterpret_cast<const uint4*>(row + c) + q), x + q * E::kVec);
-    } else if constexpr (U == 2 && sizeof(typename E::T) == 2) {
-      const uint32_t w = ld_g(reinterpret_cast<const uint32_t*>(row + c));
-      x[0] = widen<E>((typename E::T)(w & 0xFFFFu));
-      x[1] = widen<E>((typename E::T)(w >> 16));
+      for (int k = 0; k < VPT; ++k) {
+        uint4 w;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(slot + k * 512 + lane * 16)
+                     : "memory");
+        unpack<E>(w, reinterpret_cast<float*>(&x[k * (V / 2)]) + half * (V / n));
+      }
     } else {
+      p += half * (32 * kEach / n) * es;
+      const uint32_t at = slot + (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) + lane * es;
+      float* to = reinterpret_cast<float*>(x) + half * (kEach / n);
 #pragma unroll
-      for (int e = 0; e < U; ++e) x[e] = widen<E>(ld_g(row + c + e));
+      for (int e = 0; e < kEach / n; ++e) {
+        if constexpr (es == 4) {
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(to[e]) : "r"(at + e * 32 * es) : "memory");
+        } else {
+          unsigned short w;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at + e * 32 * es) : "memory");
+          to[e] = widen<E>(w);
+        }
+      }
     }
-  }
-  // weights and gates are binary32 or of type D
-  static __device__ __forceinline__ void load_param(const void* base, int64_t at, bool f32, int k, int dim,
-                                                    float (&x)[U]) {
-    if (f32)
-      load_piece<DF32>(base, at, k, dim, x);
-    else
-      load_piece<D>(base, at, k, dim, x);
   }
 
-  template <class E>
-  static __device__ __forceinline__ void store_piece(void* base, int64_t at, int k, int dim, const float* x) {
-    typename E::T* row = static_cast<typename E::T*>(base) + at;
-    const int c = column(k);
-    if (c >= dim) return;
-    if constexpr (GRAIN == 16) {
+  // 0 in the columns past the row
+  __device__ __forceinline__ void clear(float2 (&x)[kPairs]) const {
+    if constexpr (!AL) {
+      float* f = reinterpret_cast<float*>(x);
 #pragma unroll
-      for (int q = 0; q < U / E::kVec; ++q)
-        st_stream(reinterpret_cast<uint4*>(row + c) + q, pack<E>(x + q * E::kVec));
-    } else if constexpr (U == 2 && sizeof(typename E::T) == 2) {
-      st_g(reinterpret_cast<uint32_t*>(row + c), pack2<E>(x[0], x[1]));
-    } else {
-#pragma unroll
-      for (int e = 0; e < U; ++e) st_g(row + c + e, narrow<E>(x[e]));
+      for (int e = 0; e < kEach; ++e) f[e] = has(e) ? f[e] : 0.0f;
     }
   }
-  template <class E>
-  static __device__ __forceinline__ void store(void* base, int64_t at, int dim, const float (&x)[kEach]) {
+
+  // Weights and gates, binary32 or of type D, which every row reads; 1 where there are none, 0 past the row.
+  template <class E> __device__ __forceinline__ void load_as(const void* from, int64_t elements, float2 (&x)[kPairs]) const {
+    const typename E::T* p = static_cast<const typename E::T*>(from) + elements + first();
+    float* f = reinterpret_cast<float*>(x);
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) store_piece<E>(base, at, k, dim, x + k * U);
+    for (int k = 0; k < kPieces; ++k) {
+      if constexpr (AL) {
+        if (has(k)) {
+#pragma unroll
+          for (int q = 0; q < V / E::kVec; ++q)
+            unpack<E>(ld_plain(reinterpret_cast<const uint4*>(p + k * kStep) + q), f + k * V + q * E::kVec);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[k * V + e] = 0.0f;
+        }
+      } else {
+        f[k] = has(k) ? widen<E>(ld_g(p + k * kStep)) : 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void param(const void* from, int64_t elements, bool f32, float2 (&x)[kPairs]) const {
+    if (!from) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) x[i] = splat(1.0f);
+    } else if (f32) {
+      load_as<DF32>(from, elements, x);
+    } else {
+      load_as<D>(from, elements, x);
+    }
+  }
+
+  template <class E> __device__ __forceinline__ void store(void* to, int64_t elements, const float2 (&x)[kPairs]) const {
+    typename E::T* p = static_cast<typename E::T*>(to) + elements + first();
+    const float* f = reinterpret_cast<const float*>(x);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      if (!has(k)) continue;
+      if constexpr (AL) {
+#pragma unroll
+        for (int q = 0; q < V / E::kVec; ++q)
+          st_stream(reinterpret_cast<uint4*>(p + k * kStep) + q, pack<E>(f + k * V + q * E::kVec));
+      } else {
+        st_g(p + k * kStep, narrow<E>(f[k]));
+      }
+    }
   }
 };
 
 extern __shared__ uint4 g_ring[];
 
-// The ring of one thread: its slots' addresses, the next slot to fill and to
-// read.  Every step commits one group of copies, so kDepth - 1 of them are in
-// flight; the slot that is filled is the one read in the step before.
+// The ring of one warp: the next slot to fill and to read.  Every step
+// commits one group of copies, so kDepth - 1 of them are in flight; the slot
+// that is filled is the one read in the step before.
 template <class C> struct Ring {
-  uint32_t base;
-  int fill, take;
-  __device__ __forceinline__ Ring() {
-    // a CTA's slots one after another, the rows of a CTA of narrow rows apart
-    base = smem_addr(g_ring) + threadIdx.y * (uint32_t)(C::kDepth * C::kSlotBytes) * blockDim.x;
-    fill = take = 0;
-  }
-  __device__ __forceinline__ uint32_t slot(int i) const {
-    return base + (uint32_t)i * (uint32_t)C::kSlotBytes * blockDim.x;
+  uint32_t base, fill, take, bytes, end;
+  __device__ __forceinline__ explicit Ring(const C& cols) {
+    // a CTA's slots one after another; the rows of a CTA of narrow rows apart
+    bytes = (uint32_t)C::kWarpBytes * (blockDim.x >> 5);
+    base = smem_addr(g_ring) + threadIdx.y * (uint32_t)C::kDepth * bytes + (threadIdx.x >> 5) * (uint32_t)C::kWarpBytes;
+    end = base + (uint32_t)C::kDepth * bytes;
+    fill = take = base;
+    // vectors past the row are never copied: 0 for good
+    for (uint32_t at = base + cols.lane * 16; at < end; at += bytes)
+      for (uint32_t k = 0; k + cols.lane * 16 < C::kWarpBytes; k += 512)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + k), "r"(0) : "memory");
+    __syncwarp();
   }
   // Rows: what the kernel reads, in its order; next(slot) starts the next copy
   template <class Rows> __device__ __forceinline__ void start(Rows& rows) {
-    if (C::kRing)
-      for (int i = 0; i < C::kDepth - 1; ++i) refill(rows);
+    for (int i = 0; i < C::kDepth - 1; ++i) refill(rows);
   }
   template <class Rows> __device__ __forceinline__ void refill(Rows& rows) {
-    rows.next(slot(fill));
+    rows.next(fill);
     copy_commit();
-    fill = fill + 1 == C::kDepth ? 0 : fill + 1;
+    fill += bytes;
+    if (fill == end) fill = base;
   }
-  // the oldest copy, complete
+  // the oldest copy, complete, for the whole warp; and the slot read before it is free
   __device__ __forceinline__ uint32_t oldest() {
     copy_wait<C::kDepth - 2>();
-    const uint32_t at = slot(take);
-    take = take + 1 == C::kDepth ? 0 : take + 1;
+    __syncwarp();
+    const uint32_t at = take;
+    take += bytes;
+    if (take == end) take = base;
     return at;
   }
 };
 
-// One tensor's columns of the current row, next in the ring's order (or
-// straight from memory).
-template <class C, class E, class D, class Rows>
-__device__ __forceinline__ void take(Ring<C>& ring, Rows& rows, const void* base, int64_t at, int dim,
-                                     float (&x)[C::kEach]) {
-  if constexpr (C::kRing) {
-    constexpr int halves = (int)(sizeof(typename E::T) / sizeof(typename D::T));
+// One tensor's columns of the current row, next in the ring's order; p:
+// offset()'s place.
+template <class E, class C, class Rows>
+__device__ __forceinline__ void take(const C& cols, Ring<C>& ring, Rows& rows, const char* p,
+                                     float2 (&x)[C::kPairs]) {
 #pragma unroll
-    for (int half = 0; half < halves; ++half) {
-      C::template read<E>(ring.oldest(), half, dim, x);
-      ring.refill(rows);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < C::kPieces; ++k) {
-      float v[C::U];
-      C::template load_piece<E>(base, at, k, dim, v);
-#pragma unroll
-      for (int e = 0; e < C::U; ++e) x[k * C::U + e] = v[e];
-    }
+  for (int half = 0; half < C::template halves<E>(); ++half) {
+    cols.template read<E>(ring.oldest(), p, half, x);
+    ring.refill(rows);
   }
 }
 
-template <class C, class D, class Rows>
-__device__ __forceinline__ void take_sum(Ring<C>& ring, Rows& rows, const void* const* in, int count, int64_t at,
-                                         int dim, float (&acc)[C::kEach]) {
-  take<C, D, D>(ring, rows, in[0], at, dim, acc);
-#pragma unroll 4
+template <class D, class C, class Rows>
+__device__ __forceinline__ void take_sum(const C& cols, Ring<C>& ring, Rows& rows, const void* const* in, int count,
+                                         int64_t elements, float2 (&acc)[C::kPairs]) {
+  const int64_t at = cols.template offset<D>(elements);
+  take<D>(cols, ring, rows, static_cast<const char*>(in[0]) + at, acc);
+#pragma unroll 2
   for (int r = 1; r < count; ++r) {
-    float x[C::kEach];
-    take<C, D, D>(ring, rows, in[r], at, dim, x);
+    float2 x[C::kPairs];
+    take<D>(cols, ring, rows, static_cast<const char*>(in[r]) + at, x);
 #pragma unroll
-    for (int e = 0; e < C::kEach; ++e) acc[e] = __fadd_rn(acc[e], x[e]);
+    for (int i = 0; i < C::kPairs; ++i) acc[i] = add2(acc[i], x[i]);
   }
+  cols.clear(acc);
+}
+
+// One buffer of rows that the ring reads: the warp's (or thread's) place in
+// the next row, and what bounds its reads.
+struct Source {
+  int64_t at, span;
+};
+template <class E, class C>
+__device__ __forceinline__ Source source(const C& cols, int64_t row, int64_t stride, int64_t rows) {
+  return {cols.template offset<E>(row * stride), ((rows - 1) * stride + cols.dim) * (int64_t)sizeof(typename E::T)};
 }
 
 // What forward reads: every row's R partials, then its residual.
 template <class C, class D, class RD> struct ForwardRows {
+  static constexpr int kHalves = C::template halves<RD>();
   const NormForward& a;
-  int64_t row, step;
+  const C& cols;
+  int64_t left;                 // rows from the next one on
+  int64_t step;
+  Source in, residual;
   int item;
-  __device__ __forceinline__ ForwardRows(const NormForward& args, int64_t first, int64_t by)
-      : a(args), row(first), step(by), item(0) {}
+  __device__ __forceinline__ ForwardRows(const NormForward& args, const C& c, int64_t first, int64_t every)
+      : a(args), cols(c), left(args.rows - first), step(every), item(0) {
+    in = source<D>(c, first, a.in_stride, a.rows);
+    residual = source<RD>(c, first, a.residual_stride, a.rows);
+  }
   __device__ __forceinline__ void next(uint32_t slot) {
-    constexpr int halves = (int)(sizeof(typename RD::T) / sizeof(typename D::T));
-    if (row >= a.rows) return;
-    if (item < a.R)
-      C::template fetch<D>(slot, a.in[item], row * a.in_stride, 0, a.dim);
-    else
-      C::template fetch<RD>(slot, a.residual, row * a.residual_stride, item - a.R, a.dim);
-    if (++item == a.R + halves) {
+    if (left <= 0) return;
+    if (item < a.R) {
+      const char* lo = static_cast<const char*>(a.in[item]);
+      cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
+      ++item;
+      return;
+    }
+    const char* lo = static_cast<const char*>(a.residual);
+    cols.template fetch<RD>(slot, lo + residual.at, item - a.R, lo, residual.span);
+    if (++item == a.R + kHalves) {
       item = 0;
-      row += step;
+      left -= step;
+      in.at += step * a.in_stride * (int64_t)sizeof(typename D::T);
+      residual.at += step * a.residual_stride * (int64_t)sizeof(typename RD::T);
     }
   }
 };
 
-template <class D, class RD, int VPT, int GRAIN, int MAXT>
+template <class D, class RD, int VPT, bool AL, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constant__ NormForward a) {
-  using C = Cols<D, VPT, GRAIN, MAXT>;
-  constexpr int U = C::U;
+  using C = Cols<D, VPT, AL, MAXT>;
+  constexpr int N = C::kPairs;
   __shared__ float red[2][32];
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, step = (int64_t)gridDim.x * blockDim.y;
-  ForwardRows<C, D, RD> rows(a, first, step);
-  Ring<C> ring;
+  const C cols(a.dim);
+  ForwardRows<C, D, RD> rows(a, cols, first, step);
+  Ring<C> ring(cols);
   ring.start(rows);
   for (int64_t row = first; row < a.rows; row += step) {
-    float s[C::kEach], h[C::kEach];
-    take_sum<C, D>(ring, rows, a.in, a.R, row * a.in_stride, a.dim, s);
-    if (a.total) C::template store<D>(a.total, row * a.total_stride, a.dim, s);
-    float r1 = 0.0f;
+    float2 s[N], h[N], w[N];
+    take_sum<D>(cols, ring, rows, a.in, a.R, row * a.in_stride, s);
+    if (a.total) cols.template store<D>(a.total, row * a.total_stride, s);
+    float r1 = 0.0f, f = 1.0f;
     if (a.post_weight) {
-      float sq = 0.0f;
+      float2 sq = splat(0.0f);
 #pragma unroll
-      for (int e = 0; e < C::kEach; ++e) sq = __fmaf_rn(s[e], s[e], sq);
-      r1 = rsqrtf(row_sum(sq, red, turn) * inv_dim + a.eps);
+      for (int i = 0; i < N; ++i) sq = fma2(s[i], s[i], sq);
+      f = r1 = rsqrtf(row_sum(sq.x + sq.y, red, turn) * inv_dim + a.eps);
+      cols.param(a.post_weight, 0, a.param_f32, w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = mul2(mul2(s[i], splat(f)), w[i]);
     }
-    take<C, RD, D>(ring, rows, a.residual, row * a.residual_stride, a.dim, h);
-    float sq = 0.0f;
+    if (a.gate) {
+      cols.param(a.gate, row / a.rows_per_gate * a.dim, a.param_f32, w);
 #pragma unroll
-    for (int k = 0; k < C::kPieces; ++k) {
-      if (a.post_weight) {
-        float w[U];
-        C::load_param(a.post_weight, 0, a.param_f32, k, a.dim, w);
-#pragma unroll
-        for (int e = 0; e < U; ++e) s[k * U + e] = s[k * U + e] * r1 * w[e];
-      }
-      if (a.gate) {
-        float g[U];
-        C::load_param(a.gate, row / a.rows_per_gate * a.dim, a.param_f32, k, a.dim, g);
-#pragma unroll
-        for (int e = 0; e < U; ++e) s[k * U + e] *= g[e];
-      }
-#pragma unroll
-      for (int e = 0; e < U; ++e) {
-        h[k * U + e] = __fmaf_rn(a.scale, s[k * U + e], h[k * U + e]);
-        sq = __fmaf_rn(h[k * U + e], h[k * U + e], sq);
-      }
+      for (int i = 0; i < N; ++i) s[i] = mul2(s[i], w[i]);
     }
-    C::template store<RD>(a.residual_out, row * a.residual_out_stride, a.dim, h);
-    const float r2 = rsqrtf(row_sum(sq, red, turn) * inv_dim + a.eps);
+    take<RD>(cols, ring, rows,
+             static_cast<const char*>(a.residual) + cols.template offset<RD>(row * a.residual_stride), h);
+    cols.clear(h);
+    float2 sq = splat(0.0f);
 #pragma unroll
-    for (int k = 0; k < C::kPieces; ++k) {
-      float w[U];
-      C::load_param(a.weight, 0, a.param_f32, k, a.dim, w);
-#pragma unroll
-      for (int e = 0; e < U; ++e) h[k * U + e] = h[k * U + e] * r2 * w[e];
+    for (int i = 0; i < N; ++i) {
+      h[i] = fma2(splat(a.scale), s[i], h[i]);
+      sq = fma2(h[i], h[i], sq);
     }
-    for (int q = 0; q < a.outs; ++q) C::template store<D>(a.out[q], row * a.out_stride, a.dim, h);
+    cols.template store<RD>(a.residual_out, row * a.residual_out_stride, h);
+    const float r2 = rsqrtf(row_sum(sq.x + sq.y, red, turn) * inv_dim + a.eps);
+    cols.param(a.weight, 0, a.param_f32, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = mul2(mul2(h[i], splat(r2)), w[i]);
+    for (int q = 0; q < a.outs; ++q) cols.template store<D>(a.out[q], row * a.out_stride, h);
     if (a.rstd && threadIdx.x == 0) {
       st_g(a.rstd + row, r1);
       st_g(a.rstd + a.rows + row, r2);
@@ -353,125 +418,143 @@ struct Dealt {
 // What backward reads: every row's partial gradients, what forward's residual
 // was, the residual's gradient where there is one, and the sum where it is needed.
 template <class C, class D, class RD> struct BackwardRows {
+  static constexpr int kHalves = C::template halves<RD>();
   const NormBackward& a;
   const Deal& d;
-  Dealt at;
-  int item, items;
-  static constexpr int kHalves = (int)(sizeof(typename RD::T) / sizeof(typename D::T));
-  __device__ __forceinline__ BackwardRows(const NormBackward& args, const Deal& deal, int64_t worker)
-      : a(args), d(deal), item(0) {
-    at.u = worker;
-    at.open(a, d);
-    items = a.grads + kHalves + (a.grad_residual_out ? kHalves : 0) + (a.total ? 1 : 0);
+  const C& cols;
+  Dealt row;
+  Source in;
+  int item, residuals, items;
+  __device__ __forceinline__ BackwardRows(const NormBackward& args, const Deal& deal, const C& c, int64_t worker)
+      : a(args), d(deal), cols(c), item(0) {
+    row.u = worker;
+    open();
+    residuals = a.grads + kHalves * (a.grad_residual_out ? 2 : 1);
+    items = residuals + (a.total ? 1 : 0);
+  }
+  __device__ __forceinline__ void open() {
+    row.open(a, d);
+    in = source<D>(cols, row.row, a.grad_out_stride, a.rows);
   }
   __device__ __forceinline__ void next(uint32_t slot) {
-    if (at.u >= d.units) return;
-    int i = item;
-    if (i < a.grads) {
-      C::template fetch<D>(slot, a.grad_out[i], at.row * a.grad_out_stride, 0, a.dim);
-    } else if ((i -= a.grads) < kHalves) {
-      C::template fetch<RD>(slot, a.residual_out, at.row * a.residual_out_stride, i, a.dim);
-    } else if (a.grad_residual_out && (i -= kHalves) < kHalves) {
-      C::template fetch<RD>(slot, a.grad_residual_out, at.row * a.grad_residual_out_stride, i, a.dim);
+    if (row.u >= d.units) return;
+    if (item < a.grads) {
+      const char* lo = static_cast<const char*>(a.grad_out[item]);
+      cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
+    } else if (item < residuals) {
+      const bool grad = item - a.grads >= kHalves;
+      const char* lo = static_cast<const char*>(grad ? a.grad_residual_out : a.residual_out);
+      const Source s = source<RD>(cols, row.row, grad ? a.grad_residual_out_stride : a.residual_out_stride, a.rows);
+      cols.template fetch<RD>(slot, lo + s.at, (item - a.grads) % kHalves, lo, s.span);
     } else {
-      C::template fetch<D>(slot, a.total, at.row * a.total_stride, 0, a.dim);
+      const char* lo = static_cast<const char*>(a.total);
+      const Source s = source<D>(cols, row.row, a.total_stride, a.rows);
+      cols.template fetch<D>(slot, lo + s.at, 0, lo, s.span);
     }
-    if (++item == items) {
-      item = 0;
-      if (++at.row == at.hi) {
-        at.u += d.workers;
-        at.open(a, d);
-      }
+    if (++item < items) return;
+    item = 0;
+    in.at += a.grad_out_stride * (int64_t)sizeof(typename D::T);
+    if (++row.row == row.hi) {
+      row.u += d.workers;
+      open();
     }
   }
 };
 
-template <class D, class RD, int VPT, int GRAIN, int MAXT>
+template <class D, class RD, int VPT, bool AL, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_constant__ NormBackward a,
                                                              const __grid_constant__ Deal d) {
-  using C = Cols<D, VPT, GRAIN, MAXT>;
-  constexpr int U = C::U, N = C::kEach;
+  using C = Cols<D, VPT, AL, MAXT>;
+  constexpr int N = C::kPairs;
   __shared__ float red[2][32];
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
   const int64_t worker = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  BackwardRows<C, D, RD> rows(a, d, worker);
-  Ring<C> ring;
+  const C cols(a.dim);
+  BackwardRows<C, D, RD> rows(a, d, cols, worker);
+  Ring<C> ring(cols);
   ring.start(rows);
-  float dw[N], dp[N];
+  float2 dw[N], dp[N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) dw[e] = dp[e] = 0.0f;
+  for (int i = 0; i < N; ++i) dw[i] = dp[i] = splat(0.0f);
   Dealt at;
   for (at.u = worker; at.u < d.units; at.u += d.workers) {
     at.open(a, d);
     const int64_t group = at.u / d.parts;
-    float dg[N];
+    float2 dg[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) dg[e] = 0.0f;
+    for (int i = 0; i < N; ++i) dg[i] = splat(0.0f);
     for (int64_t row = at.row; row < at.hi; ++row) {
-      float z[N], x[N];
-      take_sum<C, D>(ring, rows, a.grad_out, a.grads, row * a.grad_out_stride, a.dim, z);
-      take<C, RD, D>(ring, rows, a.residual_out, row * a.residual_out_stride, a.dim, x);
+      float2 z[N], x[N], w[N];
+      take_sum<D>(cols, ring, rows, a.grad_out, a.grads, row * a.grad_out_stride, z);
+      take<RD>(cols, ring, rows,
+               static_cast<const char*>(a.residual_out) + cols.template offset<RD>(row * a.residual_out_stride), x);
+      cols.clear(x);
       const float r2 = ld_g(a.rstd + a.rows + row);
       const float r1 = a.post_weight ? ld_g(a.rstd + row) : 1.0f;
-      float c = 0.0f;
+      cols.param(a.weight, 0, a.param_f32, w);
+      float2 c = splat(0.0f);
 #pragma unroll
-      for (int k = 0; k < C::kPieces; ++k) {
-        float w[U];
-        C::load_param(a.weight, 0, a.param_f32, k, a.dim, w);
-#pragma unroll
-        for (int e = 0; e < U; ++e) {
-          const int i = k * U + e;
-          x[i] *= r2;                                   // x2
-          dw[i] = __fmaf_rn(z[i], x[i], dw[i]);
-          z[i] *= w[e];
-          c = __fmaf_rn(z[i], x[i], c);
-        }
+      for (int i = 0; i < N; ++i) {
+        x[i] = mul2(x[i], splat(r2));         // x2
+        dw[i] = fma2(z[i], x[i], dw[i]);
+        z[i] = mul2(z[i], w[i]);
+        c = fma2(z[i], x[i], c);
       }
-      const float c2 = row_sum(c, red, turn) * inv_dim;
-#pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = r2 * __fmaf_rn(-c2, x[i], z[i]);
+      const float c2 = row_sum(c.x + c.y, red, turn) * inv_dim;
       if (a.grad_residual_out) {
-        float t[N];
-        take<C, RD, D>(ring, rows, a.grad_residual_out, row * a.grad_residual_out_stride, a.dim, t);
+        take<RD>(cols, ring, rows,
+                 static_cast<const char*>(a.grad_residual_out) +
+                     cols.template offset<RD>(row * a.grad_residual_out_stride), w);
+        cols.clear(w);
+      } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] += t[i];       // e
+        for (int i = 0; i < N; ++i) w[i] = splat(0.0f);
       }
-      C::template store<RD>(a.grad_residual, row * a.grad_residual_stride, a.dim, z);
-      if (a.total) take<C, D, D>(ring, rows, a.total, row * a.total_stride, a.dim, x);
-      c = 0.0f;
 #pragma unroll
-      for (int k = 0; k < C::kPieces; ++k) {
-        float w[U], g[U];
-        if (a.post_weight) C::load_param(a.post_weight, 0, a.param_f32, k, a.dim, w);
-        if (a.gate) C::load_param(a.gate, group * a.dim, a.param_f32, k, a.dim, g);
+      for (int i = 0; i < N; ++i) z[i] = fma2(splat(r2), fma2(splat(-c2), x[i], z[i]), w[i]);   // e
+      cols.template store<RD>(a.grad_residual, row * a.grad_residual_stride, z);
+      if (a.total) {
+        take<D>(cols, ring, rows, static_cast<const char*>(a.total) + cols.template offset<D>(row * a.total_stride), x);
+        cols.clear(x);
+      }
+      cols.param(a.post_weight, 0, a.param_f32, w);
+      // without a post norm w and r1 are 1: dp then counts for nothing, and c1 is 0
 #pragma unroll
-        for (int e = 0; e < U; ++e) {
-          const int i = k * U + e;
-          x[i] *= r1;                                   // x1 (S without a post norm)
-          z[i] *= a.scale;
-          if (a.grad_gate) dg[i] = __fmaf_rn(a.post_weight ? x[i] * w[e] : x[i], z[i], dg[i]);
-          if (a.gate) z[i] *= g[e];                     // the gradient of y
-          if (a.post_weight) {
-            dp[i] = __fmaf_rn(z[i], x[i], dp[i]);
-            z[i] *= w[e];
-            c = __fmaf_rn(z[i], x[i], c);
-          }
-        }
+      for (int i = 0; i < N; ++i) {
+        x[i] = mul2(x[i], splat(r1));         // x1
+        dg[i] = fma2(mul2(x[i], w[i]), z[i], dg[i]);
+      }
+      if (a.gate) {
+        float2 g[N];
+        cols.param(a.gate, group * a.dim, a.param_f32, g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = mul2(z[i], g[i]);
+      }
+      c = splat(0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        z[i] = mul2(z[i], splat(a.scale));    // the gradient of y
+        dp[i] = fma2(z[i], x[i], dp[i]);
+        z[i] = mul2(z[i], w[i]);
+        c = fma2(z[i], x[i], c);
       }
       if (a.post_weight) {
-        const float c1 = row_sum(c, red, turn) * inv_dim;
+        const float c1 = row_sum(c.x + c.y, red, turn) * inv_dim;
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = r1 * __fmaf_rn(-c1, x[i], z[i]);
+        for (int i = 0; i < N; ++i) z[i] = mul2(splat(r1), fma2(splat(-c1), x[i], z[i]));
       }
-      for (int q = 0; q < a.outs; ++q) C::template store<D>(a.grad_in[q], row * a.grad_in_stride, a.dim, z);
+      for (int q = 0; q < a.outs; ++q) cols.template store<D>(a.grad_in[q], row * a.grad_in_stride, z);
     }
     // one unit per gate row: its gradient is whole; else a partial per unit
-    if (a.grad_gate)
-      C::template store<DF32>(d.parts == 1 ? a.grad_gate : a.work + 2 * d.workers * a.dim, at.u * a.dim, a.dim, dg);
+    if (a.grad_gate) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) dg[i] = mul2(dg[i], splat(a.scale));
+      cols.template store<DF32>(d.parts == 1 ? a.grad_gate : a.work + 2 * d.workers * a.dim, at.u * a.dim, dg);
+    }
   }
-  if (a.grad_weight) C::template store<DF32>(a.work, worker * a.dim, a.dim, dw);
-  if (a.grad_post_weight) C::template store<DF32>(a.work, (d.workers + worker) * a.dim, a.dim, dp);
+  if (a.grad_weight) cols.template store<DF32>(a.work, worker * a.dim, dw);
+  if (a.grad_post_weight) cols.template store<DF32>(a.work, (d.workers + worker) * a.dim, dp);
 }
 
 // How a row of `dim` columns is spread: threads, 16-byte vectors per thread,
@@ -512,16 +595,6 @@ inline int64_t most_ctas(const Shape& s, int sms) {
   return (int64_t)sms * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm);
 }
 
-// f(IntC<GRAIN>) for what every row is aligned to.
-template <class D, class F> cudaError_t with_grain(int grain, F&& f) {
-  if (grain == 16) return f(IntC<16>{});
-  if (grain == 4) return f(IntC<4>{});
-  if constexpr (sizeof(typename D::T) == 2) {
-    if (grain == 2) return f(IntC<2>{});
-  }
-  return cudaErrorInvalidValue;
-}
-
 // f(IntC<groups per thread>)
 template <class D, class F> cudaError_t with_groups(int groups, F&& f) {
   if (groups == 1) return f(IntC<1>{});
@@ -534,49 +607,52 @@ template <class D, class F> cudaError_t with_groups(int groups, F&& f) {
 
 // The ring's shared memory, opted in to.
 template <class C, class K> cudaError_t ring_bytes(K kernel, const Shape& s, size_t* bytes) {
-  *bytes = C::kRing ? (size_t)C::kDepth * C::kSlotBytes * s.threads * s.rows : 0;
+  *bytes = (size_t)C::kDepth * C::kWarpBytes * (s.threads / 32) * s.rows;
   if (*bytes <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
 }
 
 template <class D, class RD>
-cudaError_t run_forward(const Shape& s, int grain, const NormForward& a, unsigned grid, cudaStream_t st) {
+cudaError_t run_forward(const Shape& s, bool aligned, const NormForward& a, unsigned grid, cudaStream_t st) {
   cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
   return with_groups<D>(s.groups, [&](auto g) {
-    return with_grain<D>(grain, [&](auto al) {
-      constexpr int kGroups = decltype(g)::value, kGrain = decltype(al)::value;
-      auto kernel = norm_forward_kernel<D, RD, kGroups, kGrain, 1024>;
+    constexpr int kGroups = decltype(g)::value;
+    auto launch = [&](auto kernel, auto al) {
       size_t smem;
-      const cudaError_t e2 = ring_bytes<Cols<D, kGroups, kGrain, 1024>>(kernel, s, &smem);
+      const cudaError_t e2 = ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, 1024>>(kernel, s, &smem);
       if (e2 != cudaSuccess) return e2;
       kernel<<<grid, dim3(s.threads, s.rows), smem, st>>>(a);
       return cudaGetLastError();
-    });
+    };
+    if (aligned) return launch(norm_forward_kernel<D, RD, kGroups, true, 1024>, IntC<1>{});
+    return launch(norm_forward_kernel<D, RD, kGroups, false, 1024>, IntC<0>{});
   });
 }
 
 template <class D, class RD>
-cudaError_t run_backward(const Shape& s, int grain, const NormBackward& a, const Deal& d, unsigned grid,
+cudaError_t run_backward(const Shape& s, bool aligned, const NormBackward& a, const Deal& d, unsigned grid,
                          cudaStream_t st) {
   cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
   return with_groups<D>(s.groups, [&](auto g) {
-    return with_grain<D>(grain, [&](auto al) {
-      constexpr int kGroups = decltype(g)::value, kGrain = decltype(al)::value;
-      auto launch = [&](auto kernel, auto cols) {
-        size_t smem;
-        const cudaError_t e2 = ring_bytes<decltype(cols)>(kernel, s, &smem);
-        if (e2 != cudaSuccess) return e2;
-        kernel<<<grid, dim3(s.threads, s.rows), smem, st>>>(a, d);
-        return cudaGetLastError();
-      };
-      if constexpr (kGroups * D::kVec == 16) {
-        if (s.most == 1024)
-          return launch(norm_backward_kernel<D, RD, kGroups, kGrain, 1024>, Cols<D, kGroups, kGrain, 1024>{});
+    constexpr int kGroups = decltype(g)::value;
+    auto launch = [&](auto kernel, auto al, auto most) {
+      size_t smem;
+      const cudaError_t e2 =
+          ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, decltype(most)::value>>(kernel, s, &smem);
+      if (e2 != cudaSuccess) return e2;
+      kernel<<<grid, dim3(s.threads, s.rows), smem, st>>>(a, d);
+      return cudaGetLastError();
+    };
+    if constexpr (kGroups * D::kVec == 16) {
+      if (s.most == 1024) {
+        if (aligned) return launch(norm_backward_kernel<D, RD, kGroups, true, 1024>, IntC<1>{}, IntC<1024>{});
+        return launch(norm_backward_kernel<D, RD, kGroups, false, 1024>, IntC<0>{}, IntC<1024>{});
       }
-      return launch(norm_backward_kernel<D, RD, kGroups, kGrain, 512>, Cols<D, kGroups, kGrain, 512>{});
-    });
+    }
+    if (aligned) return launch(norm_backward_kernel<D, RD, kGroups, true, 512>, IntC<1>{}, IntC<512>{});
+    return launch(norm_backward_kernel<D, RD, kGroups, false, 512>, IntC<0>{}, IntC<512>{});
   });
 }
 

@@ -5,8 +5,8 @@
 namespace ra {
 namespace norm {
 
-template cudaError_t run_forward<RA_INST_D, RA_INST_RD>(const Shape&, int, const NormForward&, unsigned, cudaStream_t);
-template cudaError_t run_backward<RA_INST_D, RA_INST_RD>(const Shape&, int, const NormBackward&, const Deal&, unsigned,
+template cudaError_t run_forward<RA_INST_D, RA_INST_RD>(const Shape&, bool, const NormForward&, unsigned, cudaStream_t);
+template cudaError_t run_backward<RA_INST_D, RA_INST_RD>(const Shape&, bool, const NormBackward&, const Deal&, unsigned,
                                                          cudaStream_t);
 
 }  // namespace norm

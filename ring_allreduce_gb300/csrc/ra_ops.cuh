@@ -26,18 +26,30 @@ template <> __device__ __forceinline__ uint16_t narrow<DF16>(float v) {
   return __half_as_ushort(__float2half_rn(v));
 }
 
+// Two 16-bit elements of a word as binary32.
+template <class D> __device__ __forceinline__ void unpack2(uint32_t w, float* x);
+template <> __device__ __forceinline__ void unpack2<DBF16>(uint32_t w, float* x) {
+  x[0] = __uint_as_float(w << 16);
+  x[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+template <> __device__ __forceinline__ void unpack2<DF16>(uint32_t w, float* x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x[0] = f.x;
+  x[1] = f.y;
+}
+
 // The elements of one 16-byte vector as binary32, and back.
 template <class D> __device__ __forceinline__ void unpack(uint4 v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if (sizeof(typename D::T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+  if constexpr (sizeof(typename D::T) == 4) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = widen<D>((typename D::T)(w[i] & 0xFFFFu));
-      x[2 * i + 1] = widen<D>((typename D::T)(w[i] >> 16));
-    }
+    unpack2<D>(v.x, x);
+    unpack2<D>(v.y, x + 2);
+    unpack2<D>(v.z, x + 4);
+    unpack2<D>(v.w, x + 6);
   }
 }
 

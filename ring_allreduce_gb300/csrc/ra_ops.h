@@ -58,11 +58,10 @@ struct NormBackward {
   float scale;
 };
 
-// grain: the bytes that every row of every buffer starts on a multiple of and
-// holds whole multiples of: 16, 4 or 2
-cudaError_t launch_norm_forward(int dtype, int residual_dtype, int grain, const NormForward& a, int sms,
+// aligned: every row of every buffer starts on a 16-byte boundary and holds whole 16-byte vectors
+cudaError_t launch_norm_forward(int dtype, int residual_dtype, bool aligned, const NormForward& a, int sms,
                                 cudaStream_t st);
-cudaError_t launch_norm_backward(int dtype, int residual_dtype, int grain, const NormBackward& a, int sms,
+cudaError_t launch_norm_backward(int dtype, int residual_dtype, bool aligned, const NormBackward& a, int sms,
                                  cudaStream_t st);
 // Floats of column partials a backward call of this width may use.
 size_t norm_workspace_floats(int dim, int sms);

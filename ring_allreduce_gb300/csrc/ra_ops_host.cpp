@@ -147,12 +147,12 @@ class Buffers {
     return RA_OK;
   }
 
-  // The largest of 16, 4 and 2 bytes that every row of every buffer so far
-  // starts on a multiple of and that rows of `row_bytes` are whole multiples of.
-  int grain(size_t row_bytes) const {
+  // Every row of every buffer so far starts on a 16-byte boundary, and rows
+  // of `row_bytes` hold whole 16-byte vectors.
+  bool aligned(size_t row_bytes) const {
     uintptr_t bits = row_bytes;
     for (int i = 0; i < count_; ++i) bits |= b_[i].lo | (b_[i].span > b_[i].width ? b_[i].stride : 0);
-    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    return bits % 16 == 0;
   }
 
  private:
@@ -291,7 +291,7 @@ static ra_status norm_forward(ra_norm_handle h, const ra_norm_forward_args* g, c
   }
   RA_TRY(buf.add("residual_out", -1, g->residual_out, rb, dim, &res_out_stride, true, g->residual));
   if (g->total) RA_TRY(buf.add("total", -1, g->total, b, dim, &total_stride, true));
-  const int grain = buf.grain(dim * b);
+  const bool aligned = buf.aligned(dim * b);
   if (g->rstd) RA_TRY(buf.flat("rstd", g->rstd, 4, 2 * g->rows, true));
   RA_TRY(buf.check());
   a.residual = g->residual;
@@ -314,7 +314,7 @@ static ra_status norm_forward(ra_norm_handle h, const ra_norm_forward_args* g, c
   a.param_f32 = h->param_dtype == RA_F32;
   a.eps = h->eps;
   a.scale = h->scale;
-  const cudaError_t e = ra::launch_norm_forward(h->dtype, h->residual_dtype, grain, a, h->sms, st);
+  const cudaError_t e = ra::launch_norm_forward(h->dtype, h->residual_dtype, aligned, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "norm forward launch");
 }
 
@@ -358,7 +358,7 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
   }
   RA_TRY(buf.add("grad_residual", -1, g->grad_residual, rb, dim, &gr_stride, true, g->grad_residual_out));
   if (g->grad_gate) RA_TRY(buf.add("grad_gate", -1, g->grad_gate, 4, dim, &gg_stride, true, g->gate_rows));
-  const int grain = buf.grain(dim * b);
+  const bool aligned = buf.aligned(dim * b);
   if (g->grad_weight) RA_TRY(buf.flat("grad_weight", g->grad_weight, 4, dim, true));
   if (g->grad_post_weight) RA_TRY(buf.flat("grad_post_weight", g->grad_post_weight, 4, dim, true));
   RA_TRY(buf.flat("rstd", g->rstd, 4, 2 * g->rows, false));
@@ -403,7 +403,7 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
   a.dim = h->dim;
   a.param_f32 = h->param_dtype == RA_F32;
   a.scale = h->scale;
-  const cudaError_t e = ra::launch_norm_backward(h->dtype, h->residual_dtype, grain, a, h->sms, st);
+  const cudaError_t e = ra::launch_norm_backward(h->dtype, h->residual_dtype, aligned, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "norm backward launch");
 }
 
