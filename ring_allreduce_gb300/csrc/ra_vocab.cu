@@ -9,10 +9,11 @@
 //                      loss = tau^2 sum_k q_k (log q_k - log p_{id_k})
 //     gradient         dL_j = g tau (p_j - sum_{k: id_k = j} q_k)
 //
-// The forward pass reads the row once: every thread keeps its own running
-// maximum m, sum s = sum e^{x-m} and u = sum (x-m) e^{x-m}, which are joined
-// over the block; H = log s - u / s is then a sum of two terms that are never
-// negative, with no cancellation.  All statistics are binary32.
+// The forward pass reads the row once.  With t = x log2(e) - ref, every thread
+// keeps s = sum 2^t and u = sum t 2^t; ref is at most kLag below the largest x
+// log2(e) that the thread saw, and s and u are moved when it is passed by more
+// (rare after the first vectors), so 2^t never leaves its range.  Then lse =
+// ln2 (ref + log2 s) and H = ln2 (log2 s - u / s).  All statistics are binary32.
 //
 // The top K come out of the same pass without a comparison per element
 // against a list: each thread also keeps the largest logit it saw and where.
@@ -20,9 +21,15 @@
 // below, and only the K threads whose maximum reaches it can hold one of the
 // top K: their columns, K / threads of the row, are read again.
 //
-// A row's 16-byte slots are numbered through all shards; a slot that a
-// shard's first or last columns share with other memory is read element by
+// A row's shards are cut into 16-byte slots, and these into chunks of 128, a
+// lane's four 512 bytes apart; a warp takes every warps-th chunk.  A slot that
+// a shard's first or last columns share with other memory is read element by
 // element, so rows may start on any element.
+//
+// What bounds it: 16-bit logits arrive at 12 a clock and SM at the copy
+// bandwidth, so that at three instructions a clock and scheduler quartet each
+// may take eight: arithmetic on pairs, a maximum on packed halves, and no
+// index arithmetic within a chunk.
 #include "ra_ops.cuh"
 
 namespace ra {
@@ -30,15 +37,45 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kFarBelow = -200.0f;   // exponents are held above this: 2^-200 is 0 in binary32,
-                                       // and 0 times the exponent then stays 0 (not 0 * inf)
+constexpr float kFarBelow = -200.0f;   // 2^-200 is 0 in binary32: exponents that are multiplied with their power
+                                       // are held above this, so that it stays 0 (not 0 * inf)
+constexpr float kLag = 4.0f;
+constexpr float kNoRef = -8.5e37f;     // ref before the first finite logit
 
 constexpr float kNothingLeft = -1e30f;
 
 template <class D> struct NegInf;
-template <> struct NegInf<DF32> { static constexpr uint32_t bits = 0xFF800000u; };
-template <> struct NegInf<DBF16> { static constexpr uint32_t bits = 0xFF80u; };
-template <> struct NegInf<DF16> { static constexpr uint32_t bits = 0xFC00u; };
+template <> struct NegInf<DF32> { static constexpr uint32_t word = 0xFF800000u, one = 0xFF800000u; };
+template <> struct NegInf<DBF16> { static constexpr uint32_t word = 0xFF80FF80u, one = 0xFF80u; };
+template <> struct NegInf<DF16> { static constexpr uint32_t word = 0xFC00FC00u, one = 0xFC00u; };
+
+// The largest of a slot's logits, NaN if there is one.
+template <class D> __device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t word_max<DF32>(uint32_t a, uint32_t b) {
+  return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+}
+template <> __device__ __forceinline__ uint32_t word_max<DBF16>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <> __device__ __forceinline__ uint32_t word_max<DF16>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <class D> __device__ __forceinline__ uint32_t vector_max(uint4 v) {
+  return word_max<D>(word_max<D>(v.x, v.y), word_max<D>(v.z, v.w));
+}
+template <class D> __device__ __forceinline__ float word_value(uint32_t w) {
+  if constexpr (sizeof(typename D::T) == 4) {
+    return __uint_as_float(w);
+  } else {
+    float x[2];
+    unpack2<D>(w, x);
+    return max_nan(x[0], x[1]);
+  }
+}
 
 // A logit as a whole number of the same order: -0 as +0, NaN above all.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -53,8 +90,7 @@ __device__ __forceinline__ uint64_t top_key(float x, uint32_t column) {
   return ((uint64_t)ordered(x) << 32) | (uint32_t)~column;
 }
 
-// One row's shards, in shared memory: first byte, columns and the element
-// offset of the first byte within its 16-byte slot.
+// One row's shards, in shared memory: the first byte, and the columns.
 struct RowShards {
   uintptr_t first[kMaxRanks];
   int len[kMaxRanks];
@@ -68,22 +104,25 @@ __device__ __forceinline__ void load_row(const VocabRows& x, int64_t row, RowSha
   }
 }
 
-// Slots per shard: the most that C columns can touch.
-template <class D> __host__ __device__ __forceinline__ int slots_per_shard(int C) {
-  return (int)(((int64_t)C * (int64_t)sizeof(typename D::T) + 15) / 16) + 1;
+constexpr int kChunk = 128;                  // slots
+constexpr int kPerLane = kChunk / 32;
+
+// Chunks per shard: what C columns can touch at most.
+template <class D> __host__ __device__ __forceinline__ int chunks_per_shard(int C) {
+  const int64_t slots = ((int64_t)C * (int64_t)sizeof(typename D::T) + 15) / 16 + 1;
+  return (int)((slots + kChunk - 1) / kChunk);
 }
 
-// Where slot g of a row lies: shard r, slot j of it; [lo, hi) are the slot's
-// elements that belong to the shard, e0 the shard's column of its element 0.
+// Where slot j of a shard lies: [lo, hi) are the slot's elements that belong
+// to the shard, e0 the shard's column of its element 0.
 template <class D> struct Slot {
   const uint4* at;
-  int r, lo, hi, e0;
-  __device__ __forceinline__ Slot(const RowShards& s, int rr, int j) : r(rr) {
-    const uintptr_t a = s.first[rr];
-    at = reinterpret_cast<const uint4*>(a & ~uintptr_t(15)) + j;
-    e0 = j * D::kVec - (int)((a & 15u) / sizeof(typename D::T));
+  int lo, hi, e0;
+  __device__ __forceinline__ Slot(uintptr_t first, int len, int j) {
+    at = reinterpret_cast<const uint4*>(first & ~uintptr_t(15)) + j;
+    e0 = j * D::kVec - (int)((first & 15u) / sizeof(typename D::T));
     lo = max(0, -e0);
-    hi = min(D::kVec, s.len[rr] - e0);
+    hi = min(D::kVec, len - e0);
   }
   __device__ __forceinline__ bool empty() const { return hi <= lo; }
   __device__ __forceinline__ bool whole() const { return lo == 0 && hi == D::kVec; }
@@ -92,7 +131,7 @@ template <class D> struct Slot {
     if (whole()) return ld_stream(at);
     uint32_t w[4];
     const typename D::T* p = reinterpret_cast<const typename D::T*>(at);
-    constexpr uint32_t none = NegInf<D>::bits;
+    constexpr uint32_t none = NegInf<D>::one;
     if constexpr (sizeof(typename D::T) == 4) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = i >= lo && i < hi ? __float_as_uint(ld_stream_scalar(p + i)) : none;
@@ -108,6 +147,67 @@ template <class D> struct Slot {
   }
 };
 
+// A warp's walk over the chunks q, q + step, ... below `end` of a row, chunk q
+// being chunk k of shard r.  The same in every lane.
+template <class D> struct Walk {
+  const RowShards& s;
+  int per, q, end, step;
+  int r, k;
+  uintptr_t first;
+  int len;
+  __device__ __forceinline__ Walk(const RowShards& rows, int chunks, int begin, int last, int by)
+      : s(rows), per(chunks), q(begin), end(last), step(by) {
+    r = q / per;
+    k = q - r * per;
+    open();
+  }
+  __device__ __forceinline__ void open() {
+    if (q < end) {
+      first = s.first[r];
+      len = s.len[r];
+    }
+  }
+  __device__ __forceinline__ bool more() const { return q < end; }
+  __device__ __forceinline__ void next() {
+    q += step;
+    k += step;
+    if (k >= per) {
+      do {
+        k -= per;
+        ++r;
+      } while (k >= per);
+      open();
+    }
+  }
+  // every slot is the shard's alone
+  __device__ __forceinline__ bool whole() const {
+    const int e0 = k * kChunk * D::kVec - (int)((first & 15u) / sizeof(typename D::T));
+    return e0 >= 0 && e0 + kChunk * D::kVec <= len;
+  }
+  __device__ __forceinline__ int slot(int i) const { return k * kChunk + 32 * i + (int)(threadIdx.x & 31); }
+  __device__ __forceinline__ Slot<D> at(int i) const { return Slot<D>(first, len, slot(i)); }
+  // the lane's slots; bit i of the answer: slot i has a logit
+  __device__ __forceinline__ unsigned load(uint4 (&raw)[kPerLane]) const {
+    constexpr uint32_t none = NegInf<D>::word;
+    if (whole()) {
+      const uint4* p = reinterpret_cast<const uint4*>(first & ~uintptr_t(15)) + slot(0);
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) raw[i] = ld_stream(p + 32 * i);
+      return (1u << kPerLane) - 1;
+    }
+    unsigned some = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      raw[i] = make_uint4(none, none, none, none);
+      const Slot<D> t = at(i);
+      if (t.empty()) continue;
+      some |= 1u << i;
+      raw[i] = t.load();
+    }
+    return some;
+  }
+};
+
 // The logit of column c (0 <= c < V).
 template <class D>
 __device__ __forceinline__ float logit_at(const VocabRows& x, int64_t row, int c) {
@@ -116,39 +216,62 @@ __device__ __forceinline__ float logit_at(const VocabRows& x, int64_t row, int c
   return widen<D>(ld_stream_scalar(p));
 }
 
-__device__ __forceinline__ float exponent(float x, float m, float scale) {
-  return fmaxf((x - m) * scale, kFarBelow);
-}
-
-// Running statistics of a row relative to m (the largest logit so far, or the
-// lowest finite number): s = sum 2^t, u = sum t 2^t, t = (x - m) log2(e) / tau.
+// Running statistics of a row: s = sum 2^t, u = sum t 2^t, t = x scale - ref.
 struct Stats {
-  float m, s, u;
-  __device__ __forceinline__ void shift(float to, float scale) {
-    const float t = exponent(m, to, scale);
+  float ref, s, u;
+  __device__ __forceinline__ void move(float to) {
+    const float t = fmaxf(ref - to, kFarBelow);
     const float f = exp2_fast(t);
     u = __fmaf_rn(t, s, u) * f;
     s *= f;
-    m = to;
+    ref = to;
   }
-  __device__ __forceinline__ void join(Stats o, float scale) {
-    const float to = max_nan(m, o.m);
-    shift(to, scale);
-    o.shift(to, scale);
+  __device__ __forceinline__ void join(Stats o) {
+    const float to = fmaxf(ref, o.ref);
+    move(to);
+    o.move(to);
     s += o.s;
     u += o.u;
   }
 };
 
-__device__ __forceinline__ Stats warp_stats(Stats v, float scale) {
+__device__ __forceinline__ Stats warp_stats(Stats v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     Stats o;
-    o.m = __shfl_xor_sync(0xFFFFFFFFu, v.m, d);
+    o.ref = __shfl_xor_sync(0xFFFFFFFFu, v.ref, d);
     o.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, d);
     o.u = __shfl_xor_sync(0xFFFFFFFFu, v.u, d);
-    v.join(o, scale);
+    v.join(o);
   }
+  return v;
+}
+
+// ------------------------------------------- the CTAs that share a row (few
+// rows): one cluster, each CTA with a part of the chunks
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// `mine`'s place in the shared memory of CTA `rank`
+__device__ __forceinline__ uint32_t in_cta(const void* mine, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(mine)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float far_float(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t far_u64(uint32_t a) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
 
@@ -263,140 +386,235 @@ __device__ __forceinline__ bool load_teacher(Teacher& t, const int64_t* ids, con
 
 // ------------------------------------------------------------------ forward
 
-constexpr int kUnroll = 4;   // slots in flight per thread
+constexpr int kMaxThreads = 512;
+constexpr int kMaxParts = 8;   // CTAs of a portable cluster
 
 struct ForwardShared {
   RowShards rows;
-  Stats warp[32];
-  uint64_t lists[32][32];
+  Stats warp[kMaxThreads / 32];
+  Stats block;                         // for the other CTAs of the row
+  uint64_t lists[kMaxThreads / 32][32];
+  Teacher teacher;
   float red[2];
 };
 
-template <class D, bool DISTILL>
-__global__ void __launch_bounds__(512) vocab_forward_kernel(const __grid_constant__ VocabForward a) {
-  constexpr int V = D::kVec;
-  __shared__ ForwardShared sh;
-  const int64_t row = blockIdx.x;
-  const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float scale = kLog2e * a.x.inv_tau;
-  const int per = slots_per_shard<D>(a.x.C), slots = per * a.x.shards;
-  load_row<D>(a.x, row, sh.rows);
+// The block's statistics, the same in every thread (and of every CTA of the row).
+__device__ __forceinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  st = warp_stats(st);
+  if (lane == 0) sh.warp[threadIdx.x >> 5] = st;
   __syncthreads();
-
-  Stats st{-FLT_MAX, 0.0f, 0.0f};
-  float best = -INFINITY;   // the thread's largest logit and its slot (-1: it saw none)
-  int best_at = -1;
-  int r = tid / per, j = tid - r * per;
-  for (int g = tid; g < slots; g += n * kUnroll) {
-    uint4 raw[kUnroll];
-    bool some[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      constexpr uint32_t none = sizeof(typename D::T) == 4 ? NegInf<D>::bits : NegInf<D>::bits * 0x10001u;
-      raw[i] = make_uint4(none, none, none, none);
-      some[i] = false;
-      if (g + i * n < slots) {
-        const Slot<D> s(sh.rows, r, j);
-        some[i] = !s.empty();
-        if (some[i]) raw[i] = s.load();
-      }
-      j += n;
-      while (j >= per) {
-        j -= per;
-        ++r;
-      }
+  st = lane < warps ? sh.warp[lane] : Stats{kNoRef, 0.0f, 0.0f};
+  st = warp_stats(st);
+  if (parts > 1) {
+    if (threadIdx.x == 0) sh.block = st;
+    cluster_sync();
+    st = Stats{kNoRef, 0.0f, 0.0f};
+    if (lane < parts) {
+      const uint32_t a = in_cta(&sh.block, (uint32_t)lane);
+      st = Stats{far_float(a), far_float(a + 4), far_float(a + 8)};
     }
+    st = warp_stats(st);
+  }
+  return st;
+}
+
+// Rows without a logit above kNoRef: -inf everywhere, or the type's lowest
+// value in places (near -3e38, where x scale is out of range).  Their largest
+// logit m first, then t = (x - m) scale.  Rare, so it reads the row twice
+// more; m comes back as `largest`.
+template <class D>
+__device__ __noinline__ Stats lowest_stats(const VocabForward& a, ForwardShared& sh, int per, int begin, int end,
+                                           int parts, float scale, float* largest) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float m = -INFINITY;
+  uint4 raw[kPerLane];
+  for (Walk<D> w(sh.rows, per, begin + (int)(threadIdx.x >> 5), end, warps); w.more(); w.next()) {
+    w.load(raw);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (!some[i]) continue;
-      float x[V];
+    for (int i = 0; i < kPerLane; ++i) m = max_nan(m, word_value<D>(vector_max<D>(raw[i])));
+  }
+  m = warp_max_nan(m);
+  __syncthreads();   // sh.warp is read no more
+  if (lane == 0) sh.warp[threadIdx.x >> 5].s = m;
+  __syncthreads();
+  m = warp_max_nan(lane < warps ? sh.warp[lane].s : -INFINITY);
+  if (parts > 1) {
+    cluster_sync();   // sh.block is read no more
+    if (threadIdx.x == 0) sh.block.s = m;
+    cluster_sync();
+    m = lane < parts ? far_float(in_cta(&sh.block, (uint32_t)lane) + 4) : -INFINITY;
+    m = warp_max_nan(m);
+    cluster_sync();
+  }
+  __syncthreads();
+  *largest = m;
+  Stats st{0.0f, 0.0f, 0.0f};   // relative to m
+  for (Walk<D> w(sh.rows, per, begin + (int)(threadIdx.x >> 5), end, warps); w.more() && m > -INFINITY; w.next()) {
+    w.load(raw);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      float x[D::kVec];
       unpack<D>(raw[i], x);
-      float vm = x[0];
 #pragma unroll
-      for (int e = 1; e < V; ++e) vm = max_nan(vm, x[e]);
-      // of equals the first slot keeps the place; the first NaN takes it for good
-      if (vm > best || best_at < 0 || (vm != vm && best == best)) {
-        best = vm;
-        best_at = g + i * n;
-      }
-      if (!(vm <= st.m)) st.shift(max_nan(st.m, vm), scale);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float t = exponent(x[e], st.m, scale);
-        const float p = exp2_fast(t);
+      for (int e = 0; e < D::kVec; ++e) {
+        const float t = fmaxf((x[e] - m) * scale, kFarBelow), p = exp2_fast(t);
         st.s += p;
-        if (!DISTILL) st.u = __fmaf_rn(t, p, st.u);
+        st.u = __fmaf_rn(t, p, st.u);
       }
     }
   }
+  return block_stats(st, sh, parts);
+}
 
-  // the block's statistics, the same in every thread
-  st = warp_stats(st, scale);
-  if (lane == 0) sh.warp[warp] = st;
+template <class D, bool DISTILL>
+__global__ void __launch_bounds__(kMaxThreads, 2) vocab_forward_kernel(const __grid_constant__ VocabForward a,
+                                                                       int parts) {
+  constexpr int V = D::kVec;
+  __shared__ ForwardShared sh;
+  const int64_t row = blockIdx.x / parts;
+  const int part = parts > 1 ? (int)cluster_rank() : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const float scale = kLog2e * a.x.inv_tau;
+  const int per = chunks_per_shard<D>(a.x.C), chunks = per * a.x.shards;
+  const int share = (chunks + parts - 1) / parts;
+  const int begin = part * share, end = min(chunks, begin + share);
+  load_row<D>(a.x, row, sh.rows);
   __syncthreads();
-  st = lane < (n >> 5) ? sh.warp[lane] : Stats{-FLT_MAX, 0.0f, 0.0f};
-  st = warp_stats(st, scale);
-  const bool empty = st.s == 0.0f && st.m == -FLT_MAX;   // nothing but -inf
-  const bool broken = !(st.m < INFINITY);                // +inf or NaN: the row's values are NaN
-  const float log_s = broken ? NAN : logf(st.s);         // empty: -inf
-  const float lse = broken ? NAN : empty ? -INFINITY : __fmaf_rn(st.m, a.x.inv_tau, log_s);
-  auto log_prob = [&](float x) { return empty ? -INFINITY : (x - st.m) * a.x.inv_tau - log_s; };
-  if (tid == 0) st_g(a.lse + row, lse);
 
-  if constexpr (DISTILL) {
-    Teacher& t = *reinterpret_cast<Teacher*>(&sh.lists);
-    const bool taught = load_teacher<D>(t, a.ids, a.teacher, a.K, a.teacher_f32, row, a.x.V, a.x.inv_tau, sh.red);
-    if (warp == 0) {
-      float loss = 0.0f;
-      for (int k = lane; k < a.K; k += 32) {
-        if (t.q[k] != 0.0f) {   // NaN included
-          const float lp = log_prob(logit_at<D>(a.x, row, t.id[k]));
-          loss += t.q[k] * (t.logq[k] - lp);
+  Stats st{kNoRef, 0.0f, 0.0f};
+  float2 s2 = make_float2(0.0f, 0.0f), u2 = make_float2(0.0f, 0.0f);
+  float best = -INFINITY;   // the thread's largest logit and its slot (-1: it saw none)
+  int best_at = -1;
+  {
+    uint4 raw[kPerLane], ahead[kPerLane];
+    Walk<D> w(sh.rows, per, begin + warp, end, warps);
+    unsigned some = 0, some_ahead = 0;
+    if (w.more()) some = w.load(raw);
+    while (w.more()) {
+      const int slot = w.r * per * kChunk + w.slot(0);
+      w.next();
+      if (w.more()) some_ahead = w.load(ahead);
+      // the largest of the lane's 32 (16) logits, and where it passes `best`
+      float largest = -INFINITY;
+      if (!DISTILL) {
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const float vm = word_value<D>(vector_max<D>(raw[i]));
+          largest = fmaxf(largest, vm);
+          // of equals the first slot keeps the place; the first NaN takes it for good
+          if ((vm > best || best_at < 0 || (vm != vm && best == best)) && (some >> i & 1u)) {
+            best = vm;
+            best_at = slot + 32 * i;
+          }
+        }
+      } else {
+        uint32_t vm = vector_max<D>(raw[0]);
+#pragma unroll
+        for (int i = 1; i < kPerLane; ++i) vm = word_max<D>(vm, vector_max<D>(raw[i]));
+        largest = word_value<D>(vm);
+      }
+      if (largest * scale > st.ref + kLag) {
+        st.s = s2.x + s2.y;
+        st.u = u2.x + u2.y;
+        st.move(largest * scale);
+        s2 = make_float2(st.s, 0.0f);
+        u2 = make_float2(st.u, 0.0f);
+      }
+      const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(-st.ref, -st.ref);
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) {
+        float x[V];
+        unpack<D>(raw[i], x);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 t = __ffma2_rn(make_float2(x[e], x[e + 1]), scale2, ref2);
+          const float2 p = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+          s2 = __fadd2_rn(s2, p);
+          if (!DISTILL) u2 = __ffma2_rn(make_float2(fmaxf(t.x, kFarBelow), fmaxf(t.y, kFarBelow)), p, u2);
         }
       }
-      loss = warp_sum(loss);
-      if (lane == 0) st_g(a.loss + row, taught ? loss * a.x.tau * a.x.tau : 0.0f);
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) raw[i] = ahead[i];
+      some = some_ahead;
+    }
+  }
+  st.s = s2.x + s2.y;
+  st.u = u2.x + u2.y;
+  st = block_stats(st, sh, parts);
+  float lowest = 0.0f;
+  const bool low = st.s == 0.0f;   // no logit above kNoRef
+  if (low) st = lowest_stats<D>(a, sh, per, begin, end, parts, scale, &lowest);
+  const bool empty = low && lowest == -INFINITY;   // nothing but -inf
+  const float log2_s = log2f(st.s);                // NaN where the row has +inf or NaN
+  const float lse = empty ? -INFINITY
+                    : low ? __fmaf_rn(lowest, a.x.inv_tau, kLn2 * log2_s)
+                          : kLn2 * (st.ref + log2_s);
+  auto log_prob = [&](float x) {
+    if (empty) return -INFINITY;
+    const float d = low ? x - lowest : x;
+    const float t = __fmaf_rn(d, scale, low ? 0.0f : -st.ref);
+    // a masked logit near the type's lowest value leaves binary32's range in t before it does so itself
+    return t == -INFINITY && log2_s == log2_s ? d * a.x.inv_tau : kLn2 * (t - log2_s);
+  };
+  const bool first = part == 0;
+  if (first && tid == 0) st_g(a.lse + row, lse);
+
+  if constexpr (DISTILL) {
+    if (first) {
+      Teacher& t = sh.teacher;
+      const bool taught = load_teacher<D>(t, a.ids, a.teacher, a.K, a.teacher_f32, row, a.x.V, a.x.inv_tau, sh.red);
+      if (warp == 0) {
+        float loss = 0.0f;
+        for (int k = lane; k < a.K; k += 32) {
+          if (t.q[k] != 0.0f) {   // NaN included
+            const float lp = log_prob(logit_at<D>(a.x, row, t.id[k]));
+            loss += t.q[k] * (t.logq[k] - lp);
+          }
+        }
+        loss = warp_sum(loss);
+        if (lane == 0) st_g(a.loss + row, taught ? loss * a.x.tau * a.x.tau : 0.0f);
+      }
     }
   } else {
-    if (tid == 0) {
+    if (first && tid == 0) {
       const int64_t target = ld_g(a.targets + row);
       // no target: 0; a target that is no column: NaN
       st_g(a.logprob + row, target < 0 ? 0.0f : target >= a.x.V ? NAN : log_prob(logit_at<D>(a.x, row, (int)target)));
-      if (a.entropy) st_g(a.entropy + row, empty ? 0.0f : log_s - kLn2 * (st.u / st.s));
+      if (a.entropy) st_g(a.entropy + row, empty ? 0.0f : kLn2 * (log2_s - st.u / st.s));
     }
     if (a.top > 0) {
       // the K-th largest of the threads' maxima, by (logit, slot)
       uint64_t k = best_at < 0 ? 0 : top_key(best, (uint32_t)best_at);
       k = block_merge(warp_sort(k), sh.lists);
-      if (warp == 0) sh.lists[0][lane] = k;
-      __syncthreads();
       const uint64_t mine = sh.lists[0][lane];
       const uint64_t bound = __shfl_sync(0xFFFFFFFFu, mine, a.top - 1);
       __syncthreads();
       // the threads that reach it: each warp reads its share of their slots again
       uint64_t list = 0;
-      for (int q = warp; q < a.top; q += n >> 5) {
-        const uint64_t key = __shfl_sync(0xFFFFFFFFu, mine, q);
+      for (int i = warp; i < a.top; i += warps) {
+        const uint64_t key = __shfl_sync(0xFFFFFFFFu, mine, i);
         if (key == 0) continue;   // fewer threads than K saw a logit
-        const int owner = (int)(~(uint32_t)key) % n;
-        for (int g0 = owner; g0 < slots; g0 += 32 * n) {
-          const int64_t g = g0 + (int64_t)lane * n;
-          bool have = g < slots;
+        const int at = (int)~(uint32_t)key;   // a slot of the thread's: r per kChunk + k kChunk + 32 i + lane
+        const int owner = (at / kChunk - begin) % warps, owner_lane = at & 31;
+        for (int q0 = begin + owner; q0 < end; q0 += 8 * warps) {
+          const int q = q0 + (lane >> 2) * warps;   // eight of its chunks at a time, four slots each
           uint4 raw = make_uint4(0, 0, 0, 0);
-          int lo = 0, hi = 0, column = 0;
-          if (have) {
-            const int rr = (int)g / per;
-            const Slot<D> s(sh.rows, rr, (int)g - rr * per);
+          int lo = 0, hi = 0, column = 0, slot = 0;
+          if (q < end) {
+            const int r = q / per, j = (q - r * per) * kChunk + 32 * (lane & 3) + owner_lane;
+            const Slot<D> s(sh.rows.first[r], sh.rows.len[r], j);
             lo = s.lo;
             hi = s.hi;
-            column = rr * a.x.C + s.e0;
+            column = r * a.x.C + s.e0;
+            slot = r * per * kChunk + j;
             if (!s.empty()) raw = s.load();
           }
           float x[V];
           unpack<D>(raw, x);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const bool may = e >= lo && e < hi && top_key(x[e], (uint32_t)g) >= bound;
+            const bool may = e >= lo && e < hi && top_key(x[e], (uint32_t)slot) >= bound;
             uint32_t hits = __ballot_sync(0xFFFFFFFFu, may);
             const uint64_t full = top_key(x[e], (uint32_t)(column + e));
             while (hits) {
@@ -408,12 +626,18 @@ __global__ void __launch_bounds__(512) vocab_forward_kernel(const __grid_constan
         }
       }
       list = block_merge(list, sh.lists);
-      if (warp == 0 && lane < a.top) {
+      if (parts > 1) {
+        cluster_sync();
+        if (first && warp == 0)
+          for (int i = 1; i < parts; ++i) list = warp_merge(list, far_u64(in_cta(&sh.lists[0][lane], (uint32_t)i)));
+      }
+      if (first && warp == 0 && lane < a.top) {
         st_g(a.top_ids + row * a.top + lane, (int64_t)(uint32_t)~(uint32_t)list);
         st_g(a.top_logprobs + row * a.top + lane, log_prob(from_ordered((uint32_t)(list >> 32))));
       }
     }
   }
+  if (parts > 1) cluster_sync();   // no CTA ends while its shared memory may be read
 }
 
 // ----------------------------------------------------------------- backward
@@ -427,21 +651,25 @@ struct BackwardShared {
 };
 
 template <class D, bool DISTILL>
-__global__ void __launch_bounds__(512) vocab_backward_kernel(const __grid_constant__ VocabBackward a, int parts) {
+__global__ void __launch_bounds__(256, 4) vocab_backward_kernel(const __grid_constant__ VocabBackward a, int parts) {
   constexpr int V = D::kVec;
   using T = typename D::T;
   __shared__ BackwardShared sh;
   const int64_t row = blockIdx.x / parts;
   const int part = (int)(blockIdx.x - row * parts);
   const int n = blockDim.x, tid = threadIdx.x;
-  const int per = slots_per_shard<D>(a.x.C), slots = per * a.x.shards;
-  const int share = (slots + parts - 1) / parts;
-  const int begin = part * share, end = min(slots, begin + share);
+  const int per = chunks_per_shard<D>(a.x.C), chunks = per * a.x.shards;
+  const int share = (chunks + parts - 1) / parts;
+  const int begin = part * share, end = min(chunks, begin + share);
   const float inv_tau = a.x.inv_tau;
   load_row<D>(a.x, row, sh.rows);
   for (int r = tid; r < a.x.shards; r += n)
     sh.grad[r] = reinterpret_cast<uintptr_t>(a.grad[r]) + (uintptr_t)(row * a.grad_stride[r]) * sizeof(T);
   __syncthreads();
+  // the first chunk is on its way while the row's coefficients are made
+  uint4 raw[kPerLane], ahead[kPerLane];
+  Walk<D> w(sh.rows, per, begin + (tid >> 5), end, n >> 5);
+  if (w.more()) w.load(raw);
 
   // dL_j = p_j (A + B log p_j), plus what the target or the teacher adds
   float A, B = 0.0f, add = 0.0f;
@@ -471,11 +699,20 @@ __global__ void __launch_bounds__(512) vocab_backward_kernel(const __grid_consta
     __syncthreads();
   }
   if (zero) A = B = 0.0f;
-  auto gradient = [&](float x) {
-    const float lp = __fmaf_rn(x, inv_tau, -lse);
-    const float p = sizeof(T) == 4 ? expf(lp) : exp2_fast(lp * kLog2e);
-    if (DISTILL || B == 0.0f) return A * p;
-    return p * __fmaf_rn(B, fmaxf(lp, kFarBelow), A);
+  // binary32 outputs show the exponent's rounding: expf there
+  auto gradient = [&](float2 x) {
+    const float2 lp = __ffma2_rn(x, make_float2(inv_tau, inv_tau), make_float2(-lse, -lse));
+    float2 p;
+    if (sizeof(T) == 4) {
+      p = make_float2(expf(lp.x), expf(lp.y));
+    } else {
+      const float2 t = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
+      p = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+    }
+    float2 c = make_float2(A, A);
+    if (!DISTILL && B != 0.0f)
+      c = __ffma2_rn(make_float2(B, B), make_float2(fmaxf(lp.x, kFarBelow), fmaxf(lp.y, kFarBelow)), c);
+    return __fmul2_rn(p, c);
   };
   // the columns with more than that, read before any of them is written (the
   // gradient may stand in the logits' place); of equal tokens the first one
@@ -486,8 +723,8 @@ __global__ void __launch_bounds__(512) vocab_backward_kernel(const __grid_consta
     bool mine = false;
     if (c >= 0) {
       const int r = c / a.x.C;
-      const int slot = r * per + (int)((sh.rows.first[r] & 15u) / sizeof(T) + (c - r * a.x.C)) / V;
-      mine = slot >= begin && slot < end;
+      const int chunk = r * per + ((int)((sh.rows.first[r] & 15u) / sizeof(T)) + (c - r * a.x.C)) / (V * kChunk);
+      mine = chunk >= begin && chunk < end;
     }
     if (mine) {
       if (DISTILL) {
@@ -498,7 +735,7 @@ __global__ void __launch_bounds__(512) vocab_backward_kernel(const __grid_consta
           }
         }
       }
-      if (mine) v = gradient(logit_at<D>(a.x, row, c)) + add;
+      if (mine) v = gradient(make_float2(logit_at<D>(a.x, row, c), 0.0f)).x + add;
       if (DISTILL) add = 0.0f;
     }
     sh.fix[k] = v;
@@ -506,40 +743,34 @@ __global__ void __launch_bounds__(512) vocab_backward_kernel(const __grid_consta
   }
   __syncthreads();
 
-  int g = begin + tid, r = g / per, j = g - r * per;
-  for (; g < end; g += n * kUnroll) {
-    uint4 raw[kUnroll];
-    Slot<D> s[kUnroll] = {Slot<D>(sh.rows, 0, 0), Slot<D>(sh.rows, 0, 0), Slot<D>(sh.rows, 0, 0),
-                          Slot<D>(sh.rows, 0, 0)};
+  while (w.more()) {
+    const bool whole = w.whole();
+    const int r = w.r, j = w.slot(0), len = w.len;
+    const uintptr_t first = w.first;
+    w.next();
+    if (w.more()) w.load(ahead);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      s[i].hi = s[i].lo;
-      if (g + i * n < end) {
-        s[i] = Slot<D>(sh.rows, r, j);
-        if (!s[i].empty()) raw[i] = s[i].load();
-      }
-      j += n;
-      while (j >= per) {
-        j -= per;
-        ++r;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (s[i].empty()) continue;
+    for (int i = 0; i < kPerLane; ++i) {
       float x[V];
       unpack<D>(raw[i], x);
 #pragma unroll
-      for (int e = 0; e < V; ++e) x[e] = zero ? 0.0f : gradient(x[e]);
-      T* to = reinterpret_cast<T*>(sh.grad[s[i].r]) + s[i].e0;
-      if (s[i].whole() && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+      for (int e = 0; e < V; e += 2) {
+        const float2 d = gradient(make_float2(x[e], x[e + 1]));
+        x[e] = zero ? 0.0f : d.x;
+        x[e + 1] = zero ? 0.0f : d.y;
+      }
+      const Slot<D> s(first, len, j + 32 * i);
+      T* to = reinterpret_cast<T*>(sh.grad[r]) + s.e0;
+      if ((whole || s.whole()) && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
         st_stream(reinterpret_cast<uint4*>(to), pack<D>(x));
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (e >= s[i].lo && e < s[i].hi) st_g(to + e, narrow<D>(x[e]));
+          if (e >= s.lo && e < s.hi) st_g(to + e, narrow<D>(x[e]));
       }
     }
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) raw[i] = ahead[i];
   }
   if (fixes == 0) return;
   __syncthreads();
@@ -559,21 +790,34 @@ template <class F> cudaError_t with_float(int dtype, F&& f) {
   }
 }
 
-int threads_for(int slots) { return slots > 256 * kUnroll ? 512 : slots > 128 * kUnroll ? 256 : 128; }
-
 }  // namespace
 
-cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int, cudaStream_t st) {
+cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cudaStream_t st) {
   cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
-    const int threads = threads_for(slots_per_shard<D>(a.x.C) * a.x.shards);
-    if (a.ids)
-      vocab_forward_kernel<D, true><<<(unsigned)a.x.rows, threads, 0, st>>>(a);
-    else
-      vocab_forward_kernel<D, false><<<(unsigned)a.x.rows, threads, 0, st>>>(a);
-    return cudaGetLastError();
+    const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
+    // Many rows: CTAs of 256 threads, so that one's sums and lists overlap
+    // the others' reading.  Few rows: 512 threads, and clusters that split a
+    // row until the SMs are covered, eight chunks a CTA at least.
+    const bool many = a.x.rows >= 2 * (int64_t)sms;
+    const int threads = many ? 256 : chunks >= 16 ? 512 : chunks >= 8 ? 256 : 128;
+    int parts = 1;
+    if (!many)
+      while (parts < kMaxParts && a.x.rows * parts * 2 <= 2 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
+    auto kernel = a.ids ? vocab_forward_kernel<D, true> : vocab_forward_kernel<D, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.x.rows * parts));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)parts;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, parts);
   });
 }
 
@@ -582,12 +826,11 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
   if (e != cudaSuccess) return e;
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
-    const int slots = slots_per_shard<D>(a.x.C) * a.x.shards;
-    const int threads = threads_for(slots);
-    // few rows: split each over CTAs until the SMs are covered, a batch of
-    // slots each at least
+    const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
+    const int threads = chunks >= 8 ? 256 : 128, warps = threads / 32;
+    // few rows: split each over CTAs until the SMs are covered, a chunk a warp at least
     int64_t parts = ((int64_t)4 * sms + a.x.rows - 1) / a.x.rows;
-    const int64_t most = (slots + threads * kUnroll - 1) / (threads * kUnroll);
+    const int64_t most = (chunks + warps - 1) / warps;
     if (parts > most) parts = most;
     const unsigned grid = (unsigned)(a.x.rows * parts);
     if (a.ids)
