@@ -16,10 +16,11 @@
 // ln2 (ref + log2 s) and H = ln2 (log2 s - u / s).  All statistics are binary32.
 //
 // The top K come out of the same pass without a comparison per element
-// against a list: each thread also keeps the largest logit it saw and where.
-// The K-th largest of those maxima bounds the row's K-th largest logit from
-// below, and only the K threads whose maximum reaches it can hold one of the
-// top K: their columns, K / threads of the row, are read again.
+// against a list: each thread also keeps the largest logit it saw, and its
+// largest of every chunk in shared memory.  The K-th largest of the threads'
+// maxima bounds the row's K-th largest logit from below; a lane's part of a
+// chunk is read again only where its largest reaches that, and the few logits
+// that do are ranked against each other.
 //
 // A row's shards are cut into 16-byte slots, and these into chunks of 128, a
 // lane's four 512 bytes apart; a warp takes every warps-th chunk.  A slot that
@@ -45,9 +46,11 @@ constexpr float kNoRef = -8.5e37f;     // ref before the first finite logit
 constexpr float kNothingLeft = -1e30f;
 
 template <class D> struct NegInf;
-template <> struct NegInf<DF32> { static constexpr uint32_t word = 0xFF800000u, one = 0xFF800000u; };
-template <> struct NegInf<DBF16> { static constexpr uint32_t word = 0xFF80FF80u, one = 0xFF80u; };
-template <> struct NegInf<DF16> { static constexpr uint32_t word = 0xFC00FC00u, one = 0xFC00u; };
+// -inf, and the type's lowest value, ordered()
+template <> struct NegInf<DF32> { static constexpr uint32_t word = 0xFF800000u, one = 0xFF800000u, lowest = 0x00800000u; };
+template <> struct NegInf<DBF16> { static constexpr uint32_t word = 0xFF80FF80u, one = 0xFF80u, lowest = 0x0080FFFFu; };
+template <> struct NegInf<DF16> { static constexpr uint32_t word = 0xFC00FC00u, one = 0xFC00u, lowest = 0x38801FFFu; };
+constexpr uint32_t kOrderedNegInf = 0x007FFFFFu;
 
 // The largest of a slot's logits, NaN if there is one.
 template <class D> __device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b);
@@ -186,22 +189,22 @@ template <class D> struct Walk {
   }
   __device__ __forceinline__ int slot(int i) const { return k * kChunk + 32 * i + (int)(threadIdx.x & 31); }
   __device__ __forceinline__ Slot<D> at(int i) const { return Slot<D>(first, len, slot(i)); }
-  // the lane's slots; bit i of the answer: slot i has a logit
-  __device__ __forceinline__ unsigned load(uint4 (&raw)[kPerLane]) const {
+  // the lane's slots; whether any of them has a logit
+  __device__ __forceinline__ bool load(uint4 (&raw)[kPerLane]) const {
     constexpr uint32_t none = NegInf<D>::word;
     if (whole()) {
       const uint4* p = reinterpret_cast<const uint4*>(first & ~uintptr_t(15)) + slot(0);
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) raw[i] = ld_stream(p + 32 * i);
-      return (1u << kPerLane) - 1;
+      return true;
     }
-    unsigned some = 0;
+    bool some = false;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       raw[i] = make_uint4(none, none, none, none);
       const Slot<D> t = at(i);
       if (t.empty()) continue;
-      some |= 1u << i;
+      some = true;
       raw[i] = t.load();
     }
     return some;
@@ -236,7 +239,7 @@ struct Stats {
 };
 
 __device__ __forceinline__ Stats warp_stats(Stats v) {
-#pragma unroll
+#pragma unroll 1
   for (int d = 16; d > 0; d >>= 1) {
     Stats o;
     o.ref = __shfl_xor_sync(0xFFFFFFFFu, v.ref, d);
@@ -278,8 +281,9 @@ __device__ __forceinline__ uint64_t far_u64(uint32_t a) {
 // ---------------------------------------------- lists of a warp's 32 largest
 // A warp holds 32 keys, falling from lane 0; 0 is no key.
 
-// A bitonic sequence of 32 keys into falling order.
-__device__ __forceinline__ uint64_t warp_fall(uint64_t k) {
+// (Called, not inlined: what runs once a row costs mostly its way into the
+// instruction cache.)  A bitonic sequence of 32 keys into falling order.
+__device__ __noinline__ uint64_t warp_fall(uint64_t k) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
@@ -291,11 +295,11 @@ __device__ __forceinline__ uint64_t warp_fall(uint64_t k) {
 }
 
 // Any 32 keys into falling order.
-__device__ __forceinline__ uint64_t warp_sort(uint64_t k) {
+__device__ __noinline__ uint64_t warp_sort(uint64_t k) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
+#pragma unroll 1
     for (int d = size >> 1; d > 0; d >>= 1) {
       const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, k, d);
       const bool falling = (lane & size) == 0 || size == 32;
@@ -313,7 +317,7 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
 }
 
 // The block's 32 largest of every warp's list, in warp 0.
-__device__ __forceinline__ uint64_t block_merge(uint64_t k, uint64_t (*lists)[32]) {
+__device__ __noinline__ uint64_t block_merge(uint64_t k, uint64_t (*lists)[32]) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
   lists[w][lane] = k;
   __syncthreads();
@@ -334,72 +338,107 @@ __device__ __forceinline__ uint64_t warp_insert(uint64_t mine, uint64_t key) {
   return lane < pos ? mine : lane == pos ? key : above;
 }
 
-// ------------------------------------------------------------------ teacher
-
-// The teacher's distribution over its tokens, in every thread of the block
-// that runs this: q[k], log q[k] (0 where the token is absent), and whether
-// the row has any.  ids[k] is -1 where the token is absent: a negative id or
-// one that is no column, or a teacher logit of -inf.
-struct Teacher {
-  int id[kTeacherMax];
-  float q[kTeacherMax];
-  float logq[kTeacherMax];
+// A warp's 32 best logits so far (by value, then column), and the K-th of them.
+struct Best {
+  uint64_t list, last, bound;
+  int top;
+  // The lanes' slots, elements [lo, hi) of each: what comes before the bound
+  // by (logit, chunk) and before the K-th.
+  template <class D> __device__ __noinline__ void offer(uint4 raw, int lo, int hi, int chunk, int column) {
+    float x[D::kVec];
+    unpack<D>(raw, x);
+    unsigned want = 0;
+#pragma unroll
+    for (int e = 0; e < D::kVec; ++e)
+      if (e >= lo && e < hi && top_key(x[e], (uint32_t)chunk) > bound) want |= 1u << e;
+    while (__any_sync(0xFFFFFFFFu, want != 0)) {   // a logit of each lane at a time
+      const bool some = want != 0;
+      const int e = some ? __ffs(want) - 1 : 0;
+      want &= want - 1;   // of 0: 0
+      float v = x[0];
+#pragma unroll
+      for (int k = 1; k < D::kVec; ++k) v = e == k ? x[k] : v;
+      const uint64_t full = top_key(v, (uint32_t)(column + e));
+      const bool may = some && full > last;
+      unsigned hits = __ballot_sync(0xFFFFFFFFu, may);
+      if (__popc(hits) > 8) {   // all of them at once
+        list = warp_merge(list, warp_sort(may ? full : 0));
+      } else {
+        for (; hits; hits &= hits - 1) list = warp_insert(list, __shfl_sync(0xFFFFFFFFu, full, __ffs(hits) - 1));
+      }
+      last = __shfl_sync(0xFFFFFFFFu, list, top - 1);
+    }
+  }
 };
 
+// ------------------------------------------------------------------ teacher
+
+// The teacher's tokens: columns (-1 where one is absent: an id that is no
+// column, or a teacher logit of -inf), logits, and the student's logits there.
+struct Teacher {
+  int id[kTeacherMax];
+  float t[kTeacherMax];
+  float x[kTeacherMax];
+};
+
+// Called by the whole block, before a barrier.
 template <class D>
-__device__ __forceinline__ bool load_teacher(Teacher& t, const int64_t* ids, const void* teacher, int K, bool f32,
-                                             int64_t row, int V, float inv_tau, float* red) {
-  // one warp: K is at most 256, eight a lane
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    float m = -INFINITY;
-    for (int k = lane; k < K; k += 32) {
-      const int64_t id = ld_g(ids + row * K + k);
-      float x = f32 ? ld_g(static_cast<const float*>(teacher) + row * K + k)
-                    : widen<D>(ld_g(static_cast<const typename D::T*>(teacher) + row * K + k));
-      const bool absent = id < 0 || id >= V || x == -INFINITY;
-      t.id[k] = absent ? -1 : (int)id;
-      t.logq[k] = x;
-      if (!absent) m = max_nan(m, x);
-    }
-    m = warp_max_nan(m);
-    float s = 0.0f;
-    for (int k = lane; k < K; k += 32) {
-      const float d = (t.logq[k] - m) * inv_tau;
-      const float e = t.id[k] < 0 ? 0.0f : expf(d);
-      t.q[k] = e;
-      t.logq[k] = d;
-      s += e;
-    }
-    s = warp_sum(s);
-    const float log_s = logf(s);
-    for (int k = lane; k < K; k += 32) {
-      const bool some = t.id[k] >= 0;
-      t.q[k] = some ? t.q[k] / s : 0.0f;
-      t.logq[k] = some ? t.logq[k] - log_s : 0.0f;
-    }
-    if (lane == 0) red[0] = m;
+__device__ __forceinline__ void load_teacher(Teacher& to, const VocabRows& rows, const int64_t* ids,
+                                             const void* teacher, int K, bool f32, int64_t row) {
+  for (int k = threadIdx.x; k < K; k += blockDim.x) {
+    const int64_t id = ld_g(ids + row * K + k);
+    const float t = f32 ? ld_g(static_cast<const float*>(teacher) + row * K + k)
+                        : widen<D>(ld_g(static_cast<const typename D::T*>(teacher) + row * K + k));
+    const bool absent = id < 0 || id >= rows.V || t == -INFINITY;
+    to.id[k] = absent ? -1 : (int)id;
+    to.t[k] = t;
+    to.x[k] = absent ? 0.0f : logit_at<D>(rows, row, (int)id);
   }
-  __syncthreads();
-  return red[0] != -INFINITY;   // NaN: the row has a teacher, and its values are NaN
 }
+
+// The softmax's largest logit and sum over the tokens, in every lane of the
+// warp that runs this (every warp that needs them does, so that no barrier
+// follows); m is -inf where the row has none, NaN where a logit is.
+struct Softmax {
+  float m, s;
+  __device__ __forceinline__ Softmax(const Teacher& t, int K, float inv_tau) {
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+    for (int k = lane; k < K; k += 32)
+      if (t.id[k] >= 0) m = max_nan(m, t.t[k]);
+    m = warp_max_nan(m);
+    s = 0.0f;
+    for (int k = lane; k < K; k += 32)
+      if (t.id[k] >= 0) s += expf((t.t[k] - m) * inv_tau);
+    s = warp_sum(s);
+  }
+  __device__ __forceinline__ bool taught() const { return m != -INFINITY; }
+};
 
 // ------------------------------------------------------------------ forward
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 256;
 constexpr int kMaxParts = 8;   // CTAs of a portable cluster
+constexpr int kCandidates = 512;
 
 struct ForwardShared {
   RowShards rows;
   Stats warp[kMaxThreads / 32];
   Stats block;                         // for the other CTAs of the row
   uint64_t lists[kMaxThreads / 32][32];
+  uint32_t again[kMaxThreads / 32][32];   // parts of chunks to read again
+  uint64_t candidates[kCandidates];
+  int found;
+  int lowest;                             // a logit of the type's lowest value was seen
   Teacher teacher;
-  float red[2];
 };
 
+// Every lane's largest logit of every chunk of the CTA, ordered(): [chunk - begin][lane].
+extern __shared__ uint32_t g_largest[];
+constexpr int kMostLarge = 512;   // chunks (64 KB); a CTA with more reads all its chunks again
+
 // The block's statistics, the same in every thread (and of every CTA of the row).
-__device__ __forceinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts) {
+__device__ __noinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   st = warp_stats(st);
   if (lane == 0) sh.warp[threadIdx.x >> 5] = st;
@@ -467,8 +506,146 @@ __device__ __noinline__ Stats lowest_stats(const VocabForward& a, ForwardShared&
   return block_stats(st, sh, parts);
 }
 
+// The lanes' slots, elements [lo, hi) of each: those that reach the bound
+// become candidates, as far as there is room.
+template <class D>
+__device__ __noinline__ void collect(ForwardShared& sh, uint4 raw, int lo, int hi, int column, uint32_t bound) {
+  const int lane = threadIdx.x & 31;
+  float x[D::kVec];
+  unpack<D>(raw, x);
+  unsigned want = 0;
+#pragma unroll
+  for (int e = 0; e < D::kVec; ++e) {
+    if (e < lo || e >= hi) continue;
+    if (ordered(x[e]) >= bound) want |= 1u << e;
+    if (ordered(x[e]) == NegInf<D>::lowest) sh.lowest = 1;
+  }
+  int before = __popc(want);   // and in the lanes below
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const int below = __shfl_up_sync(0xFFFFFFFFu, before, d);
+    if (lane >= d) before += below;
+  }
+  const int all = __shfl_sync(0xFFFFFFFFu, before, 31);
+  if (all == 0) return;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(&sh.found, all);   // their order does not matter: they are ranked
+  at = __shfl_sync(0xFFFFFFFFu, at, 0) + before - __popc(want);
+  for (; want; want &= want - 1, ++at) {
+    const int e = __ffs(want) - 1;
+    float v = x[0];
+#pragma unroll
+    for (int k = 1; k < D::kVec; ++k) v = e == k ? x[k] : v;
+    if (at < kCandidates) sh.candidates[at] = top_key(v, (uint32_t)(column + e));
+  }
+}
+
+// The first column from chunk q on.
+template <class D>
+__device__ __forceinline__ int column_of(const RowShards& s, int q, int per, int chunks, int C, int V) {
+  if (q >= chunks) return V;
+  const int r = q / per;
+  const int c = (q - r * per) * kChunk * D::kVec - (int)((s.first[r] & 15u) / sizeof(typename D::T));
+  return r * C + min(max(c, 0), s.len[r]);
+}
+
+// The same from all the CTA's chunks.
+template <class D>
+__device__ __noinline__ void read_all(ForwardShared& sh, int per, int begin, int end, int C, uint32_t bound) {
+  for (Walk<D> w(sh.rows, per, begin + (int)(threadIdx.x >> 5), end, blockDim.x >> 5); w.more(); w.next()) {
+    uint4 raw[kPerLane];
+    w.load(raw);
+#pragma unroll 1
+    for (int i = 0; i < kPerLane; ++i) {
+      const Slot<D> s = w.at(i);
+      const uint4 v = i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3];
+      const uint32_t most = s.empty() ? 0 : ordered(word_value<D>(vector_max<D>(v)));
+      if (most == NegInf<D>::lowest) sh.lowest = 1;
+      if (__any_sync(0xFFFFFFFFu, most >= bound && most != 0)) collect<D>(sh, v, s.lo, s.hi, w.r * C + s.e0, bound);
+    }
+  }
+}
+
+// lists[0]: the `top` largest of the candidates (0: none), falling; all keys
+// but 0 differ.
+__device__ __noinline__ void rank_candidates(ForwardShared& sh, int n, int top) {
+  if (threadIdx.x < 32) sh.lists[0][threadIdx.x] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint64_t key = sh.candidates[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) rank += sh.candidates[k] > key;
+    if (key != 0 && rank < top) sh.lists[0][rank] = key;
+  }
+  __syncthreads();
+}
+
+// The same where too many logits reach a bound of 16 bits (equal ones, mostly:
+// a mask that leaves fewer than K).  The K-th largest of the threads' maxima
+// by (logit, chunk): chunks are numbered in the columns' order, so whatever
+// comes after that is beaten by K logits.  What comes before it is read again;
+// what is equal to it lies in its chunk.
+template <class D>
+__device__ __noinline__ void top_of_many(ForwardShared& sh, float best, int best_at, int top, int C, int per,
+                                         int begin, int end) {
+  constexpr int V = D::kVec;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const uint64_t mine = best_at < 0 ? 0 : top_key(best, (uint32_t)best_at);
+  __syncthreads();
+  block_merge(warp_sort(mine), sh.lists);
+  const uint64_t bound = sh.lists[0][top - 1];
+  __syncthreads();
+  Best best_of{0, 0, bound, top};
+  if (__any_sync(0xFFFFFFFFu, mine > bound)) {   // else no logit of the warp comes before it
+    const uint32_t least = (uint32_t)(bound >> 32);
+    for (Walk<D> w(sh.rows, per, begin + warp, end, warps); w.more(); w.next()) {
+      uint4 raw[kPerLane];
+      w.load(raw);
+#pragma unroll 1
+      for (int i = 0; i < kPerLane; ++i) {
+        const Slot<D> s = w.at(i);
+        const uint4 v = i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3];
+        const bool reach = ordered(word_value<D>(vector_max<D>(v))) >= least;
+        if (__any_sync(0xFFFFFFFFu, reach)) best_of.offer<D>(v, s.lo, s.hi, w.q, w.r * C + s.e0);
+      }
+    }
+  }
+  // the first 32 of the logits equal to the bound in its chunk: one warp, in the columns' order
+  const int tied = (int)~(uint32_t)bound;
+  if (bound != 0 && (tied - begin) % warps == warp) {
+    const int r = tied / per;
+    int got = 0;
+    for (int i = 0; i < kPerLane && got < 32; ++i) {
+      const Slot<D> s(sh.rows.first[r], sh.rows.len[r], (tied - r * per) * kChunk + 32 * i + lane);
+      float x[V];
+      unpack<D>(s.empty() ? make_uint4(0, 0, 0, 0) : s.load(), x);
+      unsigned equal = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e >= s.lo && e < s.hi && ordered(x[e]) == (uint32_t)(bound >> 32)) equal |= 1u << e;
+      int before = __popc(equal);   // and in the lanes below
+#pragma unroll 1
+      for (int d = 1; d < 32; d <<= 1) {
+        const int below = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d) before += below;
+      }
+      int at = got + before - __popc(equal);
+      for (; equal; equal &= equal - 1, ++at)
+        if (at < 32)
+          sh.lists[warp][at] =
+              ((uint64_t)(uint32_t)(bound >> 32) << 32) | (uint32_t)~(uint32_t)(r * C + s.e0 + __ffs(equal) - 1);
+      got += __shfl_sync(0xFFFFFFFFu, before, 31);
+    }
+    __syncwarp();
+    best_of.list = warp_merge(best_of.list, lane < got ? sh.lists[warp][lane] : 0);
+    __syncwarp();
+  }
+  block_merge(best_of.list, sh.lists);
+}
+
 template <class D, bool DISTILL>
-__global__ void __launch_bounds__(kMaxThreads, 2) vocab_forward_kernel(const __grid_constant__ VocabForward a,
+__global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __grid_constant__ VocabForward a,
                                                                        int parts) {
   constexpr int V = D::kVec;
   __shared__ ForwardShared sh;
@@ -480,40 +657,43 @@ __global__ void __launch_bounds__(kMaxThreads, 2) vocab_forward_kernel(const __g
   const int share = (chunks + parts - 1) / parts;
   const int begin = part * share, end = min(chunks, begin + share);
   load_row<D>(a.x, row, sh.rows);
+  if (tid == 0) sh.found = sh.lowest = 0;
+  if (part == 0) {
+    if (DISTILL) {
+      load_teacher<D>(sh.teacher, a.x, a.ids, a.teacher, a.K, a.teacher_f32, row);
+    } else if (tid == 0) {
+      const int64_t target = ld_g(a.targets + row);
+      // no target: -1; one that is no column: -2
+      sh.teacher.id[0] = target < 0 ? -1 : target >= a.x.V ? -2 : 0;
+      sh.teacher.x[0] = target < 0 || target >= a.x.V ? 0.0f : logit_at<D>(a.x, row, (int)target);
+    }
+  }
   __syncthreads();
 
   Stats st{kNoRef, 0.0f, 0.0f};
   float2 s2 = make_float2(0.0f, 0.0f), u2 = make_float2(0.0f, 0.0f);
-  float best = -INFINITY;   // the thread's largest logit and its slot (-1: it saw none)
+  float best = -INFINITY;   // the thread's largest logit, and the first chunk that has it (-1: it saw none)
   int best_at = -1;
+  const bool keep = !DISTILL && a.top > 0 && share <= kMostLarge;
   {
     uint4 raw[kPerLane], ahead[kPerLane];
     Walk<D> w(sh.rows, per, begin + warp, end, warps);
-    unsigned some = 0, some_ahead = 0;
+    bool some = false, some_ahead = false;
     if (w.more()) some = w.load(raw);
     while (w.more()) {
-      const int slot = w.r * per * kChunk + w.slot(0);
+      const int chunk = w.q;
       w.next();
       if (w.more()) some_ahead = w.load(ahead);
-      // the largest of the lane's 32 (16) logits, and where it passes `best`
-      float largest = -INFINITY;
-      if (!DISTILL) {
+      uint32_t vm = vector_max<D>(raw[0]);
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-          const float vm = word_value<D>(vector_max<D>(raw[i]));
-          largest = fmaxf(largest, vm);
-          // of equals the first slot keeps the place; the first NaN takes it for good
-          if ((vm > best || best_at < 0 || (vm != vm && best == best)) && (some >> i & 1u)) {
-            best = vm;
-            best_at = slot + 32 * i;
-          }
-        }
-      } else {
-        uint32_t vm = vector_max<D>(raw[0]);
-#pragma unroll
-        for (int i = 1; i < kPerLane; ++i) vm = word_max<D>(vm, vector_max<D>(raw[i]));
-        largest = word_value<D>(vm);
+      for (int i = 1; i < kPerLane; ++i) vm = word_max<D>(vm, vector_max<D>(raw[i]));
+      const float largest = word_value<D>(vm);
+      // the first NaN takes the place for good
+      if (!DISTILL && (((largest > best || best_at < 0) && some) || (largest != largest && best == best))) {
+        best = largest;
+        best_at = chunk;
       }
+      if (!DISTILL && keep) g_largest[(chunk - begin) * 32 + lane] = some ? ordered(largest) : 0;
       if (largest * scale > st.ref + kLag) {
         st.s = s2.x + s2.y;
         st.u = u2.x + u2.y;
@@ -561,83 +741,116 @@ __global__ void __launch_bounds__(kMaxThreads, 2) vocab_forward_kernel(const __g
   if (first && tid == 0) st_g(a.lse + row, lse);
 
   if constexpr (DISTILL) {
-    if (first) {
-      Teacher& t = sh.teacher;
-      const bool taught = load_teacher<D>(t, a.ids, a.teacher, a.K, a.teacher_f32, row, a.x.V, a.x.inv_tau, sh.red);
-      if (warp == 0) {
-        float loss = 0.0f;
-        for (int k = lane; k < a.K; k += 32) {
-          if (t.q[k] != 0.0f) {   // NaN included
-            const float lp = log_prob(logit_at<D>(a.x, row, t.id[k]));
-            loss += t.q[k] * (t.logq[k] - lp);
-          }
-        }
-        loss = warp_sum(loss);
-        if (lane == 0) st_g(a.loss + row, taught ? loss * a.x.tau * a.x.tau : 0.0f);
+    if (first && warp == 0) {
+      const Teacher& t = sh.teacher;
+      const Softmax q(t, a.K, a.x.inv_tau);
+      const float log_s = logf(q.s);
+      float loss = 0.0f;
+      for (int k = lane; k < a.K; k += 32) {
+        if (t.id[k] < 0) continue;
+        const float d = (t.t[k] - q.m) * a.x.inv_tau, p = expf(d) / q.s;
+        if (p != 0.0f) loss += p * ((d - log_s) - log_prob(t.x[k]));   // NaN included
       }
+      loss = warp_sum(loss);
+      if (lane == 0) st_g(a.loss + row, q.taught() ? loss * a.x.tau * a.x.tau : 0.0f);
     }
   } else {
     if (first && tid == 0) {
-      const int64_t target = ld_g(a.targets + row);
-      // no target: 0; a target that is no column: NaN
-      st_g(a.logprob + row, target < 0 ? 0.0f : target >= a.x.V ? NAN : log_prob(logit_at<D>(a.x, row, (int)target)));
+      const int target = sh.teacher.id[0];
+      st_g(a.logprob + row, target == -1 ? 0.0f : target == -2 ? NAN : log_prob(sh.teacher.x[0]));
       if (a.entropy) st_g(a.entropy + row, empty ? 0.0f : kLn2 * (log2_s - st.u / st.s));
     }
     if (a.top > 0) {
-      // the K-th largest of the threads' maxima, by (logit, slot)
-      uint64_t k = best_at < 0 ? 0 : top_key(best, (uint32_t)best_at);
-      k = block_merge(warp_sort(k), sh.lists);
-      const uint64_t mine = sh.lists[0][lane];
-      const uint64_t bound = __shfl_sync(0xFFFFFFFFu, mine, a.top - 1);
-      __syncthreads();
-      // the threads that reach it: each warp reads its share of their slots again
-      uint64_t list = 0;
-      for (int i = warp; i < a.top; i += warps) {
-        const uint64_t key = __shfl_sync(0xFFFFFFFFu, mine, i);
-        if (key == 0) continue;   // fewer threads than K saw a logit
-        const int at = (int)~(uint32_t)key;   // a slot of the thread's: r per kChunk + k kChunk + 32 i + lane
-        const int owner = (at / kChunk - begin) % warps, owner_lane = at & 31;
-        for (int q0 = begin + owner; q0 < end; q0 += 8 * warps) {
-          const int q = q0 + (lane >> 2) * warps;   // eight of its chunks at a time, four slots each
-          uint4 raw = make_uint4(0, 0, 0, 0);
-          int lo = 0, hi = 0, column = 0, slot = 0;
-          if (q < end) {
-            const int r = q / per, j = (q - r * per) * kChunk + 32 * (lane & 3) + owner_lane;
-            const Slot<D> s(sh.rows.first[r], sh.rows.len[r], j);
-            lo = s.lo;
-            hi = s.hi;
-            column = r * a.x.C + s.e0;
-            slot = r * per * kChunk + j;
-            if (!s.empty()) raw = s.load();
+      // A bound that K threads' maxima reach: their K-th largest, cut to 16
+      // bits, found bit by bit.  What reaches it is read again and ranked.
+      const uint32_t mine = best_at < 0 ? 0 : ordered(best);
+      uint32_t bound = 0;
+#pragma unroll 1
+      for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
+        if (__syncthreads_count(mine >= (bound | bit)) >= a.top) bound |= bit;
+      // Fewer than K threads saw more than what a mask leaves (-inf, or the
+      // type's lowest value): only that is read again.
+      const bool masked = bound <= NegInf<D>::lowest;
+      if (masked) bound = NegInf<D>::lowest + 1;
+      if (keep) {
+        uint32_t* again = sh.again[warp];   // chunk << 5 | lane
+        for (int q = begin + warp; q < end;) {
+          int n = 0;
+          for (; q < end; q += warps) {   // a chunk's parts, and the next ones' while they fit
+            const uint32_t largest = g_largest[(q - begin) * 32 + lane];
+            const unsigned hits = __ballot_sync(0xFFFFFFFFu, largest >= bound);
+            if (largest == NegInf<D>::lowest) sh.lowest = 1;
+            if (n + __popc(hits) > 32) break;
+            if (hits >> lane & 1u) again[n + __popc(hits & ((1u << lane) - 1))] = (uint32_t)(q - begin) << 5 | lane;
+            n += __popc(hits);
           }
-          float x[V];
-          unpack<D>(raw, x);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const bool may = e >= lo && e < hi && top_key(x[e], (uint32_t)slot) >= bound;
-            uint32_t hits = __ballot_sync(0xFFFFFFFFu, may);
-            const uint64_t full = top_key(x[e], (uint32_t)(column + e));
-            while (hits) {
-              const int from = __ffs(hits) - 1;
-              hits &= hits - 1;
-              list = warp_insert(list, __shfl_sync(0xFFFFFFFFu, full, from));
+          __syncwarp();
+          for (int i = 0; i < n; i += 8) {   // eight parts of four slots at a time
+            const int k = i + (lane >> 2);
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            int lo = 0, hi = 0, column = 0;
+            if (k < n) {
+              const int at = begin + (int)(again[k] >> 5), r = at / per;
+              const Slot<D> s(sh.rows.first[r], sh.rows.len[r],
+                              (at - r * per) * kChunk + 32 * (lane & 3) + (int)(again[k] & 31u));
+              lo = s.lo;
+              hi = s.hi;
+              column = r * a.x.C + s.e0;
+              if (!s.empty()) raw = s.load();
             }
+            collect<D>(sh, raw, lo, hi, column, bound);
           }
+          __syncwarp();
+        }
+      } else {
+        read_all<D>(sh, per, begin, end, a.x.C, bound);
+      }
+      __syncthreads();
+      bool many = sh.found > kCandidates;
+      if (masked && sh.found < a.top) {
+        // The rest of the K are masked ones, the lowest columns first.  Where
+        // they are all -inf, the part's first K columns hold enough of them;
+        // of the type's lowest value they may.
+        const int had = sh.found;
+        __syncthreads();
+        if (warp == 0) {
+          const int c = column_of<D>(sh.rows, begin, per, chunks, a.x.C, a.x.V) + lane;
+          const bool in = lane < a.top && c < column_of<D>(sh.rows, end, per, chunks, a.x.C, a.x.V);
+          const float x = in ? logit_at<D>(a.x, row, c) : 0.0f;
+          const unsigned fill =
+              __ballot_sync(0xFFFFFFFFu, in && ordered(x) == (sh.lowest ? NegInf<D>::lowest : kOrderedNegInf));
+          if (fill >> lane & 1u) sh.candidates[had + __popc(fill & ((1u << lane) - 1))] = top_key(x, (uint32_t)c);
+          if (lane == 0) sh.found = had + __popc(fill);
+        }
+        __syncthreads();
+        many = sh.lowest && sh.found < a.top;
+      }
+      if (many)
+        top_of_many<D>(sh, best, best_at, a.top, a.x.C, per, begin, end);
+      else
+        rank_candidates(sh, sh.found, a.top);
+      // lists[0]: the K largest, falling
+      if (parts > 1) {
+        // the parts' lists, a warp each, ranked in the first part
+        cluster_sync();
+        uint64_t other = 0;
+        if (first && warp < parts) other = far_u64(in_cta(&sh.lists[0][lane], (uint32_t)warp));
+        cluster_sync();   // after which the other parts may end
+        if (first) {
+          if (warp < parts && lane < a.top) sh.candidates[warp * a.top + lane] = other;
+          __syncthreads();
+          rank_candidates(sh, parts * a.top, a.top);
         }
       }
-      list = block_merge(list, sh.lists);
-      if (parts > 1) {
-        cluster_sync();
-        if (first && warp == 0)
-          for (int i = 1; i < parts; ++i) list = warp_merge(list, far_u64(in_cta(&sh.lists[0][lane], (uint32_t)i)));
-      }
       if (first && warp == 0 && lane < a.top) {
-        st_g(a.top_ids + row * a.top + lane, (int64_t)(uint32_t)~(uint32_t)list);
-        st_g(a.top_logprobs + row * a.top + lane, log_prob(from_ordered((uint32_t)(list >> 32))));
+        const uint64_t key = sh.lists[0][lane];
+        st_g(a.top_ids + row * a.top + lane, (int64_t)(uint32_t)~(uint32_t)key);
+        st_g(a.top_logprobs + row * a.top + lane, log_prob(from_ordered((uint32_t)(key >> 32))));
       }
     }
   }
-  if (parts > 1) cluster_sync();   // no CTA ends while its shared memory may be read
+  // no CTA ends while its shared memory may be read
+  if (parts > 1 && (DISTILL || a.top == 0)) cluster_sync();
 }
 
 // ----------------------------------------------------------------- backward
@@ -646,12 +859,10 @@ struct BackwardShared {
   RowShards rows;
   uintptr_t grad[kMaxRanks];
   Teacher teacher;
-  float fix[kTeacherMax];
-  float red[2];
 };
 
 template <class D, bool DISTILL>
-__global__ void __launch_bounds__(256, 4) vocab_backward_kernel(const __grid_constant__ VocabBackward a, int parts) {
+__global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_constant__ VocabBackward a, int parts) {
   constexpr int V = D::kVec;
   using T = typename D::T;
   __shared__ BackwardShared sh;
@@ -671,21 +882,48 @@ __global__ void __launch_bounds__(256, 4) vocab_backward_kernel(const __grid_con
   Walk<D> w(sh.rows, per, begin + (tid >> 5), end, n >> 5);
   if (w.more()) w.load(raw);
 
-  // dL_j = p_j (A + B log p_j), plus what the target or the teacher adds
-  float A, B = 0.0f, add = 0.0f;
+  // The columns where the target or the teacher adds something are read
+  // before any column is written (the gradient may stand in the logits' place).
+  if (DISTILL) {
+    load_teacher<D>(sh.teacher, a.x, a.ids, a.teacher, a.K, a.teacher_f32, row);
+  } else if (tid == 0) {
+    const int64_t target = ld_g(a.targets + row);
+    const bool some = target >= 0 && target < a.x.V;
+    sh.teacher.id[0] = some ? (int)target : -1;
+    sh.teacher.x[0] = some ? logit_at<D>(a.x, row, (int)target) : 0.0f;
+  }
+  __syncthreads();
+  // dL_j = p_j (A + B log p_j), plus that
+  float A, B = 0.0f;
   const float row_lse = ld_g(a.lse + row);
   // nothing left by the mask: -inf everywhere, or logits so low (the type's
   // lowest value) that lse cannot hold the logarithm of their sum beside them
-  const bool empty = row_lse < kNothingLeft;
-  bool zero = empty;
-  const float lse = empty ? 0.0f : row_lse;
-  int fixes = 0;
+  bool zero = row_lse < kNothingLeft;
+  const float lse = zero ? 0.0f : row_lse;
+  // what is added for tokens tid and tid + n (at least 128 threads, at most 256 tokens)
+  float fixed[2] = {0.0f, 0.0f};
+  bool repeated[2] = {false, false};
   if constexpr (DISTILL) {
-    const bool taught =
-        load_teacher<D>(sh.teacher, a.ids, a.teacher, a.K, a.teacher_f32, row, a.x.V, inv_tau, sh.red);
-    zero = zero || !taught;
+    const Softmax q(sh.teacher, a.K, inv_tau);
+    zero = zero || !q.taught();
     A = zero ? 0.0f : ld_g(a.g + row) * a.x.tau;
-    fixes = zero ? 0 : a.K;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // of equal tokens the first one adds for all
+      const int k = tid + i * n;
+      if (k >= a.K || zero) continue;
+      const int c = sh.teacher.id[k];
+      if (c < 0) continue;
+      bool earlier = false;
+      float sum = 0.0f;
+      for (int o = 0; o < a.K; ++o) {
+        if (sh.teacher.id[o] != c) continue;
+        earlier = earlier || o < k;
+        sum += expf((sh.teacher.t[o] - q.m) * inv_tau) / q.s;
+      }
+      fixed[i] = -A * sum;
+      repeated[i] = earlier;
+    }
   } else {
     const int64_t target = ld_g(a.targets + row);
     const float g = target < 0 ? 0.0f : target >= a.x.V ? NAN : ld_g(a.g + row);
@@ -693,10 +931,7 @@ __global__ void __launch_bounds__(256, 4) vocab_backward_kernel(const __grid_con
     const float H = a.grad_entropy ? ld_g(a.entropy + row) : 0.0f;
     A = -(g + gh * H) * inv_tau;
     B = -gh * inv_tau;
-    add = g * inv_tau;
-    fixes = !zero && target >= 0 && target < a.x.V ? 1 : 0;
-    if (tid == 0) sh.teacher.id[0] = (int)target;
-    __syncthreads();
+    fixed[0] = g * inv_tau;
   }
   if (zero) A = B = 0.0f;
   // binary32 outputs show the exponent's rounding: expf there
@@ -714,35 +949,6 @@ __global__ void __launch_bounds__(256, 4) vocab_backward_kernel(const __grid_con
       c = __ffma2_rn(make_float2(B, B), make_float2(fmaxf(lp.x, kFarBelow), fmaxf(lp.y, kFarBelow)), c);
     return __fmul2_rn(p, c);
   };
-  // the columns with more than that, read before any of them is written (the
-  // gradient may stand in the logits' place); of equal tokens the first one
-  // holds the sum
-  for (int k = tid; k < fixes; k += n) {
-    const int c = sh.teacher.id[k];
-    float v = 0.0f;
-    bool mine = false;
-    if (c >= 0) {
-      const int r = c / a.x.C;
-      const int chunk = r * per + ((int)((sh.rows.first[r] & 15u) / sizeof(T)) + (c - r * a.x.C)) / (V * kChunk);
-      mine = chunk >= begin && chunk < end;
-    }
-    if (mine) {
-      if (DISTILL) {
-        for (int i = 0; i < a.K; ++i) {
-          if (sh.teacher.id[i] == c) {
-            add -= A * sh.teacher.q[i];
-            if (i < k) mine = false;
-          }
-        }
-      }
-      if (mine) v = gradient(make_float2(logit_at<D>(a.x, row, c), 0.0f)).x + add;
-      if (DISTILL) add = 0.0f;
-    }
-    sh.fix[k] = v;
-    sh.teacher.logq[k] = mine ? 1.0f : 0.0f;   // no further use of logq here
-  }
-  __syncthreads();
-
   while (w.more()) {
     const bool whole = w.whole();
     const int r = w.r, j = w.slot(0), len = w.len;
@@ -772,12 +978,19 @@ __global__ void __launch_bounds__(256, 4) vocab_backward_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) raw[i] = ahead[i];
   }
-  if (fixes == 0) return;
   __syncthreads();
-  for (int k = tid; k < fixes; k += n) {
-    if (sh.teacher.logq[k] == 0.0f) continue;
-    const int c = sh.teacher.id[k], q = c / a.x.C;
-    st_g(reinterpret_cast<T*>(sh.grad[q]) + (c - q * a.x.C), narrow<D>(sh.fix[k]));
+  const int tokens = zero ? 0 : DISTILL ? a.K : 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = tid + i * n;
+    if (k >= tokens) continue;
+    const int c = sh.teacher.id[k];
+    if (c < 0 || repeated[i]) continue;
+    const int r = c / a.x.C, e = c - r * a.x.C;
+    const int chunk = r * per + ((int)((sh.rows.first[r] & 15u) / sizeof(T)) + e) / (V * kChunk);
+    if (chunk < begin || chunk >= end) continue;   // another CTA's part of the row
+    st_g(reinterpret_cast<T*>(sh.grad[r]) + e,
+         narrow<D>(gradient(make_float2(sh.teacher.x[k], 0.0f)).x + fixed[i]));
   }
 }
 
@@ -798,16 +1011,23 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
     const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
-    // Many rows: CTAs of 256 threads, so that one's sums and lists overlap
-    // the others' reading.  Few rows: 512 threads, and clusters that split a
+    // Many rows: CTAs of 128 threads, so that one's sums and lists overlap
+    // the others' reading.  Few rows: 256 threads, and clusters that split a
     // row until the SMs are covered, eight chunks a CTA at least.
-    const bool many = a.x.rows >= 2 * (int64_t)sms;
-    const int threads = many ? 256 : chunks >= 16 ? 512 : chunks >= 8 ? 256 : 128;
+    const bool many = a.x.rows >= 4 * (int64_t)sms;
+    const int threads = many || chunks < 8 ? 128 : 256;
     int parts = 1;
     if (!many)
       while (parts < kMaxParts && a.x.rows * parts * 2 <= 2 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
+    const int share = (chunks + parts - 1) / parts;
+    const size_t smem = a.top > 0 && share <= kMostLarge ? (size_t)share * 32 * sizeof(uint32_t) : 0;
     auto kernel = a.ids ? vocab_forward_kernel<D, true> : vocab_forward_kernel<D, false>;
+    if (smem > 32 * 1024) {
+      const cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostLarge * 128);
+      if (e2 != cudaSuccess) return e2;
+    }
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3((unsigned)(a.x.rows * parts));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
@@ -827,9 +1047,9 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
     const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
-    const int threads = chunks >= 8 ? 256 : 128, warps = threads / 32;
+    const int threads = 128, warps = threads / 32;
     // few rows: split each over CTAs until the SMs are covered, a chunk a warp at least
-    int64_t parts = ((int64_t)4 * sms + a.x.rows - 1) / a.x.rows;
+    int64_t parts = ((int64_t)8 * sms + a.x.rows - 1) / a.x.rows;
     const int64_t most = (chunks + warps - 1) / warps;
     if (parts > most) parts = most;
     const unsigned grid = (unsigned)(a.x.rows * parts);
