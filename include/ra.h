@@ -518,6 +518,11 @@ ra_status ra_norm_create(int R, int dim, ra_dtype dtype, ra_dtype residual_dtype
 /* Free the handle after synchronising the device.  NULL is a no-op. */
 ra_status ra_norm_destroy(ra_norm_handle h);
 
+/* RA_OPT_CHECK_POINTERS as for ra_set_option: 1 (default), every call checks
+ * that its buffers are device memory of the handle's device; 0 for a caller
+ * that knows.  Other keys: RA_ERR_INVALID. */
+ra_status ra_norm_set_option(ra_norm_handle h, int key, long long value);
+
 /* S = sum_r in[r];  y = S r1 post_weight, r1 = 1 / sqrt(mean S^2 + eps), or
  * y = S without post_weight;  residual_out = residual + scale * gate * y;
  * out = residual_out r2 weight, r2 = 1 / sqrt(mean residual_out^2 + eps)
@@ -582,6 +587,7 @@ ra_status ra_norm_backward(ra_norm_handle h, const ra_norm_backward_args* args, 
  * temperature > 0 in every call. */
 ra_status ra_vocab_create(int R, size_t V, ra_dtype dtype, float temperature, ra_vocab_handle* out);
 ra_status ra_vocab_destroy(ra_vocab_handle h);
+ra_status ra_vocab_set_option(ra_vocab_handle h, int key, long long value);   /* as ra_norm_set_option */
 
 /* Per row: lse = log sum_j e^{x_j}, x = logits / temperature; logprob =
  * x_target - lse (0 where the target is negative, NaN where it is no column);

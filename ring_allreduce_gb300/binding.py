@@ -129,10 +129,12 @@ EXPORTED = {
     "ra_seed_signals": (_ST, [_P, ctypes.c_uint64, ctypes.c_uint64]),
     "ra_debug_bounds_report": (_ST, [ctypes.POINTER(ctypes.c_ulonglong), ctypes.POINTER(ctypes.c_ulonglong),
                                      ctypes.c_int]),
-    # model operators: the argument blocks are the structures of operators.py
+    # model operators: their calls take the header's argument blocks by address
     "ra_norm_create": (_ST, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                              ctypes.c_float, ctypes.c_float, ctypes.POINTER(_P)]),
     "ra_norm_destroy": (_ST, [_P]),
+    "ra_norm_set_option": (_ST, [_P, ctypes.c_int, ctypes.c_longlong]),
+    "ra_vocab_set_option": (_ST, [_P, ctypes.c_int, ctypes.c_longlong]),
     "ra_norm_forward": (_ST, [_P, _P, _P]),
     "ra_norm_backward": (_ST, [_P, _P, _P]),
     "ra_vocab_create": (_ST, [ctypes.c_int, _SZ, ctypes.c_int, ctypes.c_float, ctypes.POINTER(_P)]),

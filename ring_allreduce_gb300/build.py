@@ -16,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libra_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+TORCH_EXT = "_ra_torch"   # the Python extension that marshals torch tensors for the model operators
+TORCH_EXT_PATH = os.path.join(HERE, TORCH_EXT + ".so")
 DEBUG_BUILD_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(HERE, "libra_gb300_debug.so")
 
@@ -97,6 +100,42 @@ def _stamp(extra):
     return h.hexdigest()
 
 
+def _torch_dir():
+    import importlib.util
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _build_torch_ext(force=False):
+    """Compile _ra_torch.so against the installed torch; its own stamp, since
+    that is what it depends on beside its source."""
+    import importlib.metadata
+    src = os.path.join(CSRC, "ra_torch.cpp")
+    torch_dir = _torch_dir()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), src,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath," + os.path.join(torch_dir, "lib")]
+    h = hashlib.sha256(" ".join(cmd + [sys.version, importlib.metadata.version("torch")]).encode())
+    for f in (src, os.path.join(INCLUDE, "ra.h")):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    stamp_file = os.path.join(BUILD_DIR, "stamp_torch")
+    if not force and os.path.exists(TORCH_EXT_PATH) and os.path.exists(stamp_file):
+        with open(stamp_file) as f:
+            if f.read().strip() == h.hexdigest():
+                return
+    tmp = TORCH_EXT_PATH + ".tmp"
+    res = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"build of {TORCH_EXT}.so failed")
+    os.replace(tmp, TORCH_EXT_PATH)
+    with open(stamp_file, "w") as f:
+        f.write(h.hexdigest())
+
+
 def build(force=False, verbose=None, jobs=None, debug=False):
     """Compile and link the library (the bounds-checked one with debug=True);
     returns its path."""
@@ -108,6 +147,7 @@ def build(force=False, verbose=None, jobs=None, debug=False):
     if not force and os.path.exists(lib_path) and os.path.exists(stamp_file):
         with open(stamp_file) as f:
             if f.read().strip() == stamp:
+                _build_torch_ext()
                 return lib_path
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -120,8 +160,10 @@ def build(force=False, verbose=None, jobs=None, debug=False):
         res = subprocess.run(cmd, capture_output=True, text=True)
         return stem, obj, res
 
-    with ThreadPoolExecutor(max_workers=jobs or min(len(UNITS), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=jobs or min(len(UNITS) + 1, os.cpu_count() or 4)) as ex:
+        ext = ex.submit(_build_torch_ext, force)
         results = list(ex.map(compile_one, UNITS))
+        ext.result()
     failed = [(s, r) for s, _, r in results if r.returncode != 0]
     for s, _, r in results:
         if verbose or r.returncode != 0:

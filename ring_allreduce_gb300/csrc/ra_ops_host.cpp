@@ -18,6 +18,7 @@ struct ra_norm_ctx {
   int R, dim, device, sms;
   ra_dtype dtype, residual_dtype, param_dtype;
   float eps, scale;
+  bool check_pointers = true;
   float* work = nullptr;   // column partials of the weights' gradients, from the first backward call on
 };
 
@@ -25,6 +26,7 @@ struct ra_vocab_ctx {
   int R, V, C, shards, device, sms;
   ra_dtype dtype;
   float tau;
+  bool check_pointers = true;
 };
 
 namespace {
@@ -82,7 +84,8 @@ struct Buffer {
 // The buffers of one call and what has to hold of them.
 class Buffers {
  public:
-  Buffers(int device, size_t rows) : device_(device), rows_(rows) {}
+  Buffers(int device, bool check_pointers, size_t rows)
+      : device_(device), rows_(rows), check_pointers_(check_pointers) {}
 
   // A buffer of rows() rows (or `rows` of them) of `width` elements; `stride`
   // in elements, made the width where there is one row.  The checked stride comes back.
@@ -129,6 +132,7 @@ class Buffers {
             other[sizeof(other) - 1] = 0;
             return record_error(RA_ERR_INVALID, "output %s overlaps %s", label(b_[i].name, b_[i].index), other);
           }
+      if (!check_pointers_) continue;
       cudaPointerAttributes at;
       const void* p = (const void*)b_[i].lo;
       const cudaError_t e = cudaPointerGetAttributes(&at, p);
@@ -192,6 +196,7 @@ class Buffers {
   int count_ = 0;
   int device_;
   size_t rows_;
+  bool check_pointers_;
   char text_[32];
 };
 
@@ -276,7 +281,7 @@ static ra_status norm_forward(ra_norm_handle h, const ra_norm_forward_args* g, c
   size_t in_stride = g->in_stride, out_stride = g->out_stride, res_stride = g->residual_stride,
          res_out_stride = g->residual_out_stride, total_stride = g->total_stride, gate_stride = dim;
   ra::NormForward a{};
-  Buffers buf(h->device, g->rows);
+  Buffers buf(h->device, h->check_pointers, g->rows);
   for (int r = 0; r < h->R; ++r) {
     RA_TRY(buf.add("in", r, g->in[r], b, dim, &in_stride, false));
     a.in[r] = g->in[r];
@@ -339,7 +344,7 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
          ro_stride = g->residual_out_stride, total_stride = g->total_stride, gr_stride = g->grad_residual_stride,
          gate_stride = dim, gg_stride = dim;
   ra::NormBackward a{};
-  Buffers buf(h->device, g->rows);
+  Buffers buf(h->device, h->check_pointers, g->rows);
   for (int r = 0; r < g->grads; ++r) {
     RA_TRY(buf.add("grad_out", r, g->grad_out[r], b, dim, &go_stride, false));
     a.grad_out[r] = g->grad_out[r];
@@ -465,7 +470,7 @@ static ra_status vocab_logprobs(ra_vocab_handle h, const ra_vocab_logprobs_args*
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
   ra::VocabForward a{};
-  Buffers buf(h->device, g->rows);
+  Buffers buf(h->device, h->check_pointers, g->rows);
   RA_TRY(add_shards(h, buf, "shards", g->shards, g->strides, a.x.stride, false, nullptr));
   RA_TRY(buf.flat("targets", g->targets, 8, g->rows, false));
   RA_TRY(buf.flat("logprob", g->logprob, 4, g->rows, true));
@@ -497,7 +502,7 @@ static ra_status vocab_logprobs_backward(ra_vocab_handle h, const ra_vocab_logpr
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
   ra::VocabBackward a{};
-  Buffers buf(h->device, g->rows);
+  Buffers buf(h->device, h->check_pointers, g->rows);
   RA_TRY(add_shards(h, buf, "shards", g->shards, g->strides, a.x.stride, false, nullptr));
   RA_TRY(buf.flat("targets", g->targets, 8, g->rows, false));
   RA_TRY(buf.flat("lse", g->lse, 4, g->rows, false));
@@ -537,7 +542,7 @@ static ra_status vocab_distill(ra_vocab_handle h, const ra_vocab_distill_args* g
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
   ra::VocabForward a{};
-  Buffers buf(h->device, g->rows);
+  Buffers buf(h->device, h->check_pointers, g->rows);
   RA_TRY(add_shards(h, buf, "shards", g->shards, g->strides, a.x.stride, false, nullptr));
   RA_TRY(add_teacher(h, buf, g->rows, g->teacher_k, g->teacher_ids, g->teacher_logits, g->teacher_dtype));
   RA_TRY(buf.flat("loss", g->loss, 4, g->rows, true));
@@ -562,7 +567,7 @@ static ra_status vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distil
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
   ra::VocabBackward a{};
-  Buffers buf(h->device, g->rows);
+  Buffers buf(h->device, h->check_pointers, g->rows);
   RA_TRY(add_shards(h, buf, "shards", g->shards, g->strides, a.x.stride, false, nullptr));
   RA_TRY(add_teacher(h, buf, g->rows, g->teacher_k, g->teacher_ids, g->teacher_logits, g->teacher_dtype));
   RA_TRY(buf.flat("lse", g->lse, 4, g->rows, false));
@@ -579,6 +584,14 @@ static ra_status vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distil
   a.teacher_f32 = g->teacher_dtype == RA_F32;
   const cudaError_t e = ra::launch_vocab_backward(h->dtype, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "distillation's gradient launch");
+}
+
+template <class H> static ra_status set_option(H h, int key, long long value) {
+  if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
+  if (key != RA_OPT_CHECK_POINTERS) return record_error(RA_ERR_INVALID, "option %d: only RA_OPT_CHECK_POINTERS", key);
+  if (value != 0 && value != 1) return record_error(RA_ERR_INVALID, "value %lld: 0 or 1", value);
+  h->check_pointers = value != 0;
+  return RA_OK;
 }
 
 extern "C" {
@@ -601,6 +614,14 @@ ra_status ra_norm_destroy(ra_norm_handle h) {
     delete h;
     return s;
   });
+}
+
+ra_status ra_norm_set_option(ra_norm_handle h, int key, long long value) {
+  return guarded([&] { return set_option(h, key, value); });
+}
+
+ra_status ra_vocab_set_option(ra_vocab_handle h, int key, long long value) {
+  return guarded([&] { return set_option(h, key, value); });
 }
 
 ra_status ra_norm_forward(ra_norm_handle h, const ra_norm_forward_args* args, void* stream) {

@@ -795,13 +795,24 @@ def test_refusals(ops):
 def test_host_memory_is_refused_by_the_library(ops):
     """The C boundary itself: host addresses and NULL come back as RA_ERR_INVALID."""
     import ctypes
-    op = ops.BlockNorm(1, 64, "f32")
-    dev, host = torch.zeros((2, 64), device="cuda"), torch.zeros((2, 64))
-    w = torch.ones(64, device="cuda")
-    for ptr in (host.data_ptr(), None):
-        ins, outs = (ctypes.c_void_p * 1)(ptr), (ctypes.c_void_p * 1)(torch.empty_like(dev).data_ptr())
-        res = torch.empty_like(dev)
-        a = ops._NormForward(rows=2, in_=ctypes.addressof(ins), in_stride=64, residual=dev.data_ptr(),
-                             residual_stride=64, weight=w.data_ptr(), out=ctypes.addressof(outs), out_stride=64, outs=1,
-                             residual_out=res.data_ptr(), residual_out_stride=64)
-        assert ops._lib.ra_norm_forward(op._h, ctypes.addressof(a), None) == 1
+    from ring_allreduce_gb300 import binding
+
+    class Args(ctypes.Structure):   # ra_norm_forward_args
+        _fields_ = [(n, ctypes.c_int if n == "outs" else ctypes.c_size_t if n == "rows" or n.endswith("stride") or
+                     n == "gate_rows" else ctypes.c_void_p) for n in
+                    ("rows in in_stride residual residual_stride weight post_weight gate gate_rows out out_stride outs "
+                     "residual_out residual_out_stride total total_stride rstd").split()]
+
+    lib, h = binding._lib, ctypes.c_void_p()
+    assert lib.ra_norm_create(1, 64, 0, 0, 0, 1e-6, 1.0, ctypes.byref(h)) == 0
+    dev, host, w = torch.zeros((2, 64), device="cuda"), torch.zeros((2, 64)), torch.ones(64, device="cuda")
+    out, res = torch.empty_like(dev), torch.empty_like(dev)
+    for ptr, status in ((host.data_ptr(), 1), (None, 1), (dev.data_ptr(), 0)):
+        ins, outs = (ctypes.c_void_p * 1)(ptr), (ctypes.c_void_p * 1)(out.data_ptr())
+        a = Args(rows=2, residual=dev.data_ptr(), residual_stride=64, in_stride=64, weight=w.data_ptr(),
+                 out=ctypes.addressof(outs), out_stride=64, outs=1, residual_out=res.data_ptr(), residual_out_stride=64)
+        setattr(a, "in", ctypes.addressof(ins))
+        assert lib.ra_norm_forward(h, ctypes.addressof(a), None) == status
+    assert lib.ra_norm_set_option(h, binding.Option.VARIANT, 1) == 1
+    assert lib.ra_norm_set_option(h, binding.Option.CHECK_POINTERS, 2) == 1
+    assert lib.ra_norm_destroy(h) == 0

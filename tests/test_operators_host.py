@@ -1,15 +1,9 @@
-"""The model operators without a GPU: argument structures of the binding match
-the header's, and refusals that come before any device call."""
+"""The model operators without a GPU: the extension's checks of tensors, and
+refusals that come before any device call."""
 
 import ctypes
-import os
-import re
 
 import pytest
-
-from conftest import ROOT
-
-HEADER = os.path.join(ROOT, "include", "ra.h")
 
 
 @pytest.fixture(scope="module")
@@ -20,27 +14,35 @@ def ops():
     return operators
 
 
-def _struct_fields(name):
-    """Field names of a struct of ra.h, in order, with a size and kind each."""
-    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
-    body = re.search(r"typedef struct %s \{(.*?)\} %s;" % (name, name), text, flags=re.S).group(1)
-    out = []
-    for decl in body.split(";"):
-        decl = " ".join(decl.split())
-        if decl:
-            kind = "pointer" if "*" in decl else "size" if decl.startswith("size_t") else "int"
-            out.append((re.search(r"(\w+)$", decl).group(1), kind))
-    return out
-
-
-@pytest.mark.parametrize("name,cls", [
-    ("ra_norm_forward_args", "_NormForward"), ("ra_norm_backward_args", "_NormBackward"),
-    ("ra_vocab_logprobs_args", "_Logprobs"), ("ra_vocab_logprobs_backward_args", "_LogprobsBackward"),
-    ("ra_vocab_distill_args", "_Distill"), ("ra_vocab_distill_backward_args", "_DistillBackward")])
-def test_structures_match_the_header(ops, name, cls):
-    kinds = {ctypes.c_void_p: "pointer", ctypes.c_size_t: "size", ctypes.c_int: "int"}
-    got = [(n.rstrip("_"), kinds[t]) for n, t in getattr(ops, cls)._fields_]
-    assert got == _struct_fields(name)
+def test_extension_refuses_what_is_no_tensor(ops):
+    """The extension's own checks, on CPU tensors and things that are none: ValueError, and nothing is called."""
+    import torch
+    ext = ops._ext
+    x, w = torch.zeros(3, 8), torch.ones(8)
+    norm = (0, 0, 2, 8, 0, 0, 0)      # a NULL handle on device 0
+    for args in ((), norm, ("a",) * 17, norm + ([x, x], x, w, [x], x, None, None, None, None, 0),
+                 norm + ([x, x], 5, w, [x], x, None, None, None, None, 0),
+                 norm + ([x, 7], x, w, [x], x, None, None, None, None, 0),
+                 norm + (3, x, w, [x], x, None, None, None, None, 0)):
+        with pytest.raises(ValueError):
+            ext.norm_forward(*args)
+    # device -1 is the CPU: a fitting call goes through to the library, which refuses the NULL handle
+    cpu = (0, -1, 2, 8, 0, 0, 0)
+    assert ext.norm_forward(*cpu, [x, x], x, w, [x], x, None, None, None, None, 0) == 1
+    assert ext.norm_forward(*cpu, torch.zeros(2, 3, 8), x, w, torch.zeros(1, 3, 8), x, w, None, None, None, 0) == 1
+    for bad in ((torch.zeros(3, 3, 8), x), (torch.zeros(2, 3, 8).double(), x), (torch.zeros(2, 4, 8), x),
+                ([x], x), ([x, x.t().contiguous().t()], x), ([x, torch.zeros(3, 16)[:, :8]], x),
+                ([x, x], x.to_sparse()), ([x, x], torch.zeros(8))):
+        with pytest.raises(ValueError):
+            ext.norm_forward(*cpu, bad[0], bad[1], w, [x], x, None, None, None, None, 0)
+    head = (0, -1, 2, 5, 0)
+    s = [torch.zeros(3, 3), torch.zeros(3, 2)]
+    t, f = torch.zeros(3, dtype=torch.int64), torch.zeros(3)
+    assert ext.logprobs(*head, s, t, f, f, None, None, None, 0) == 1
+    for bad in ((s[:1], t, f, f, None, None, None), (s, t.int(), f, f, None, None, None), (s, t, f, x, None, None, None),
+                (s, t, f, f, None, torch.zeros(3, 2, dtype=torch.int64), None)):
+        with pytest.raises(ValueError):
+            ext.logprobs(*head, *bad, 0)
 
 
 def test_null_handles_and_arguments(ops):
