@@ -17,14 +17,16 @@
 // and every output written once: the kernels are bound by memory traffic, few
 // rows by the latency of two sums over a block.
 //
-// The rows reach the registers through a ring of kDepth slots in shared
-// memory: a slot holds one tensor's part of a row, every warp copies its own
-// columns into its part of it (cp.async) kDepth - 1 slots ahead and reads them
-// back itself, so the copies need no barrier of the block and run on through
-// the sums over it and into the next row.  What binds next is the
+// The rows reach the registers through a ring of kDepth steps in shared
+// memory: a step holds up to kQ tensors' parts of a row, every warp copies its
+// own columns into its part of it (cp.async) kDepth - 1 steps ahead and reads
+// them back itself, so the copies need no barrier of the block and run on
+// through the sums over it and into the next row.  What binds next is the
 // instructions per column: arithmetic is done on pairs of columns
-// (fma.rn.f32x2 and its like), and a warp's columns lie side by side, so that
-// all addresses within a row are constants away from the warp's first one.
+// (fma.rn.f32x2 and its like), a warp's columns lie side by side, so that all
+// addresses within a row are constants away from the warp's first one, and a
+// step of four tensors waits, counts and commits once (one at a time, that
+// took 40 to 60 instructions a tensor beside the 13 a vector needs).
 #pragma once
 
 #include "ra_ops.cuh"
@@ -58,6 +60,9 @@ template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A value that is the same in the whole warp, in a form the compiler can see to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
@@ -77,16 +82,19 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   static constexpr int V = D::kVec;
   static constexpr int kEach = V * VPT, kPairs = kEach / 2;
   static constexpr int kWarpBytes = 32 * kEach * (int)sizeof(T) + (AL ? 0 : 16);   // of a slot
-  // slots of the ring: 8, or what 192 KB hold for MAXT threads
-  static constexpr int kFit = 192 * 1024 / (MAXT / 32 * kWarpBytes);
-  static constexpr int kDepth = kFit < 8 ? kFit : 8;
+  // tensors of a step, and steps of the ring: 128 KB for 1024 threads of one
+  // vector each (the L1 cache keeps the rest, for the weights)
+  static constexpr int kFits = 33 * 1024 / (MAXT / 32 * kWarpBytes);
+  static constexpr int kQ = kFits >= 4 ? 4 : kFits >= 2 ? 2 : 1;
+  static constexpr int kSteps = 198 * 1024 / (MAXT / 32 * kWarpBytes * kQ);
+  static constexpr int kDepth = kSteps < 4 ? kSteps : 4;
 
   int lane, base;   // base: the warp's first column
   int left;         // columns of the row from the thread's first on
   int dim;
   __device__ __forceinline__ explicit Cols(int columns) : dim(columns) {
     lane = threadIdx.x & 31;
-    base = (int)(threadIdx.x >> 5) * 32 * kEach;
+    base = uniform((int)(threadIdx.x >> 5)) * 32 * kEach;
     left = dim - base - (AL ? lane * V : lane);
   }
   // pieces: AL a vector, else a column
@@ -234,53 +242,56 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
 
 extern __shared__ uint4 g_ring[];
 
-// The ring of one warp: the next slot to fill and to read.  Every step
-// commits one group of copies, so kDepth - 1 of them are in flight; the slot
-// that is filled is the one read in the step before.
+// The ring of one warp: the next step to fill and the one being read.  Every
+// step commits one group of copies; a step is filled again as soon as the
+// warp has gone on to the next one.
 template <class C> struct Ring {
-  uint32_t base, fill, take, bytes, end;
+  uint32_t base, fill, now, end;
+  uint32_t part, step;   // bytes of a tensor's slot in a step, and of a step, for the row's warps
   __device__ __forceinline__ explicit Ring(const C& cols) {
     // a CTA's slots one after another; the rows of a CTA of narrow rows apart
-    bytes = (uint32_t)C::kWarpBytes * (blockDim.x >> 5);
-    base = smem_addr(g_ring) + threadIdx.y * (uint32_t)C::kDepth * bytes + (threadIdx.x >> 5) * (uint32_t)C::kWarpBytes;
-    end = base + (uint32_t)C::kDepth * bytes;
-    fill = take = base;
+    part = (uint32_t)C::kWarpBytes * (blockDim.x >> 5);
+    step = part * C::kQ;
+    base = smem_addr(g_ring) + (uint32_t)uniform((int)threadIdx.y) * (uint32_t)C::kDepth * step +
+           (uint32_t)uniform((int)(threadIdx.x >> 5)) * (uint32_t)C::kWarpBytes;
+    end = base + (uint32_t)C::kDepth * step;
     // vectors past the row are never copied: 0 for good
-    for (uint32_t at = base + cols.lane * 16; at < end; at += bytes)
+    for (uint32_t at = base + cols.lane * 16; at < end; at += part)
       for (uint32_t k = 0; k + cols.lane * 16 < C::kWarpBytes; k += 512)
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + k), "r"(0) : "memory");
     __syncwarp();
+    fill = base;
+    now = end - step;    // the first advance() goes on to `base`
   }
-  // Rows: what the kernel reads, in its order; next(slot) starts the next copy
+  // Rows: what the kernel reads, in its order
   template <class Rows> __device__ __forceinline__ void start(Rows& rows) {
     for (int i = 0; i < C::kDepth - 1; ++i) refill(rows);
   }
   template <class Rows> __device__ __forceinline__ void refill(Rows& rows) {
-    rows.next(fill);
+    rows.fetch(fill, part);
     copy_commit();
-    fill += bytes;
-    if (fill == end) fill = base;
+    fill += step;
+    fill = fill == end ? base : fill;
   }
-  // the oldest copy, complete, for the whole warp; and the slot read before it is free
-  __device__ __forceinline__ uint32_t oldest() {
+  // On to the next step, complete for the whole warp; the one before is filled again.
+  template <class Rows> __device__ __forceinline__ void advance(Rows& rows) {
     copy_wait<C::kDepth - 2>();
     __syncwarp();
-    const uint32_t at = take;
-    take += bytes;
-    if (take == end) take = base;
-    return at;
+    now += step;
+    now = now == end ? base : now;
+    refill(rows);
   }
 };
 
-// One tensor's columns of the current row, next in the ring's order; p:
-// offset()'s place.
+// The tensors of a row in their order; the first one opens a step.
 template <class E, class C, class Rows>
-__device__ __forceinline__ void take(const C& cols, Ring<C>& ring, Rows& rows, const char* p,
+__device__ __forceinline__ void take(const C& cols, Ring<C>& ring, Rows& rows, int item, const char* p,
                                      float2 (&x)[C::kPairs]) {
 #pragma unroll
   for (int half = 0; half < C::template halves<E>(); ++half) {
-    cols.template read<E>(ring.oldest(), p, half, x);
-    ring.refill(rows);
+    const int q = (item + half) & (C::kQ - 1);
+    if (q == 0) ring.advance(rows);
+    cols.template read<E>(ring.now + (uint32_t)q * ring.part, p, half, x);
   }
 }
 
@@ -288,13 +299,22 @@ template <class D, class C, class Rows>
 __device__ __forceinline__ void take_sum(const C& cols, Ring<C>& ring, Rows& rows, const void* const* in, int count,
                                          int64_t elements, float2 (&acc)[C::kPairs]) {
   const int64_t at = cols.template offset<D>(elements);
-  take<D>(cols, ring, rows, static_cast<const char*>(in[0]) + at, acc);
-#pragma unroll 2
-  for (int r = 1; r < count; ++r) {
-    float2 x[C::kPairs];
-    take<D>(cols, ring, rows, static_cast<const char*>(in[r]) + at, x);
+#pragma unroll 1
+  for (int r = 0; r < count; r += C::kQ) {
+    ring.advance(rows);
 #pragma unroll
-    for (int i = 0; i < C::kPairs; ++i) acc[i] = add2(acc[i], x[i]);
+    for (int q = 0; q < C::kQ; ++q) {
+      if (r + q >= count) break;
+      float2 x[C::kPairs];
+      cols.template read<D>(ring.now + (uint32_t)q * ring.part, static_cast<const char*>(in[r + q]) + at, 0, x);
+      if (q == 0 && r == 0) {
+#pragma unroll
+        for (int i = 0; i < C::kPairs; ++i) acc[i] = x[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kPairs; ++i) acc[i] = add2(acc[i], x[i]);
+      }
+    }
   }
   cols.clear(acc);
 }
@@ -311,34 +331,37 @@ __device__ __forceinline__ Source source(const C& cols, int64_t row, int64_t str
 
 // What forward reads: every row's R partials, then its residual.
 template <class C, class D, class RD> struct ForwardRows {
-  static constexpr int kHalves = C::template halves<RD>();
   const NormForward& a;
   const C& cols;
   int64_t left;                 // rows from the next one on
   int64_t step;
   Source in, residual;
-  int item;
+  int item, items;
   __device__ __forceinline__ ForwardRows(const NormForward& args, const C& c, int64_t first, int64_t every)
-      : a(args), cols(c), left(args.rows - first), step(every), item(0) {
+      : a(args), cols(c), left(args.rows - first), step(every), item(0), items(args.R + C::template halves<RD>()) {
     in = source<D>(c, first, a.in_stride, a.rows);
     residual = source<RD>(c, first, a.residual_stride, a.rows);
   }
-  __device__ __forceinline__ void next(uint32_t slot) {
+  // the next step's tensors, `part` bytes apart
+  __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
     if (left <= 0) return;
-    if (item < a.R) {
-      const char* lo = static_cast<const char*>(a.in[item]);
-      cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
-      ++item;
-      return;
+#pragma unroll
+    for (int q = 0; q < C::kQ; ++q, slot += part) {
+      const int i = item + q;
+      if (i < a.R) {
+        const char* lo = static_cast<const char*>(a.in[i]);
+        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
+      } else if (i < items) {
+        const char* lo = static_cast<const char*>(a.residual);
+        cols.template fetch<RD>(slot, lo + residual.at, i - a.R, lo, residual.span);
+      }
     }
-    const char* lo = static_cast<const char*>(a.residual);
-    cols.template fetch<RD>(slot, lo + residual.at, item - a.R, lo, residual.span);
-    if (++item == a.R + kHalves) {
-      item = 0;
-      left -= step;
-      in.at += step * a.in_stride * (int64_t)sizeof(typename D::T);
-      residual.at += step * a.residual_stride * (int64_t)sizeof(typename RD::T);
-    }
+    item += C::kQ;
+    if (item < items) return;
+    item = 0;
+    left -= step;
+    in.at += step * a.in_stride * (int64_t)sizeof(typename D::T);
+    residual.at += step * a.residual_stride * (int64_t)sizeof(typename RD::T);
   }
 };
 
@@ -349,7 +372,7 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constan
   __shared__ float red[2][32];
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y), step = (int64_t)gridDim.x * blockDim.y;
   const C cols(a.dim);
   ForwardRows<C, D, RD> rows(a, cols, first, step);
   Ring<C> ring(cols);
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < N; ++i) s[i] = mul2(s[i], w[i]);
     }
-    take<RD>(cols, ring, rows,
+    take<RD>(cols, ring, rows, a.R,
              static_cast<const char*>(a.residual) + cols.template offset<RD>(row * a.residual_stride), h);
     cols.clear(h);
     float2 sq = splat(0.0f);
@@ -436,22 +459,27 @@ template <class C, class D, class RD> struct BackwardRows {
     row.open(a, d);
     in = source<D>(cols, row.row, a.grad_out_stride, a.rows);
   }
-  __device__ __forceinline__ void next(uint32_t slot) {
+  __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
     if (row.u >= d.units) return;
-    if (item < a.grads) {
-      const char* lo = static_cast<const char*>(a.grad_out[item]);
-      cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
-    } else if (item < residuals) {
-      const bool grad = item - a.grads >= kHalves;
-      const char* lo = static_cast<const char*>(grad ? a.grad_residual_out : a.residual_out);
-      const Source s = source<RD>(cols, row.row, grad ? a.grad_residual_out_stride : a.residual_out_stride, a.rows);
-      cols.template fetch<RD>(slot, lo + s.at, (item - a.grads) % kHalves, lo, s.span);
-    } else {
-      const char* lo = static_cast<const char*>(a.total);
-      const Source s = source<D>(cols, row.row, a.total_stride, a.rows);
-      cols.template fetch<D>(slot, lo + s.at, 0, lo, s.span);
+#pragma unroll
+    for (int q = 0; q < C::kQ; ++q, slot += part) {
+      const int i = item + q;
+      if (i < a.grads) {
+        const char* lo = static_cast<const char*>(a.grad_out[i]);
+        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
+      } else if (i < residuals) {
+        const bool grad = i - a.grads >= kHalves;
+        const char* lo = static_cast<const char*>(grad ? a.grad_residual_out : a.residual_out);
+        const Source s = source<RD>(cols, row.row, grad ? a.grad_residual_out_stride : a.residual_out_stride, a.rows);
+        cols.template fetch<RD>(slot, lo + s.at, (i - a.grads) & (kHalves - 1), lo, s.span);
+      } else if (i < items) {
+        const char* lo = static_cast<const char*>(a.total);
+        const Source s = source<D>(cols, row.row, a.total_stride, a.rows);
+        cols.template fetch<D>(slot, lo + s.at, 0, lo, s.span);
+      }
     }
-    if (++item < items) return;
+    item += C::kQ;
+    if (item < items) return;
     item = 0;
     in.at += a.grad_out_stride * (int64_t)sizeof(typename D::T);
     if (++row.row == row.hi) {
@@ -465,11 +493,11 @@ template <class D, class RD, int VPT, bool AL, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_constant__ NormBackward a,
                                                              const __grid_constant__ Deal d) {
   using C = Cols<D, VPT, AL, MAXT>;
-  constexpr int N = C::kPairs;
+  constexpr int N = C::kPairs, kHalves = C::template halves<RD>();
   __shared__ float red[2][32];
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
-  const int64_t worker = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t worker = (int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y);
   const C cols(a.dim);
   BackwardRows<C, D, RD> rows(a, d, cols, worker);
   Ring<C> ring(cols);
@@ -487,7 +515,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
     for (int64_t row = at.row; row < at.hi; ++row) {
       float2 z[N], x[N], w[N];
       take_sum<D>(cols, ring, rows, a.grad_out, a.grads, row * a.grad_out_stride, z);
-      take<RD>(cols, ring, rows,
+      take<RD>(cols, ring, rows, a.grads,
                static_cast<const char*>(a.residual_out) + cols.template offset<RD>(row * a.residual_out_stride), x);
       cols.clear(x);
       const float r2 = ld_g(a.rstd + a.rows + row);
@@ -503,7 +531,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
       }
       const float c2 = row_sum(c.x + c.y, red, turn) * inv_dim;
       if (a.grad_residual_out) {
-        take<RD>(cols, ring, rows,
+        take<RD>(cols, ring, rows, a.grads + kHalves,
                  static_cast<const char*>(a.grad_residual_out) +
                      cols.template offset<RD>(row * a.grad_residual_out_stride), w);
         cols.clear(w);
@@ -515,7 +543,8 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
       for (int i = 0; i < N; ++i) z[i] = fma2(splat(r2), fma2(splat(-c2), x[i], z[i]), w[i]);   // e
       cols.template store<RD>(a.grad_residual, row * a.grad_residual_stride, z);
       if (a.total) {
-        take<D>(cols, ring, rows, static_cast<const char*>(a.total) + cols.template offset<D>(row * a.total_stride), x);
+        take<D>(cols, ring, rows, a.grads + kHalves * (a.grad_residual_out ? 2 : 1),
+                static_cast<const char*>(a.total) + cols.template offset<D>(row * a.total_stride), x);
         cols.clear(x);
       }
       cols.param(a.post_weight, 0, a.param_f32, w);
@@ -607,8 +636,8 @@ template <class D, class F> cudaError_t with_groups(int groups, F&& f) {
 
 // The ring's shared memory, opted in to.
 template <class C, class K> cudaError_t ring_bytes(K kernel, const Shape& s, size_t* bytes) {
-  *bytes = (size_t)C::kDepth * C::kWarpBytes * (s.threads / 32) * s.rows;
-  if (*bytes <= 48 * 1024) return cudaSuccess;
+  *bytes = (size_t)C::kDepth * C::kQ * C::kWarpBytes * (s.threads / 32) * s.rows;
+  if (*bytes <= 40 * 1024) return cudaSuccess;   // 48 KB, the static part included, need no opt-in
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
 }
 
