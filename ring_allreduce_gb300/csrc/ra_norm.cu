@@ -83,15 +83,17 @@ size_t norm_workspace_floats(int dim, int sms) {
   // worker (`parts` > 1 only where there are fewer gate rows than workers)
   size_t most = 0;
   for (int vec : {4, 8}) {
-    const Shape s = backward_shape(dim, vec);
-    const size_t w = (size_t)most_ctas(s, sms) * s.rows;
-    if (w > most) most = w;
+    for (bool deep : {false, true}) {
+      const Shape s = backward_shape(dim, vec, deep);
+      const size_t w = (size_t)most_ctas(s, sms) * s.rows;
+      if (w > most) most = w;
+    }
   }
   return 4 * most * (size_t)dim;
 }
 
 cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormForward& a, int sms, cudaStream_t st) {
-  const Shape s = forward_shape(a.dim, vec_of(dtype));
+  const Shape s = forward_shape(a.dim, vec_of(dtype), a.rows >= 2 * (int64_t)sms);
   const int64_t want = (a.rows + s.rows - 1) / s.rows, most = most_ctas(s, sms);
   const unsigned grid = (unsigned)(want < most ? want : most);
   return with_types(dtype, rdtype, [&](auto d, auto r) {
@@ -100,7 +102,7 @@ cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormF
 }
 
 cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const NormBackward& a, int sms, cudaStream_t st) {
-  const Shape s = backward_shape(a.dim, vec_of(dtype));
+  const Shape s = backward_shape(a.dim, vec_of(dtype), a.rows >= 2 * (int64_t)sms);
   const Deal dl = make_deal(a, s, sms);
   const unsigned grid = (unsigned)(dl.workers / s.rows);
   cudaError_t e = with_types(dtype, rdtype, [&](auto d, auto r) {

@@ -602,9 +602,18 @@ inline Shape spread(int dim, int vec, int groups, int most) {
   return s;
 }
 
-// Forward: one vector a thread up to 1024 threads.
-inline Shape forward_shape(int dim, int vec) {
+// With rows enough for every SM (`deep`) a thread takes up to sixteen columns,
+// so that what a warp does once a row counts for more of them and several
+// CTAs share an SM, one's sums over the block beside another's loads; a few
+// rows are spread over as many threads as there are vectors.
+inline int groups_for(int dim, int vec, bool deep) {
   int groups = 1;
+  while (deep && vec * groups < 16 && dim >= 64 * vec * groups) groups *= 2;
+  return groups;
+}
+
+inline Shape forward_shape(int dim, int vec, bool deep) {
+  int groups = groups_for(dim, vec, deep);
   while (dim > vec * 1024 * groups) groups *= 2;
   return spread(dim, vec, groups, 1024);
 }
@@ -612,8 +621,8 @@ inline Shape forward_shape(int dim, int vec) {
 // Backward keeps three sums per column in registers: at 128 registers a
 // thread, up to 512 threads, sixteen columns fit; wider rows take 1024
 // threads of 64.
-inline Shape backward_shape(int dim, int vec) {
-  int groups = 1;
+inline Shape backward_shape(int dim, int vec, bool deep) {
+  int groups = groups_for(dim, vec, deep);
   while (dim > vec * 512 * groups && vec * groups < 16) groups *= 2;
   return spread(dim, vec, groups, dim > vec * 512 * groups ? 1024 : 512);
 }
@@ -621,7 +630,7 @@ inline Shape backward_shape(int dim, int vec) {
 // CTAs that the SMs hold: 64 K registers each.
 inline int64_t most_ctas(const Shape& s, int sms) {
   const int per_sm = s.most / (s.threads * s.rows);
-  return (int64_t)sms * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm);
+  return (int64_t)sms * (per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm);
 }
 
 // f(IntC<groups per thread>)
