@@ -92,13 +92,20 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   int lane, base;   // base: the warp's first column
   int left;         // columns of the row from the thread's first on
   int dim;
+  bool whole;       // all of the warp's columns are in the row
   __device__ __forceinline__ explicit Cols(int columns) : dim(columns) {
     lane = threadIdx.x & 31;
     base = uniform((int)(threadIdx.x >> 5)) * 32 * kEach;
     left = dim - base - (AL ? lane * V : lane);
+    whole = base + 32 * kEach <= dim;
   }
   // pieces: AL a vector, else a column
   static constexpr int kPieces = AL ? VPT : kEach;
+  // Columns one by one are loaded and stored without a test each by the warps
+  // that are whole, which doubles that code: where there are many rows (sixteen
+  // columns a thread) 4096 x 5001 bf16 took 102 us without and 82 us with it, but
+  // a call of 96 rows, whose time is its code's way into the cache, 10.7 and 12.7.
+  static constexpr bool kTwice = !AL && kEach == 16;
   static constexpr int kStep = AL ? 32 * V : 32;   // columns from a thread's piece to its next
   __device__ __forceinline__ bool has(int k) const { return k * kStep < left; }
   __device__ __forceinline__ int first() const { return base + (AL ? lane * V : lane); }
@@ -113,9 +120,11 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   // columns (AL) or of the warp's columns (else).
   template <class E> static __host__ __device__ constexpr int halves() { return (int)(sizeof(typename E::T) / sizeof(T)); }
 
-  // p: offset()'s place; lo, span: where the buffer begins and its bytes
+  // p: offset()'s place; lo, span: where the buffer begins and its bytes;
+  // inner: 16 bytes on both sides of the row are the buffer's
   template <class E>
-  __device__ __forceinline__ void fetch(uint32_t slot, const char* p, int half, const char* lo, int64_t span) const {
+  __device__ __forceinline__ void fetch(uint32_t slot, const char* p, int half, const char* lo, int64_t span,
+                                        bool inner) const {
     constexpr int es = (int)sizeof(typename E::T);
     if constexpr (AL) {
 #pragma unroll
@@ -129,12 +138,12 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
       const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
       const char* v0 = p - shift;
       const int vectors = (shift + columns * es + 15) >> 4;
-      const bool whole = v0 >= lo && v0 + 16 * vectors <= lo + span;   // nothing outside the buffer is read
+      const bool inside = inner || (v0 >= lo && v0 + 16 * vectors <= lo + span);   // nothing else is read
 #pragma unroll
       for (int i = 0; i < (most * es / 16 + 1 + 31) / 32; ++i) {
         const int v = lane + 32 * i;
         if (v >= vectors) break;
-        if (whole || (v > 0 && v < vectors - 1)) {
+        if (inside || (v > 0 && v < vectors - 1)) {
           copy_async(slot + v * 16, v0 + v * 16);
         } else {
           for (int e = 0; e < 16 / es; ++e) {
@@ -185,17 +194,23 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
 
   // 0 in the columns past the row
   __device__ __forceinline__ void clear(float2 (&x)[kPairs]) const {
-    if constexpr (!AL) {
-      float* f = reinterpret_cast<float*>(x);
+    if (AL || whole) return;
+    float* f = reinterpret_cast<float*>(x);
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) f[e] = has(e) ? f[e] : 0.0f;
-    }
+    for (int e = 0; e < kEach; ++e) f[e] = has(e) ? f[e] : 0.0f;
   }
 
   // Weights and gates, binary32 or of type D, which every row reads; 1 where there are none, 0 past the row.
   template <class E> __device__ __forceinline__ void load_as(const void* from, int64_t elements, float2 (&x)[kPairs]) const {
     const typename E::T* p = static_cast<const typename E::T*>(from) + elements + first();
     float* f = reinterpret_cast<float*>(x);
+    if constexpr (kTwice) {
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) f[k] = widen<E>(ld_g(p + k * kStep));
+        return;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       if constexpr (AL) {
@@ -226,6 +241,13 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   template <class E> __device__ __forceinline__ void store(void* to, int64_t elements, const float2 (&x)[kPairs]) const {
     typename E::T* p = static_cast<typename E::T*>(to) + elements + first();
     const float* f = reinterpret_cast<const float*>(x);
+    if constexpr (kTwice) {
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) st_g(p + k * kStep, narrow<E>(f[k]));
+        return;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       if (!has(k)) continue;
@@ -319,6 +341,11 @@ __device__ __forceinline__ void take_sum(const C& cols, Ring<C>& ring, Rows& row
   cols.clear(acc);
 }
 
+// Rows between others, of 16 bytes at least, have that much of their buffer on both sides.
+template <class D> __device__ __forceinline__ bool inner_row(int64_t row, int64_t rows, int dim) {
+  return row > 0 && row < rows - 1 && dim * (int)sizeof(typename D::T) >= 16;
+}
+
 // One buffer of rows that the ring reads: the warp's (or thread's) place in
 // the next row, and what bounds its reads.
 struct Source {
@@ -345,15 +372,16 @@ template <class C, class D, class RD> struct ForwardRows {
   // the next step's tensors, `part` bytes apart
   __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
     if (left <= 0) return;
+    const bool inner = inner_row<D>(a.rows - left, a.rows, a.dim);
 #pragma unroll
     for (int q = 0; q < C::kQ; ++q, slot += part) {
       const int i = item + q;
       if (i < a.R) {
         const char* lo = static_cast<const char*>(a.in[i]);
-        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
+        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span, inner);
       } else if (i < items) {
         const char* lo = static_cast<const char*>(a.residual);
-        cols.template fetch<RD>(slot, lo + residual.at, i - a.R, lo, residual.span);
+        cols.template fetch<RD>(slot, lo + residual.at, i - a.R, lo, residual.span, inner);
       }
     }
     item += C::kQ;
@@ -461,21 +489,22 @@ template <class C, class D, class RD> struct BackwardRows {
   }
   __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
     if (row.u >= d.units) return;
+    const bool inner = inner_row<D>(row.row, a.rows, a.dim);
 #pragma unroll
     for (int q = 0; q < C::kQ; ++q, slot += part) {
       const int i = item + q;
       if (i < a.grads) {
         const char* lo = static_cast<const char*>(a.grad_out[i]);
-        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span);
+        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span, inner);
       } else if (i < residuals) {
         const bool grad = i - a.grads >= kHalves;
         const char* lo = static_cast<const char*>(grad ? a.grad_residual_out : a.residual_out);
         const Source s = source<RD>(cols, row.row, grad ? a.grad_residual_out_stride : a.residual_out_stride, a.rows);
-        cols.template fetch<RD>(slot, lo + s.at, (i - a.grads) & (kHalves - 1), lo, s.span);
+        cols.template fetch<RD>(slot, lo + s.at, (i - a.grads) & (kHalves - 1), lo, s.span, inner);
       } else if (i < items) {
         const char* lo = static_cast<const char*>(a.total);
         const Source s = source<D>(cols, row.row, a.total_stride, a.rows);
-        cols.template fetch<D>(slot, lo + s.at, 0, lo, s.span);
+        cols.template fetch<D>(slot, lo + s.at, 0, lo, s.span, inner);
       }
     }
     item += C::kQ;
@@ -618,13 +647,17 @@ inline Shape forward_shape(int dim, int vec, bool deep) {
   return spread(dim, vec, groups, 1024);
 }
 
-// Backward keeps three sums per column in registers: at 128 registers a
-// thread, up to 512 threads, sixteen columns fit; wider rows take 1024
-// threads of 64.
+// Backward keeps three sums per column in registers: sixteen columns fit into
+// the 128 registers of 512 threads, eight into the 102 of 640.  Sixteen where
+// an SM then holds two rows, or a row needs them; wider rows take 1024
+// threads of 64 registers.
+constexpr int backward_most(int each, bool wide) { return wide ? 1024 : each == 16 ? 512 : 640; }
+
 inline Shape backward_shape(int dim, int vec, bool deep) {
   int groups = groups_for(dim, vec, deep);
-  while (dim > vec * 512 * groups && vec * groups < 16) groups *= 2;
-  return spread(dim, vec, groups, dim > vec * 512 * groups ? 1024 : 512);
+  if (vec * groups == 16 && dim > 16 * 256) groups /= 2;
+  while (vec * groups < 16 && dim > vec * groups * backward_most(vec * groups, false)) groups *= 2;
+  return spread(dim, vec, groups, backward_most(vec * groups, dim > vec * groups * 512 && vec * groups == 16));
 }
 
 // CTAs that the SMs hold: 64 K registers each.
@@ -689,8 +722,9 @@ cudaError_t run_backward(const Shape& s, bool aligned, const NormBackward& a, co
         return launch(norm_backward_kernel<D, RD, kGroups, false, 1024>, IntC<0>{}, IntC<1024>{});
       }
     }
-    if (aligned) return launch(norm_backward_kernel<D, RD, kGroups, true, 512>, IntC<1>{}, IntC<512>{});
-    return launch(norm_backward_kernel<D, RD, kGroups, false, 512>, IntC<0>{}, IntC<512>{});
+    constexpr int kMost = backward_most(kGroups * D::kVec, false);
+    if (aligned) return launch(norm_backward_kernel<D, RD, kGroups, true, kMost>, IntC<1>{}, IntC<kMost>{});
+    return launch(norm_backward_kernel<D, RD, kGroups, false, kMost>, IntC<0>{}, IntC<kMost>{});
   });
 }
 
