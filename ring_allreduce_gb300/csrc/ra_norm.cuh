@@ -101,6 +101,7 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   }
   // pieces: AL a vector, else a column
   static constexpr int kPieces = AL ? VPT : kEach;
+  static constexpr int kUnroll = AL ? 4 : 1;
   // Columns one by one are loaded and stored without a test each by the warps
   // that are whole, which doubles that code: where there are many rows (sixteen
   // columns a thread) 4096 x 5001 bf16 took 102 us without and 82 us with it, but
@@ -120,12 +121,15 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   // columns (AL) or of the warp's columns (else).
   template <class E> static __host__ __device__ constexpr int halves() { return (int)(sizeof(typename E::T) / sizeof(T)); }
 
-  // p: offset()'s place; lo, span: where the buffer begins and its bytes;
-  // inner: 16 bytes on both sides of the row are the buffer's
+  // One tensor's part of a row into a slot.  lo: where the buffer begins;
+  // elements: its row's offset; inner: 16 bytes on both sides of the row are
+  // the buffer's, else rows and stride say what is.
   template <class E>
-  __device__ __forceinline__ void fetch(uint32_t slot, const char* p, int half, const char* lo, int64_t span,
-                                        bool inner) const {
+  __device__ __forceinline__ void fetch(uint32_t slot, const void* buffer, int64_t elements, int half, bool inner,
+                                        int64_t rows, int64_t stride) const {
     constexpr int es = (int)sizeof(typename E::T);
+    const char* lo = static_cast<const char*>(buffer);
+    const char* p = lo + offset<E>(elements);
     if constexpr (AL) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
@@ -138,23 +142,25 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
       const int shift = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
       const char* v0 = p - shift;
       const int vectors = (shift + columns * es + 15) >> 4;
-      const bool inside = inner || (v0 >= lo && v0 + 16 * vectors <= lo + span);   // nothing else is read
+      bool inside = inner;   // nothing but the buffer is read
+      if (!inner) inside = v0 >= lo && v0 + 16 * vectors <= lo + ((rows - 1) * stride + dim) * es;
 #pragma unroll
       for (int i = 0; i < (most * es / 16 + 1 + 31) / 32; ++i) {
         const int v = lane + 32 * i;
-        if (v >= vectors) break;
-        if (inside || (v > 0 && v < vectors - 1)) {
-          copy_async(slot + v * 16, v0 + v * 16);
-        } else {
-          for (int e = 0; e < 16 / es; ++e) {
-            const int c = (v * 16 - shift) / es + e;   // 16 and shift are multiples of the element's size
-            if (c < 0 || c >= columns) continue;
-            const typename E::T x = ld_g(reinterpret_cast<const typename E::T*>(p) + c);
-            if constexpr (es == 4)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + shift + c * es), "f"(x) : "memory");
-            else
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot + shift + c * es), "h"(x) : "memory");
-          }
+        if (v < vectors && (inside || (v > 0 && v < vectors - 1))) copy_async(slot + v * 16, v0 + v * 16);
+      }
+      if (inside) return;
+      // the vectors at the ends, element by element (16 and shift are multiples of its size)
+      for (int v = lane; v < vectors; v += 32) {
+        if (v > 0 && v < vectors - 1) continue;
+        for (int e = 0; e < 16 / es; ++e) {
+          const int c = (v * 16 - shift) / es + e;
+          if (c < 0 || c >= columns) continue;
+          const typename E::T x = ld_g(reinterpret_cast<const typename E::T*>(p) + c);
+          if constexpr (es == 4)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + shift + c * es), "f"(x) : "memory");
+          else
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot + shift + c * es), "h"(x) : "memory");
         }
       }
     }
@@ -346,50 +352,37 @@ template <class D> __device__ __forceinline__ bool inner_row(int64_t row, int64_
   return row > 0 && row < rows - 1 && dim * (int)sizeof(typename D::T) >= 16;
 }
 
-// One buffer of rows that the ring reads: the warp's (or thread's) place in
-// the next row, and what bounds its reads.
-struct Source {
-  int64_t at, span;
-};
-template <class E, class C>
-__device__ __forceinline__ Source source(const C& cols, int64_t row, int64_t stride, int64_t rows) {
-  return {cols.template offset<E>(row * stride), ((rows - 1) * stride + cols.dim) * (int64_t)sizeof(typename E::T)};
-}
-
-// What forward reads: every row's R partials, then its residual.
+// What forward reads: every row's R partials, then its residual.  (fetch()
+// stands in the kernel once for every place that goes on to the next step, so
+// it is kept short: one copy of the code for all tensors of a type.)
 template <class C, class D, class RD> struct ForwardRows {
+  static constexpr int kHalves = C::template halves<RD>();
   const NormForward& a;
   const C& cols;
-  int64_t left;                 // rows from the next one on
-  int64_t step;
-  Source in, residual;
+  int64_t row, step;
   int item, items;
   __device__ __forceinline__ ForwardRows(const NormForward& args, const C& c, int64_t first, int64_t every)
-      : a(args), cols(c), left(args.rows - first), step(every), item(0), items(args.R + C::template halves<RD>()) {
-    in = source<D>(c, first, a.in_stride, a.rows);
-    residual = source<RD>(c, first, a.residual_stride, a.rows);
-  }
+      : a(args), cols(c), row(first), step(every), item(0), items(args.R + kHalves) {}
   // the next step's tensors, `part` bytes apart
   __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
-    if (left <= 0) return;
-    const bool inner = inner_row<D>(a.rows - left, a.rows, a.dim);
-#pragma unroll
+    if (row >= a.rows) return;
+    const bool inner = inner_row<D>(row, a.rows, a.dim);
+#pragma unroll(C::kUnroll)
     for (int q = 0; q < C::kQ; ++q, slot += part) {
       const int i = item + q;
-      if (i < a.R) {
-        const char* lo = static_cast<const char*>(a.in[i]);
-        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span, inner);
-      } else if (i < items) {
-        const char* lo = static_cast<const char*>(a.residual);
-        cols.template fetch<RD>(slot, lo + residual.at, i - a.R, lo, residual.span, inner);
-      }
+      if (i >= items) break;
+      const bool rank = i < a.R;
+      const void* buffer = rank ? a.in[i] : a.residual;
+      const int64_t stride = rank ? a.in_stride : a.residual_stride;
+      if (kHalves == 1 || rank)
+        cols.template fetch<D>(slot, buffer, row * stride, 0, inner, a.rows, stride);
+      else
+        cols.template fetch<RD>(slot, buffer, row * stride, i - a.R, inner, a.rows, stride);
     }
     item += C::kQ;
     if (item < items) return;
     item = 0;
-    left -= step;
-    in.at += step * a.in_stride * (int64_t)sizeof(typename D::T);
-    residual.at += step * a.residual_stride * (int64_t)sizeof(typename RD::T);
+    row += step;
   }
 };
 
@@ -474,46 +467,46 @@ template <class C, class D, class RD> struct BackwardRows {
   const Deal& d;
   const C& cols;
   Dealt row;
-  Source in;
   int item, residuals, items;
   __device__ __forceinline__ BackwardRows(const NormBackward& args, const Deal& deal, const C& c, int64_t worker)
       : a(args), d(deal), cols(c), item(0) {
     row.u = worker;
-    open();
+    row.open(a, d);
     residuals = a.grads + kHalves * (a.grad_residual_out ? 2 : 1);
     items = residuals + (a.total ? 1 : 0);
-  }
-  __device__ __forceinline__ void open() {
-    row.open(a, d);
-    in = source<D>(cols, row.row, a.grad_out_stride, a.rows);
   }
   __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
     if (row.u >= d.units) return;
     const bool inner = inner_row<D>(row.row, a.rows, a.dim);
-#pragma unroll
+#pragma unroll(C::kUnroll)
     for (int q = 0; q < C::kQ; ++q, slot += part) {
       const int i = item + q;
+      if (i >= items) break;
+      const bool residual = i >= a.grads && i < residuals;
+      const void* buffer;
+      int64_t stride;
       if (i < a.grads) {
-        const char* lo = static_cast<const char*>(a.grad_out[i]);
-        cols.template fetch<D>(slot, lo + in.at, 0, lo, in.span, inner);
-      } else if (i < residuals) {
+        buffer = a.grad_out[i];
+        stride = a.grad_out_stride;
+      } else if (!residual) {
+        buffer = a.total;
+        stride = a.total_stride;
+      } else {
         const bool grad = i - a.grads >= kHalves;
-        const char* lo = static_cast<const char*>(grad ? a.grad_residual_out : a.residual_out);
-        const Source s = source<RD>(cols, row.row, grad ? a.grad_residual_out_stride : a.residual_out_stride, a.rows);
-        cols.template fetch<RD>(slot, lo + s.at, (i - a.grads) & (kHalves - 1), lo, s.span, inner);
-      } else if (i < items) {
-        const char* lo = static_cast<const char*>(a.total);
-        const Source s = source<D>(cols, row.row, a.total_stride, a.rows);
-        cols.template fetch<D>(slot, lo + s.at, 0, lo, s.span, inner);
+        buffer = grad ? a.grad_residual_out : a.residual_out;
+        stride = grad ? a.grad_residual_out_stride : a.residual_out_stride;
       }
+      if (kHalves == 1 || !residual)
+        cols.template fetch<D>(slot, buffer, row.row * stride, 0, inner, a.rows, stride);
+      else
+        cols.template fetch<RD>(slot, buffer, row.row * stride, (i - a.grads) & (kHalves - 1), inner, a.rows, stride);
     }
     item += C::kQ;
     if (item < items) return;
     item = 0;
-    in.at += a.grad_out_stride * (int64_t)sizeof(typename D::T);
     if (++row.row == row.hi) {
       row.u += d.workers;
-      open();
+      row.open(a, d);
     }
   }
 };
