@@ -587,11 +587,11 @@ __device__ __noinline__ void rank_candidates(ForwardShared& sh, int n, int top) 
 // comes after that is beaten by K logits.  What comes before it is read again;
 // what is equal to it lies in its chunk.
 template <class D>
-__device__ __noinline__ void top_of_many(ForwardShared& sh, float best, int best_at, int top, int C, int per,
+__device__ __noinline__ void top_of_many(ForwardShared& sh, uint32_t best, int best_at, int top, int C, int per,
                                          int begin, int end) {
   constexpr int V = D::kVec;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const uint64_t mine = best_at < 0 ? 0 : top_key(best, (uint32_t)best_at);
+  const uint64_t mine = best_at < 0 ? 0 : (uint64_t)best << 32 | (uint32_t)~best_at;
   __syncthreads();
   block_merge(warp_sort(mine), sh.lists);
   const uint64_t bound = sh.lists[0][top - 1];
@@ -672,51 +672,58 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
 
   Stats st{kNoRef, 0.0f, 0.0f};
   float2 s2 = make_float2(0.0f, 0.0f), u2 = make_float2(0.0f, 0.0f);
-  float best = -INFINITY;   // the thread's largest logit, and the first chunk that has it (-1: it saw none)
+  uint32_t best = 0;   // the thread's largest logit, ordered(), and the first chunk that has it (-1: it saw none)
   int best_at = -1;
   const bool keep = !DISTILL && a.top > 0 && share <= kMostLarge;
+  const float2 scale2 = make_float2(scale, scale);
+  auto add = [&](const uint4(&raw)[kPerLane], int chunk, bool some) {
+    uint32_t vm = vector_max<D>(raw[0]);
+#pragma unroll
+    for (int i = 1; i < kPerLane; ++i) vm = word_max<D>(vm, vector_max<D>(raw[i]));
+    const float largest = word_value<D>(vm);
+    if (!DISTILL && a.top > 0) {
+      const uint32_t o = some ? ordered(largest) : 0;
+      best_at = o > best ? chunk : best_at;
+      best = max(o, best);
+      if (keep) g_largest[(chunk - begin) * 32 + lane] = o;
+    }
+    if (largest * scale > st.ref + kLag) {
+      st.s = s2.x + s2.y;
+      st.u = u2.x + u2.y;
+      st.move(largest * scale);
+      s2 = make_float2(st.s, 0.0f);
+      u2 = make_float2(st.u, 0.0f);
+    }
+    const float2 ref2 = make_float2(-st.ref, -st.ref);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      float x[V];
+      unpack<D>(raw[i], x);
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const float2 t = __ffma2_rn(make_float2(x[e], x[e + 1]), scale2, ref2);
+        const float2 p = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+        s2 = __fadd2_rn(s2, p);
+        if (!DISTILL) u2 = __ffma2_rn(make_float2(fmaxf(t.x, kFarBelow), fmaxf(t.y, kFarBelow)), p, u2);
+      }
+    }
+  };
   {
-    uint4 raw[kPerLane], ahead[kPerLane];
+    // one chunk ahead, in two sets of registers by turns
+    uint4 one[kPerLane], two[kPerLane];
     Walk<D> w(sh.rows, per, begin + warp, end, warps);
-    bool some = false, some_ahead = false;
-    if (w.more()) some = w.load(raw);
+    bool some_one = false, some_two = false;
+    if (w.more()) some_one = w.load(one);
     while (w.more()) {
-      const int chunk = w.q;
+      int chunk = w.q;
       w.next();
-      if (w.more()) some_ahead = w.load(ahead);
-      uint32_t vm = vector_max<D>(raw[0]);
-#pragma unroll
-      for (int i = 1; i < kPerLane; ++i) vm = word_max<D>(vm, vector_max<D>(raw[i]));
-      const float largest = word_value<D>(vm);
-      // the first NaN takes the place for good
-      if (!DISTILL && (((largest > best || best_at < 0) && some) || (largest != largest && best == best))) {
-        best = largest;
-        best_at = chunk;
-      }
-      if (!DISTILL && keep) g_largest[(chunk - begin) * 32 + lane] = some ? ordered(largest) : 0;
-      if (largest * scale > st.ref + kLag) {
-        st.s = s2.x + s2.y;
-        st.u = u2.x + u2.y;
-        st.move(largest * scale);
-        s2 = make_float2(st.s, 0.0f);
-        u2 = make_float2(st.u, 0.0f);
-      }
-      const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(-st.ref, -st.ref);
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
-        float x[V];
-        unpack<D>(raw[i], x);
-#pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const float2 t = __ffma2_rn(make_float2(x[e], x[e + 1]), scale2, ref2);
-          const float2 p = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-          s2 = __fadd2_rn(s2, p);
-          if (!DISTILL) u2 = __ffma2_rn(make_float2(fmaxf(t.x, kFarBelow), fmaxf(t.y, kFarBelow)), p, u2);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i) raw[i] = ahead[i];
-      some = some_ahead;
+      if (w.more()) some_two = w.load(two);
+      add(one, chunk, some_one);
+      if (!w.more()) break;
+      chunk = w.q;
+      w.next();
+      if (w.more()) some_one = w.load(one);
+      add(two, chunk, some_two);
     }
   }
   st.s = s2.x + s2.y;
@@ -763,11 +770,10 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
     if (a.top > 0) {
       // A bound that K threads' maxima reach: their K-th largest, cut to 16
       // bits, found bit by bit.  What reaches it is read again and ranked.
-      const uint32_t mine = best_at < 0 ? 0 : ordered(best);
       uint32_t bound = 0;
 #pragma unroll 1
       for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
-        if (__syncthreads_count(mine >= (bound | bit)) >= a.top) bound |= bit;
+        if (__syncthreads_count(best >= (bound | bit)) >= a.top) bound |= bit;
       // Fewer than K threads saw more than what a mask leaves (-inf, or the
       // type's lowest value): only that is read again.
       const bool masked = bound <= NegInf<D>::lowest;
@@ -935,39 +941,41 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   }
   if (zero) A = B = 0.0f;
   // binary32 outputs show the exponent's rounding: expf there
+  constexpr float kUnit = sizeof(T) == 4 ? 1.0f : kLog2e;
+  const float scale = inv_tau * kUnit, ref = -lse * kUnit, slope = B / kUnit;
   auto gradient = [&](float2 x) {
-    const float2 lp = __ffma2_rn(x, make_float2(inv_tau, inv_tau), make_float2(-lse, -lse));
-    float2 p;
-    if (sizeof(T) == 4) {
-      p = make_float2(expf(lp.x), expf(lp.y));
-    } else {
-      const float2 t = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
-      p = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-    }
+    const float2 t = __ffma2_rn(x, make_float2(scale, scale), make_float2(ref, ref));   // log p, in units of kUnit
+    const float2 p = sizeof(T) == 4 ? make_float2(expf(t.x), expf(t.y)) : make_float2(exp2_fast(t.x), exp2_fast(t.y));
     float2 c = make_float2(A, A);
     if (!DISTILL && B != 0.0f)
-      c = __ffma2_rn(make_float2(B, B), make_float2(fmaxf(lp.x, kFarBelow), fmaxf(lp.y, kFarBelow)), c);
+      c = __ffma2_rn(make_float2(slope, slope), make_float2(fmaxf(t.x, kFarBelow), fmaxf(t.y, kFarBelow)), c);
     return __fmul2_rn(p, c);
   };
-  while (w.more()) {
-    const bool whole = w.whole();
-    const int r = w.r, j = w.slot(0), len = w.len;
-    const uintptr_t first = w.first;
-    w.next();
-    if (w.more()) w.load(ahead);
+  auto write = [&](const uint4(&from)[kPerLane], int r, int j, uintptr_t first, int len, bool whole) {
+    T* out = reinterpret_cast<T*>(sh.grad[r]) - (int)((first & 15u) / sizeof(T));   // element 0 of the shard's slot 0
+    const bool vectors = whole && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       float x[V];
-      unpack<D>(raw[i], x);
+      if (zero) {   // whatever the logits are
 #pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const float2 d = gradient(make_float2(x[e], x[e + 1]));
-        x[e] = zero ? 0.0f : d.x;
-        x[e + 1] = zero ? 0.0f : d.y;
+        for (int e = 0; e < V; ++e) x[e] = 0.0f;
+      } else {
+        unpack<D>(from[i], x);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float2 d = gradient(make_float2(x[e], x[e + 1]));
+          x[e] = d.x;
+          x[e + 1] = d.y;
+        }
+      }
+      T* to = out + (int64_t)(j + 32 * i) * V;
+      if (vectors) {
+        st_stream(reinterpret_cast<uint4*>(to), pack<D>(x));
+        continue;
       }
       const Slot<D> s(first, len, j + 32 * i);
-      T* to = reinterpret_cast<T*>(sh.grad[r]) + s.e0;
-      if ((whole || s.whole()) && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+      if (s.whole() && (reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
         st_stream(reinterpret_cast<uint4*>(to), pack<D>(x));
       } else {
 #pragma unroll
@@ -975,6 +983,14 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
           if (e >= s.lo && e < s.hi) st_g(to + e, narrow<D>(x[e]));
       }
     }
+  };
+  while (w.more()) {
+    const bool whole = w.whole();
+    const int r = w.r, j = w.slot(0), len = w.len;
+    const uintptr_t first = w.first;
+    w.next();
+    if (w.more()) w.load(ahead);
+    write(raw, r, j, first, len, whole);
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) raw[i] = ahead[i];
   }
