@@ -26,6 +26,7 @@ using namespace norm;
 constexpr int kJoinSlices = 32;
 __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormBackward a, const __grid_constant__ Deal d) {
   __shared__ float part[kJoinSlices][33];
+  after_predecessor();
   const int c = blockIdx.x * 32 + threadIdx.x;
   const float* from;
   float* to;
@@ -114,8 +115,7 @@ cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const Norm
   e = debug_upload(st);
   if (e != cudaSuccess) return e;
   const dim3 join((a.dim + 31) / 32, 2 + (gates ? (unsigned)a.groups : 0u));
-  norm_join_kernel<<<join, dim3(32, kJoinSlices), 0, st>>>(a, dl);
-  return cudaGetLastError();
+  return launch_after(norm_join_kernel, join, dim3(32, kJoinSlices), 0, st, 1, a, dl);
 }
 
 }  // namespace ra

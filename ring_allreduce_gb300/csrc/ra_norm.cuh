@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constan
   using C = Cols<D, VPT, AL, MAXT>;
   constexpr int N = C::kPairs;
   __shared__ float red[2][32];
+  after_predecessor();
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y), step = (int64_t)gridDim.x * blockDim.y;
@@ -517,6 +518,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
   using C = Cols<D, VPT, AL, MAXT>;
   constexpr int N = C::kPairs, kHalves = C::template halves<RD>();
   __shared__ float red[2][32];
+  after_predecessor();
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
   const int64_t worker = (int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y);
@@ -686,8 +688,7 @@ cudaError_t run_forward(const Shape& s, bool aligned, const NormForward& a, unsi
       size_t smem;
       const cudaError_t e2 = ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, 1024>>(kernel, s, &smem);
       if (e2 != cudaSuccess) return e2;
-      kernel<<<grid, dim3(s.threads, s.rows), smem, st>>>(a);
-      return cudaGetLastError();
+      return launch_after(kernel, dim3(grid), dim3(s.threads, s.rows), smem, st, 1, a);
     };
     if (aligned) return launch(norm_forward_kernel<D, RD, kGroups, true, 1024>, IntC<1>{});
     return launch(norm_forward_kernel<D, RD, kGroups, false, 1024>, IntC<0>{});
@@ -706,8 +707,7 @@ cudaError_t run_backward(const Shape& s, bool aligned, const NormBackward& a, co
       const cudaError_t e2 =
           ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, decltype(most)::value>>(kernel, s, &smem);
       if (e2 != cudaSuccess) return e2;
-      kernel<<<grid, dim3(s.threads, s.rows), smem, st>>>(a, d);
-      return cudaGetLastError();
+      return launch_after(kernel, dim3(grid), dim3(s.threads, s.rows), smem, st, 1, a, d);
     };
     if constexpr (kGroups * D::kVec == 16) {
       if (s.most == 1024) {

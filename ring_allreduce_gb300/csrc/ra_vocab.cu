@@ -649,6 +649,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
                                                                        int parts) {
   constexpr int V = D::kVec;
   __shared__ ForwardShared sh;
+  after_predecessor();
   const int64_t row = blockIdx.x / parts;
   const int part = parts > 1 ? (int)cluster_rank() : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -872,6 +873,7 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   constexpr int V = D::kVec;
   using T = typename D::T;
   __shared__ BackwardShared sh;
+  after_predecessor();
   const int64_t row = blockIdx.x / parts;
   const int part = (int)(blockIdx.x - row * parts);
   const int n = blockDim.x, tid = threadIdx.x;
@@ -1042,18 +1044,7 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
       const cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostLarge * 128);
       if (e2 != cudaSuccess) return e2;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.dynamicSmemBytes = smem;
-    cfg.gridDim = dim3((unsigned)(a.x.rows * parts));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)parts;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = parts > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, a, parts);
+    return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), smem, st, parts, a, parts);
   });
 }
 
@@ -1068,12 +1059,8 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
     int64_t parts = ((int64_t)8 * sms + a.x.rows - 1) / a.x.rows;
     const int64_t most = (chunks + warps - 1) / warps;
     if (parts > most) parts = most;
-    const unsigned grid = (unsigned)(a.x.rows * parts);
-    if (a.ids)
-      vocab_backward_kernel<D, true><<<grid, threads, 0, st>>>(a, (int)parts);
-    else
-      vocab_backward_kernel<D, false><<<grid, threads, 0, st>>>(a, (int)parts);
-    return cudaGetLastError();
+    auto kernel = a.ids ? vocab_backward_kernel<D, true> : vocab_backward_kernel<D, false>;
+    return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), 0, st, 1, a, (int)parts);
   });
 }
 
