@@ -704,6 +704,38 @@ def test_other_stream_graph_and_repeats(ops):
             assert torch.equal(got, want)
 
 
+def test_calls_back_to_back_in_place(ops):
+    """Dependent calls in a stream with nothing between them, each reading what
+    the one before wrote in place: the same bits as with a wait after each."""
+    c = Norm(91, 3, 40, 1024, "bf16", "f32", "f32", True, 2)
+    head = ops.VocabHead(3, 1024, "bf16", temperature=1.5)
+    op, z, h2, total, rstd = c.run(ops, 1)
+    ids, t = torch.arange(40 * 6, device="cuda").view(40, 6) * 4 % 1024, randn(gen(92), 40, 6)
+
+    def chain(wait):
+        parts, residual = [p.clone() for p in c.parts], c.residual.clone()
+        loss, lse, one = (torch.ones(40, device="cuda") for _ in range(3))
+        gh, gw = torch.empty_like(residual), torch.empty(1024, device="cuda")
+        for _ in range(5):
+            op.forward(parts, residual, c.weight, parts, residual, post_weight=c.post, gate=c.gate, total=total,
+                       rstd=rstd)
+            wait()
+            sh = list(parts[0].split(head.widths, 1))
+            head.distill(sh, ids, t, loss, lse)
+            wait()
+            head.distill_backward(sh, ids, t, lse, one, sh)
+            wait()
+            op.backward(parts, residual, residual, rstd, c.weight, parts, gh, gw, post_weight=c.post, gate=c.gate,
+                        total=total)
+            wait()
+        return parts + [residual, loss, lse, gh, gw]
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(chain(lambda: None), want):
+            assert torch.equal(a, b)
+
+
 def test_first_backward_in_a_capture_is_refused(ops):
     from ring_allreduce_gb300 import RAError, Status
     c = Norm(83, 2, 8, 64, "f32", "f32", "f32", True, 1)
