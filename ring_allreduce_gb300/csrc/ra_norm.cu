@@ -44,14 +44,15 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
   if ((blockIdx.y < 2 && !to) || (blockIdx.y >= 2 && !a.grad_gate)) return;
   float s = 0.0f;
   if (c < a.dim) {
+#pragma unroll 4
     for (int64_t i = threadIdx.y; i < count; i += kJoinSlices) s += ld_g(from + i * a.dim + c);
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && c < a.dim) {
-    for (int k = 1; k < kJoinSlices; ++k) s += part[k][threadIdx.x];
-    st_g(to + c, s);
-  }
+  // a warp per column from here on
+  s = warp_sum(part[threadIdx.x][threadIdx.y]);
+  const int mine = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && mine < a.dim) st_g(to + mine, s);
 }
 
 template <class F> cudaError_t with_types(int dtype, int rdtype, F&& f) {

@@ -238,9 +238,10 @@ struct Stats {
   }
 };
 
-__device__ __forceinline__ Stats warp_stats(Stats v) {
+// Joined over `lanes` neighbouring lanes (a power of two), the same in each of them.
+__device__ __forceinline__ Stats warp_stats(Stats v, int lanes) {
 #pragma unroll 1
-  for (int d = 16; d > 0; d >>= 1) {
+  for (int d = lanes >> 1; d > 0; d >>= 1) {
     Stats o;
     o.ref = __shfl_xor_sync(0xFFFFFFFFu, v.ref, d);
     o.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, d);
@@ -439,21 +440,16 @@ constexpr int kMostLarge = 512;   // chunks (64 KB); a CTA with more reads all i
 
 // The block's statistics, the same in every thread (and of every CTA of the row).
 __device__ __noinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts) {
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  st = warp_stats(st);
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;   // four or eight
+  st = warp_stats(st, 32);
   if (lane == 0) sh.warp[threadIdx.x >> 5] = st;
   __syncthreads();
-  st = lane < warps ? sh.warp[lane] : Stats{kNoRef, 0.0f, 0.0f};
-  st = warp_stats(st);
-  if (parts > 1) {
+  st = warp_stats(sh.warp[lane & (warps - 1)], warps);
+  if (parts > 1) {   // a power of two, too
     if (threadIdx.x == 0) sh.block = st;
     cluster_sync();
-    st = Stats{kNoRef, 0.0f, 0.0f};
-    if (lane < parts) {
-      const uint32_t a = in_cta(&sh.block, (uint32_t)lane);
-      st = Stats{far_float(a), far_float(a + 4), far_float(a + 8)};
-    }
-    st = warp_stats(st);
+    const uint32_t a = in_cta(&sh.block, (uint32_t)(lane & (parts - 1)));
+    st = warp_stats(Stats{far_float(a), far_float(a + 4), far_float(a + 8)}, parts);
   }
   return st;
 }
