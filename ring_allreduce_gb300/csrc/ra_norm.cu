@@ -23,9 +23,10 @@ using namespace norm;
 
 // The workers' column partials joined, in worker order: blockIdx.y 0 the pre
 // norm's weight, 1 the post norm's, 2.. the gate rows.
-constexpr int kJoinSlices = 32;
-__global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormBackward a, const __grid_constant__ Deal d) {
-  __shared__ float part[kJoinSlices][33];
+// Warp w of a CTA's 32 columns sums every blockDim.y-th partial, then a column's slices are summed by a warp.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormBackward a,
+                                                         const __grid_constant__ Deal d) {
+  __shared__ float part[32][33];
   after_predecessor();
   const int c = blockIdx.x * 32 + threadIdx.x;
   const float* from;
@@ -45,14 +46,14 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
   float s = 0.0f;
   if (c < a.dim) {
 #pragma unroll 4
-    for (int64_t i = threadIdx.y; i < count; i += kJoinSlices) s += ld_g(from + i * a.dim + c);
+    for (int64_t i = threadIdx.y; i < count; i += blockDim.y) s += ld_g(from + i * a.dim + c);
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  // a warp per column from here on
-  s = warp_sum(part[threadIdx.x][threadIdx.y]);
-  const int mine = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && mine < a.dim) st_g(to + mine, s);
+  for (int k = threadIdx.y; k < 32; k += blockDim.y) {
+    s = warp_sum(threadIdx.x < blockDim.y ? part[threadIdx.x][k] : 0.0f);
+    if (threadIdx.x == 0 && blockIdx.x * 32 + k < a.dim) st_g(to + blockIdx.x * 32 + k, s);
+  }
 }
 
 template <class F> cudaError_t with_types(int dtype, int rdtype, F&& f) {
@@ -116,7 +117,8 @@ cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const Norm
   e = debug_upload(st);
   if (e != cudaSuccess) return e;
   const dim3 join((a.dim + 31) / 32, 2 + (gates ? (unsigned)a.groups : 0u));
-  return launch_after(norm_join_kernel, join, dim3(32, kJoinSlices), 0, st, 1, a, dl);
+  // eight slices where a handful of partials each is left, else as many as there can be
+  return launch_after(norm_join_kernel, join, dim3(32, dl.workers <= 128 ? 8 : 32), 0, st, 1, a, dl);
 }
 
 }  // namespace ra

@@ -101,6 +101,7 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   }
   // pieces: AL a vector, else a column
   static constexpr int kPieces = AL ? VPT : kEach;
+  static constexpr bool kZeroed = AL;
   static constexpr int kUnroll = AL ? 4 : 1;
   // Columns one by one are loaded and stored without a test each by the warps
   // that are whole, which doubles that code: where there are many rows (sixteen
@@ -283,10 +284,11 @@ template <class C> struct Ring {
     base = smem_addr(g_ring) + (uint32_t)uniform((int)threadIdx.y) * (uint32_t)C::kDepth * step +
            (uint32_t)uniform((int)(threadIdx.x >> 5)) * (uint32_t)C::kWarpBytes;
     end = base + (uint32_t)C::kDepth * step;
-    // vectors past the row are never copied: 0 for good
-    for (uint32_t at = base + cols.lane * 16; at < end; at += part)
-      for (uint32_t k = 0; k + cols.lane * 16 < C::kWarpBytes; k += 512)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + k), "r"(0) : "memory");
+    // vectors past the row are never copied: 0 for good (rows anywhere: see clear())
+    if (C::kZeroed && !cols.whole)
+      for (uint32_t at = base + cols.lane * 16; at < end; at += part)
+        for (uint32_t k = 0; k + cols.lane * 16 < C::kWarpBytes; k += 512)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + k), "r"(0) : "memory");
     __syncwarp();
     fill = base;
     now = end - step;    // the first advance() goes on to `base`

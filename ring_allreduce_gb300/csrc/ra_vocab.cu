@@ -420,7 +420,7 @@ struct Softmax {
 
 constexpr int kMaxThreads = 256;
 constexpr int kMaxParts = 8;   // CTAs of a portable cluster
-constexpr int kCandidates = 512;
+constexpr int kCandidates = 256;   // at least 32 of each part of a row
 
 struct ForwardShared {
   RowShards rows;
@@ -654,17 +654,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const int share = (chunks + parts - 1) / parts;
   const int begin = part * share, end = min(chunks, begin + share);
   load_row<D>(a.x, row, sh.rows);
-  if (tid == 0) sh.found = sh.lowest = 0;
-  if (part == 0) {
-    if (DISTILL) {
-      load_teacher<D>(sh.teacher, a.x, a.ids, a.teacher, a.K, a.teacher_f32, row);
-    } else if (tid == 0) {
-      const int64_t target = ld_g(a.targets + row);
-      // no target: -1; one that is no column: -2
-      sh.teacher.id[0] = target < 0 ? -1 : target >= a.x.V ? -2 : 0;
-      sh.teacher.x[0] = target < 0 || target >= a.x.V ? 0.0f : logit_at<D>(a.x, row, (int)target);
-    }
-  }
+  if (!DISTILL && tid == 0) sh.found = sh.lowest = 0;
   __syncthreads();
 
   Stats st{kNoRef, 0.0f, 0.0f};
@@ -711,6 +701,17 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
     Walk<D> w(sh.rows, per, begin + warp, end, warps);
     bool some_one = false, some_two = false;
     if (w.more()) some_one = w.load(one);
+    // what is needed at the end, beside the row's first logits
+    if (part == 0) {
+      if (DISTILL) {
+        load_teacher<D>(sh.teacher, a.x, a.ids, a.teacher, a.K, a.teacher_f32, row);
+      } else if (tid == 0) {
+        const int64_t target = ld_g(a.targets + row);
+        // no target: -1; one that is no column: -2
+        sh.teacher.id[0] = target < 0 ? -1 : target >= a.x.V ? -2 : 0;
+        sh.teacher.x[0] = target < 0 || target >= a.x.V ? 0.0f : logit_at<D>(a.x, row, (int)target);
+      }
+    }
     while (w.more()) {
       int chunk = w.q;
       w.next();
@@ -834,15 +835,28 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
         rank_candidates(sh, sh.found, a.top);
       // lists[0]: the K largest, falling
       if (parts > 1) {
-        // the parts' lists, a warp each, ranked in the first part
+        // the parts' lists, a warp each, joined in the first part
         cluster_sync();
-        uint64_t other = 0;
-        if (first && warp < parts) other = far_u64(in_cta(&sh.lists[0][lane], (uint32_t)warp));
+        uint64_t key = 0;
+        if (first && warp < parts) key = far_u64(in_cta(&sh.lists[0][lane], (uint32_t)warp));
         cluster_sync();   // after which the other parts may end
         if (first) {
-          if (warp < parts && lane < a.top) sh.candidates[warp * a.top + lane] = other;
+          sh.lists[warp][lane] = key;
           __syncthreads();
-          rank_candidates(sh, parts * a.top, a.top);
+          // a key's place is the sum of what every list has before it; all lists searched at once
+          int before[kMaxParts] = {};
+#pragma unroll
+          for (int step = 16; step > 0; step >>= 1)
+#pragma unroll
+            for (int p = 0; p < kMaxParts; ++p) before[p] += sh.lists[p][before[p] + step - 1] > key ? step : 0;
+          int rank = 0;
+#pragma unroll
+          for (int p = 0; p < kMaxParts; ++p) rank += before[p] + (sh.lists[p][before[p]] > key);
+          __syncthreads();
+          if (threadIdx.x < 32) sh.lists[0][lane] = 0;
+          __syncthreads();
+          if (key != 0 && rank < a.top) sh.lists[0][rank] = key;
+          __syncthreads();
         }
       }
       if (first && warp == 0 && lane < a.top) {
@@ -1026,13 +1040,16 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
     using D = decltype(d);
     const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
     // Many rows: CTAs of 128 threads, so that one's sums and lists overlap
-    // the others' reading.  Few rows: 256 threads, and clusters that split a
-    // row until the SMs are covered, eight chunks a CTA at least.
+    // the others' reading (4096 x 131072 bf16, 5 alternatives: 223 us, with 256
+    // threads 250).  Few rows: 256 threads, and clusters that split a row
+    // while less than five sixths of the SMs are covered, eight chunks a CTA
+    // at least (61 x 50021, 20 alternatives: 10.9 us in four parts, 11.4 in
+    // two; 129 x 32003: 11.1 in two, 9.8 in one).
     const bool many = a.x.rows >= 4 * (int64_t)sms;
     const int threads = many || chunks < 8 ? 128 : 256;
     int parts = 1;
     if (!many)
-      while (parts < kMaxParts && a.x.rows * parts * 2 <= 2 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
+      while (parts < kMaxParts && a.x.rows * parts * 6 <= 5 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
     const int share = (chunks + parts - 1) / parts;
     const size_t smem = a.top > 0 && share <= kMostLarge ? (size_t)share * 32 * sizeof(uint32_t) : 0;
     auto kernel = a.ids ? vocab_forward_kernel<D, true> : vocab_forward_kernel<D, false>;
@@ -1051,8 +1068,10 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
     using D = decltype(d);
     const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
     const int threads = 128, warps = threads / 32;
-    // few rows: split each over CTAs until the SMs are covered, a chunk a warp at least
-    int64_t parts = ((int64_t)8 * sms + a.x.rows - 1) / a.x.rows;
+    // Few rows: split each until there are four CTAs of 128 threads to an SM, a
+    // chunk a warp at least.  (Every part reads the teacher's tokens again:
+    // loss and gradient of 129 x 32003 f16 take 12.9 us so, 14.3 with eight.)
+    int64_t parts = ((int64_t)4 * sms + a.x.rows - 1) / a.x.rows;
     const int64_t most = (chunks + warps - 1) / warps;
     if (parts > most) parts = most;
     auto kernel = a.ids ? vocab_backward_kernel<D, true> : vocab_backward_kernel<D, false>;
