@@ -73,6 +73,7 @@ struct VocabRows {
   int64_t rows;
   int shards;                  // shards that hold a column
   int V, C;
+  int slots;                   // 16-byte slots that a shard's columns touch at most
   float tau, inv_tau;
 };
 

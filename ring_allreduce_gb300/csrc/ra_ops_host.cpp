@@ -452,6 +452,10 @@ static ra_status add_shards(const ra_vocab_ctx* h, Buffers& buf, const char* nam
 
 static void set_rows(const ra_vocab_ctx* h, size_t rows, const void* const* shards, ra::VocabRows* x) {
   for (int r = 0; r < h->shards; ++r) x->shard[r] = shards[r];
+  const size_t elem = bytes_of(h->dtype), bytes = (size_t)h->C * elem;
+  uintptr_t bits = 0;
+  for (int r = 0; r < h->shards; ++r) bits |= (uintptr_t)shards[r] | (rows > 1 ? (uintptr_t)x->stride[r] * elem : 0);
+  x->slots = (int)((bytes + 15) / 16 + (bits % 16 ? 1 : 0));   // rows off the 16-byte grid may touch one more
   x->rows = (int64_t)rows;
   x->shards = h->shards;
   x->V = h->V;

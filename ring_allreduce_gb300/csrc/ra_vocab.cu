@@ -17,10 +17,10 @@
 //
 // The top K come out of the same pass without a comparison per element
 // against a list: each thread also keeps the largest logit it saw, and its
-// largest of every chunk in shared memory.  The K-th largest of the threads'
-// maxima bounds the row's K-th largest logit from below; a lane's part of a
-// chunk is read again only where its largest reaches that, and the few logits
-// that do are ranked against each other.
+// largest of every few chunks in shared memory.  The K-th largest of the
+// threads' maxima bounds the row's K-th largest logit from below; a lane's
+// part of a group of chunks is read again only where its largest reaches
+// that, and the few logits that do are ranked against each other.
 //
 // A row's shards are cut into 16-byte slots, and these into chunks of 128, a
 // lane's four 512 bytes apart; a warp takes every warps-th chunk.  A slot that
@@ -110,11 +110,8 @@ __device__ __forceinline__ void load_row(const VocabRows& x, int64_t row, RowSha
 constexpr int kChunk = 128;                  // slots
 constexpr int kPerLane = kChunk / 32;
 
-// Chunks per shard: what C columns can touch at most.
-template <class D> __host__ __device__ __forceinline__ int chunks_per_shard(int C) {
-  const int64_t slots = ((int64_t)C * (int64_t)sizeof(typename D::T) + 15) / 16 + 1;
-  return (int)((slots + kChunk - 1) / kChunk);
-}
+// Chunks per shard.
+__host__ __device__ __forceinline__ int chunks_per_shard(const VocabRows& x) { return (x.slots + kChunk - 1) / kChunk; }
 
 // Where slot j of a shard lies: [lo, hi) are the slot's elements that belong
 // to the shard, e0 the shard's column of its element 0.
@@ -420,6 +417,7 @@ struct Softmax {
 
 constexpr int kMaxThreads = 256;
 constexpr int kMaxParts = 8;   // CTAs of a portable cluster
+constexpr int kGroups = 12;    // a warp's chunks, in this many groups at most
 constexpr int kCandidates = 256;   // at least 32 of each part of a row
 
 struct ForwardShared {
@@ -427,16 +425,13 @@ struct ForwardShared {
   Stats warp[kMaxThreads / 32];
   Stats block;                         // for the other CTAs of the row
   uint64_t lists[kMaxThreads / 32][32];
-  uint32_t again[kMaxThreads / 32][32];   // parts of chunks to read again
+  uint32_t largest[kMaxThreads / 32][kGroups][32];   // the lanes' largest logits of each group of chunks, ordered()
+  uint32_t again[kMaxThreads / 32][32];   // the groups and lanes to read again
   uint64_t candidates[kCandidates];
   int found;
   int lowest;                             // a logit of the type's lowest value was seen
   Teacher teacher;
 };
-
-// Every lane's largest logit of every chunk of the CTA, ordered(): [chunk - begin][lane].
-extern __shared__ uint32_t g_largest[];
-constexpr int kMostLarge = 512;   // chunks (64 KB); a CTA with more reads all its chunks again
 
 // The block's statistics, the same in every thread (and of every CTA of the row).
 __device__ __noinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts) {
@@ -545,23 +540,6 @@ __device__ __forceinline__ int column_of(const RowShards& s, int q, int per, int
   return r * C + min(max(c, 0), s.len[r]);
 }
 
-// The same from all the CTA's chunks.
-template <class D>
-__device__ __noinline__ void read_all(ForwardShared& sh, int per, int begin, int end, int C, uint32_t bound) {
-  for (Walk<D> w(sh.rows, per, begin + (int)(threadIdx.x >> 5), end, blockDim.x >> 5); w.more(); w.next()) {
-    uint4 raw[kPerLane];
-    w.load(raw);
-#pragma unroll 1
-    for (int i = 0; i < kPerLane; ++i) {
-      const Slot<D> s = w.at(i);
-      const uint4 v = i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3];
-      const uint32_t most = s.empty() ? 0 : ordered(word_value<D>(vector_max<D>(v)));
-      if (most == NegInf<D>::lowest) sh.lowest = 1;
-      if (__any_sync(0xFFFFFFFFu, most >= bound && most != 0)) collect<D>(sh, v, s.lo, s.hi, w.r * C + s.e0, bound);
-    }
-  }
-}
-
 // lists[0]: the `top` largest of the candidates (0: none), falling; all keys
 // but 0 differ.
 __device__ __noinline__ void rank_candidates(ForwardShared& sh, int n, int top) {
@@ -650,7 +628,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const int part = parts > 1 ? (int)cluster_rank() : 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const float scale = kLog2e * a.x.inv_tau;
-  const int per = chunks_per_shard<D>(a.x.C), chunks = per * a.x.shards;
+  const int per = chunks_per_shard(a.x), chunks = per * a.x.shards;
   const int share = (chunks + parts - 1) / parts;
   const int begin = part * share, end = min(chunks, begin + share);
   load_row<D>(a.x, row, sh.rows);
@@ -661,7 +639,9 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   float2 s2 = make_float2(0.0f, 0.0f), u2 = make_float2(0.0f, 0.0f);
   uint32_t best = 0;   // the thread's largest logit, ordered(), and the first chunk that has it (-1: it saw none)
   int best_at = -1;
-  const bool keep = !DISTILL && a.top > 0 && share <= kMostLarge;
+  const int of_group = ((share + warps - 1) / warps + kGroups - 1) / kGroups;   // chunks
+  int group = 0, in_group = 0;
+  uint32_t group_best = 0;
   const float2 scale2 = make_float2(scale, scale);
   auto add = [&](const uint4(&raw)[kPerLane], int chunk, bool some) {
     uint32_t vm = vector_max<D>(raw[0]);
@@ -672,7 +652,14 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       const uint32_t o = some ? ordered(largest) : 0;
       best_at = o > best ? chunk : best_at;
       best = max(o, best);
-      if (keep) g_largest[(chunk - begin) * 32 + lane] = o;
+      if (in_group == of_group) {
+        ++group;
+        in_group = 0;
+        group_best = 0;
+      }
+      ++in_group;
+      group_best = max(group_best, o);
+      sh.largest[warp][group][lane] = group_best;
     }
     if (largest * scale > st.ref + kLag) {
       st.s = s2.x + s2.y;
@@ -776,38 +763,39 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       // type's lowest value): only that is read again.
       const bool masked = bound <= NegInf<D>::lowest;
       if (masked) bound = NegInf<D>::lowest + 1;
-      if (keep) {
-        uint32_t* again = sh.again[warp];   // chunk << 5 | lane
-        for (int q = begin + warp; q < end;) {
-          int n = 0;
-          for (; q < end; q += warps) {   // a chunk's parts, and the next ones' while they fit
-            const uint32_t largest = g_largest[(q - begin) * 32 + lane];
-            const unsigned hits = __ballot_sync(0xFFFFFFFFu, largest >= bound);
-            if (largest == NegInf<D>::lowest) sh.lowest = 1;
-            if (n + __popc(hits) > 32) break;
-            if (hits >> lane & 1u) again[n + __popc(hits & ((1u << lane) - 1))] = (uint32_t)(q - begin) << 5 | lane;
-            n += __popc(hits);
-          }
-          __syncwarp();
-          for (int i = 0; i < n; i += 8) {   // eight parts of four slots at a time
-            const int k = i + (lane >> 2);
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            int lo = 0, hi = 0, column = 0;
-            if (k < n) {
-              const int at = begin + (int)(again[k] >> 5), r = at / per;
+      uint32_t* again = sh.again[warp];   // group << 5 | lane
+      const int groups = in_group ? group + 1 : 0;
+      for (int g = 0; g < groups;) {
+        int n = 0;
+        for (; g < groups; ++g) {   // a group's lanes, and the next ones' while they fit
+          const uint32_t largest = sh.largest[warp][g][lane];
+          const unsigned hits = __ballot_sync(0xFFFFFFFFu, largest >= bound);
+          if (largest == NegInf<D>::lowest) sh.lowest = 1;
+          if (n + __popc(hits) > 32) break;
+          if (hits >> lane & 1u) again[n + __popc(hits & ((1u << lane) - 1))] = (uint32_t)g << 5 | lane;
+          n += __popc(hits);
+        }
+        __syncwarp();
+        const int each = 4 * of_group;   // slots
+        for (int i = lane; i - lane < n * each; i += 32) {
+          const int k = i / each, u = i - k * each;
+          uint4 raw = make_uint4(0, 0, 0, 0);
+          int lo = 0, hi = 0, column = 0;
+          if (k < n) {
+            const int q = begin + warp + ((int)(again[k] >> 5) * of_group + (u >> 2)) * warps;
+            if (q < end) {
+              const int r = q / per;
               const Slot<D> s(sh.rows.first[r], sh.rows.len[r],
-                              (at - r * per) * kChunk + 32 * (lane & 3) + (int)(again[k] & 31u));
+                              (q - r * per) * kChunk + 32 * (u & 3) + (int)(again[k] & 31u));
               lo = s.lo;
               hi = s.hi;
               column = r * a.x.C + s.e0;
               if (!s.empty()) raw = s.load();
             }
-            collect<D>(sh, raw, lo, hi, column, bound);
           }
-          __syncwarp();
+          collect<D>(sh, raw, lo, hi, column, bound);
         }
-      } else {
-        read_all<D>(sh, per, begin, end, a.x.C, bound);
+        __syncwarp();
       }
       __syncthreads();
       bool many = sh.found > kCandidates;
@@ -887,7 +875,7 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   const int64_t row = blockIdx.x / parts;
   const int part = (int)(blockIdx.x - row * parts);
   const int n = blockDim.x, tid = threadIdx.x;
-  const int per = chunks_per_shard<D>(a.x.C), chunks = per * a.x.shards;
+  const int per = chunks_per_shard(a.x), chunks = per * a.x.shards;
   const int share = (chunks + parts - 1) / parts;
   const int begin = part * share, end = min(chunks, begin + share);
   const float inv_tau = a.x.inv_tau;
@@ -1038,26 +1026,21 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
   if (e != cudaSuccess) return e;
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
-    const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
-    // Many rows: CTAs of 128 threads, so that one's sums and lists overlap
-    // the others' reading (4096 x 131072 bf16, 5 alternatives: 223 us, with 256
-    // threads 250).  Few rows: 256 threads, and clusters that split a row
+    const int chunks = chunks_per_shard(a.x) * a.x.shards;
+    // Many rows: CTAs of 128 threads at most, eight chunks a warp, so that
+    // one's sums and lists overlap the others' reading.  Few rows: up to 256
+    // threads, a chunk a warp, and clusters that split a row
     // while less than five sixths of the SMs are covered, eight chunks a CTA
     // at least (61 x 50021, 20 alternatives: 10.9 us in four parts, 11.4 in
     // two; 129 x 32003: 11.1 in two, 9.8 in one).
     const bool many = a.x.rows >= 4 * (int64_t)sms;
-    const int threads = many || chunks < 8 ? 128 : 256;
+    int threads = 32;
+    while (threads < (many ? 128 : 256) && threads / 32 * (many ? 8 : 1) < chunks) threads *= 2;
     int parts = 1;
     if (!many)
       while (parts < kMaxParts && a.x.rows * parts * 6 <= 5 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
-    const int share = (chunks + parts - 1) / parts;
-    const size_t smem = a.top > 0 && share <= kMostLarge ? (size_t)share * 32 * sizeof(uint32_t) : 0;
     auto kernel = a.ids ? vocab_forward_kernel<D, true> : vocab_forward_kernel<D, false>;
-    if (smem > 32 * 1024) {
-      const cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostLarge * 128);
-      if (e2 != cudaSuccess) return e2;
-    }
-    return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), smem, st, parts, a, parts);
+    return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), 0, st, parts, a, parts);
   });
 }
 
@@ -1066,7 +1049,7 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
   if (e != cudaSuccess) return e;
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
-    const int chunks = chunks_per_shard<D>(a.x.C) * a.x.shards;
+    const int chunks = chunks_per_shard(a.x) * a.x.shards;
     const int threads = 128, warps = threads / 32;
     // Few rows: split each until there are four CTAs of 128 threads to an SM, a
     // chunk a warp at least.  (Every part reads the teacher's tokens again:

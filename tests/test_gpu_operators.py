@@ -388,6 +388,10 @@ HEADS = [
     (1, 8, 50021, "f32", 1, 1.0, True, 3, 1),
     (7, 400, 1537, "bf16", 3, 1.3, True, 5, 0),
     (2, 700, 8192, "bf16", 0, 1.0, False, 8, 0),
+    (4, 650, 2050, "bf16", 20, 1.0, True, 0, 0),   # rows enough for a warp or two each
+    (1, 615, 300, "f32", 32, 1.0, True, 0, 1),
+    (2, 640, 20000, "f16", 5, 0.7, True, 0, 0),
+    (3, 700, 9000, "bf16", 32, 1.0, False, 0, 0),
 ]
 
 
