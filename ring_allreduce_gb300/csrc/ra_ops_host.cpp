@@ -455,7 +455,9 @@ static void set_rows(const ra_vocab_ctx* h, size_t rows, const void* const* shar
   const size_t elem = bytes_of(h->dtype), bytes = (size_t)h->C * elem;
   uintptr_t bits = 0;
   for (int r = 0; r < h->shards; ++r) bits |= (uintptr_t)shards[r] | (rows > 1 ? (uintptr_t)x->stride[r] * elem : 0);
-  x->slots = (int)((bytes + 15) / 16 + (bits % 16 ? 1 : 0));   // rows off the 16-byte grid may touch one more
+  // rows may start up to `lag` bytes into a 128-byte line
+  const size_t lag = bits % 128 == 0 ? 0 : bits % 64 == 0 ? 64 : bits % 32 == 0 ? 96 : bits % 16 == 0 ? 112 : 126;
+  x->slots = (int)((bytes + lag + 15) / 16);
   x->rows = (int64_t)rows;
   x->shards = h->shards;
   x->V = h->V;

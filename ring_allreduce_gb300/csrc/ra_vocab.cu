@@ -108,6 +108,8 @@ __device__ __forceinline__ void load_row(const VocabRows& x, int64_t row, RowSha
 }
 
 constexpr int kChunk = 128;                  // slots
+constexpr uintptr_t kLine = 127;             // a shard's slots are counted from its first byte's 128-byte line on, so that
+                                             // a warp's accesses are of whole lines
 constexpr int kPerLane = kChunk / 32;
 
 // Chunks per shard.
@@ -119,8 +121,8 @@ template <class D> struct Slot {
   const uint4* at;
   int lo, hi, e0;
   __device__ __forceinline__ Slot(uintptr_t first, int len, int j) {
-    at = reinterpret_cast<const uint4*>(first & ~uintptr_t(15)) + j;
-    e0 = j * D::kVec - (int)((first & 15u) / sizeof(typename D::T));
+    at = reinterpret_cast<const uint4*>(first & ~kLine) + j;
+    e0 = j * D::kVec - (int)((first & kLine) / sizeof(typename D::T));
     lo = max(0, -e0);
     hi = min(D::kVec, len - e0);
   }
@@ -181,7 +183,7 @@ template <class D> struct Walk {
   }
   // every slot is the shard's alone
   __device__ __forceinline__ bool whole() const {
-    const int e0 = k * kChunk * D::kVec - (int)((first & 15u) / sizeof(typename D::T));
+    const int e0 = k * kChunk * D::kVec - (int)((first & kLine) / sizeof(typename D::T));
     return e0 >= 0 && e0 + kChunk * D::kVec <= len;
   }
   __device__ __forceinline__ int slot(int i) const { return k * kChunk + 32 * i + (int)(threadIdx.x & 31); }
@@ -190,7 +192,7 @@ template <class D> struct Walk {
   __device__ __forceinline__ bool load(uint4 (&raw)[kPerLane]) const {
     constexpr uint32_t none = NegInf<D>::word;
     if (whole()) {
-      const uint4* p = reinterpret_cast<const uint4*>(first & ~uintptr_t(15)) + slot(0);
+      const uint4* p = reinterpret_cast<const uint4*>(first & ~kLine) + slot(0);
 #pragma unroll
       for (int i = 0; i < kPerLane; ++i) raw[i] = ld_stream(p + 32 * i);
       return true;
@@ -536,7 +538,7 @@ template <class D>
 __device__ __forceinline__ int column_of(const RowShards& s, int q, int per, int chunks, int C, int V) {
   if (q >= chunks) return V;
   const int r = q / per;
-  const int c = (q - r * per) * kChunk * D::kVec - (int)((s.first[r] & 15u) / sizeof(typename D::T));
+  const int c = (q - r * per) * kChunk * D::kVec - (int)((s.first[r] & kLine) / sizeof(typename D::T));
   return r * C + min(max(c, 0), s.len[r]);
 }
 
@@ -952,7 +954,7 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
     return __fmul2_rn(p, c);
   };
   auto write = [&](const uint4(&from)[kPerLane], int r, int j, uintptr_t first, int len, bool whole) {
-    T* out = reinterpret_cast<T*>(sh.grad[r]) - (int)((first & 15u) / sizeof(T));   // element 0 of the shard's slot 0
+    T* out = reinterpret_cast<T*>(sh.grad[r]) - (int)((first & kLine) / sizeof(T));   // element 0 of the shard's slot 0
     const bool vectors = whole && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
@@ -1003,7 +1005,7 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
     const int c = sh.teacher.id[k];
     if (c < 0 || repeated[i]) continue;
     const int r = c / a.x.C, e = c - r * a.x.C;
-    const int chunk = r * per + ((int)((sh.rows.first[r] & 15u) / sizeof(T)) + e) / (V * kChunk);
+    const int chunk = r * per + ((int)((sh.rows.first[r] & kLine) / sizeof(T)) + e) / (V * kChunk);
     if (chunk < begin || chunk >= end) continue;   // another CTA's part of the row
     st_g(reinterpret_cast<T*>(sh.grad[r]) + e,
          narrow<D>(gradient(make_float2(sh.teacher.x[k], 0.0f)).x + fixed[i]));
