@@ -376,7 +376,7 @@ struct Best {
 // The teacher's tokens: columns (-1 where one is absent: an id that is no
 // column, or a teacher logit of -inf), logits, and the student's logits there.
 struct Teacher {
-  int id[kTeacherMax];
+  alignas(16) int id[kTeacherMax];   // -1, too, up to the next multiple of four past the last
   float t[kTeacherMax];
   float x[kTeacherMax];
 };
@@ -394,6 +394,7 @@ __device__ __forceinline__ void load_teacher(Teacher& to, const VocabRows& rows,
     to.t[k] = t;
     to.x[k] = absent ? 0.0f : logit_at<D>(rows, row, (int)id);
   }
+  if (threadIdx.x < (unsigned)(-K & 3)) to.id[K + threadIdx.x] = -1;
 }
 
 // The softmax's largest logit and sum over the tokens, in every lane of the
@@ -917,17 +918,29 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
     A = zero ? 0.0f : ld_g(a.g + row) * a.x.tau;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      // of equal tokens the first one adds for all
       const int k = tid + i * n;
       if (k >= a.K || zero) continue;
       const int c = sh.teacher.id[k];
       if (c < 0) continue;
+      // Of equal tokens the first one adds for all.  They are rare, so they
+      // are counted four at a time first (6783 x 12160 f16, 85 tokens: the
+      // comparisons one by one were more work than the row).
+      int equal = 0;
+#pragma unroll 4
+      for (int o = 0; o < a.K; o += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(sh.teacher.id + o);
+        equal += (v.x == c) + (v.y == c) + (v.z == c) + (v.w == c);
+      }
       bool earlier = false;
       float sum = 0.0f;
-      for (int o = 0; o < a.K; ++o) {
-        if (sh.teacher.id[o] != c) continue;
-        earlier = earlier || o < k;
-        sum += expf((sh.teacher.t[o] - q.m) * inv_tau) / q.s;
+      if (equal == 1) {
+        sum = expf((sh.teacher.t[k] - q.m) * inv_tau) / q.s;
+      } else {
+        for (int o = 0; o < a.K; ++o) {
+          if (sh.teacher.id[o] != c) continue;
+          earlier = earlier || o < k;
+          sum += expf((sh.teacher.t[o] - q.m) * inv_tau) / q.s;
+        }
       }
       fixed[i] = -A * sum;
       repeated[i] = earlier;
