@@ -151,18 +151,16 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
         if (v < vectors && (inside || (v > 0 && v < vectors - 1))) copy_async(slot + v * 16, v0 + v * 16);
       }
       if (inside) return;
-      // the vectors at the ends, element by element (16 and shift are multiples of its size)
-      for (int v = lane; v < vectors; v += 32) {
-        if (v > 0 && v < vectors - 1) continue;
-        for (int e = 0; e < 16 / es; ++e) {
-          const int c = (v * 16 - shift) / es + e;
-          if (c < 0 || c >= columns) continue;
-          const typename E::T x = ld_g(reinterpret_cast<const typename E::T*>(p) + c);
-          if constexpr (es == 4)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + shift + c * es), "f"(x) : "memory");
-          else
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot + shift + c * es), "h"(x) : "memory");
-        }
+      // the vectors at the ends, an element a lane (16 and shift are multiples of its size)
+      constexpr int each = 16 / es;
+      const int at = lane < each ? lane : lane - each + (vectors - 1) * each;   // in elements from v0
+      const int c = at - shift / es;
+      if (lane < (vectors > 1 ? 2 * each : each) && c >= 0 && c < columns) {
+        const typename E::T x = ld_g(reinterpret_cast<const typename E::T*>(p) + c);
+        if constexpr (es == 4)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + at * es), "f"(x) : "memory");
+        else
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot + at * es), "h"(x) : "memory");
       }
     }
   }
