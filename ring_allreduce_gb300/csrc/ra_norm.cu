@@ -21,7 +21,7 @@ namespace {
 
 using namespace norm;
 
-// The workers' column partials joined, in worker order: blockIdx.y 0 the pre
+// The CTAs' column partials joined, in their order (a gate row's: the units'): blockIdx.y 0 the pre
 // norm's weight, 1 the post norm's, 2.. the gate rows.
 // Warp w of a CTA's 32 columns sums every blockDim.y-th partial, then a column's slices are summed by a warp.
 __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormBackward a,
@@ -33,12 +33,12 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
   float* to;
   int64_t count;
   if (blockIdx.y < 2) {
-    from = a.work + blockIdx.y * d.workers * a.dim;
+    from = a.work + blockIdx.y * d.ctas * a.dim;
     to = blockIdx.y == 0 ? a.grad_weight : a.grad_post_weight;
-    count = d.workers;
+    count = d.ctas;
   } else {
     const int64_t g = blockIdx.y - 2;
-    from = a.work + (2 * d.workers + g * d.parts) * a.dim;
+    from = a.work + (2 * d.ctas + g * d.parts) * a.dim;
     to = a.grad_gate + g * a.dim;
     count = d.parts;
   }
@@ -76,6 +76,7 @@ Deal make_deal(const NormBackward& a, const Shape& s, int sms) {
   d.parts = (a.rows_per_gate + d.rows_per_part - 1) / d.rows_per_part;
   d.units = d.parts * a.groups;
   d.workers = d.units < most ? (d.units + s.rows - 1) / s.rows * s.rows : most;
+  d.ctas = d.workers / s.rows;
   return d;
 }
 
@@ -97,7 +98,7 @@ size_t norm_workspace_floats(int dim, int sms) {
 
 cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormForward& a, int sms, cudaStream_t st) {
   const Shape s = forward_shape(a.dim, vec_of(dtype), a.rows >= 2 * (int64_t)sms);
-  const int64_t want = (a.rows + s.rows - 1) / s.rows, most = most_ctas(s, sms);
+  const int64_t per = s.rows * (aligned ? s.packs : 1), want = (a.rows + per - 1) / per, most = most_ctas(s, sms);
   const unsigned grid = (unsigned)(want < most ? want : most);
   return with_types(dtype, rdtype, [&](auto d, auto r) {
     return run_forward<decltype(d), decltype(r)>(s, aligned, a, grid, st);
@@ -107,7 +108,7 @@ cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormF
 cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const NormBackward& a, int sms, cudaStream_t st) {
   const Shape s = backward_shape(a.dim, vec_of(dtype), a.rows >= 2 * (int64_t)sms);
   const Deal dl = make_deal(a, s, sms);
-  const unsigned grid = (unsigned)(dl.workers / s.rows);
+  const unsigned grid = (unsigned)dl.ctas;
   cudaError_t e = with_types(dtype, rdtype, [&](auto d, auto r) {
     return run_backward<decltype(d), decltype(r)>(s, aligned, a, dl, grid, st);
   });
@@ -118,7 +119,7 @@ cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const Norm
   if (e != cudaSuccess) return e;
   const dim3 join((a.dim + 31) / 32, 2 + (gates ? (unsigned)a.groups : 0u));
   // eight slices where a handful of partials each is left, else as many as there can be
-  return launch_after(norm_join_kernel, join, dim3(32, dl.workers <= 128 ? 8 : 32), 0, st, 1, a, dl);
+  return launch_after(norm_join_kernel, join, dim3(32, dl.ctas <= 128 ? 8 : 32), 0, st, 1, a, dl);
 }
 
 }  // namespace ra

@@ -77,8 +77,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 //        slot holds the 16-byte vectors that cover the warp's columns, shifted
 //        as they lie in memory (bytes of the neighbouring rows come along and
 //        are not used).
-template <class D, int VPT, bool AL, int MAXT> struct Cols {
+//   PK   AL, and a row has sixteen vectors at most: as many rows as fit share a
+//        warp, a power of two of lanes each (65536 x 128 bf16, eight ranks:
+//        36 us forward, 60 backward; a warp a row 62 and 118).
+template <class D, int VPT, bool AL, int MAXT, bool PK = false> struct Cols {
+  static_assert(!PK || (AL && VPT == 1), "rows that share a warp");
   using T = typename D::T;
+  static constexpr bool kPacked = PK;
   static constexpr int V = D::kVec;
   static constexpr int kEach = V * VPT, kPairs = kEach / 2;
   static constexpr int kWarpBytes = 32 * kEach * (int)sizeof(T) + (AL ? 0 : 16);   // of a slot
@@ -89,15 +94,34 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   static constexpr int kSteps = 198 * 1024 / (MAXT / 32 * kWarpBytes * kQ);
   static constexpr int kDepth = kSteps < 4 ? kSteps : 4;
 
-  int lane, base;   // base: the warp's first column
-  int left;         // columns of the row from the thread's first on
+  int lane, base;   // the thread among its row's lanes of the warp; the warp's first column
+  int all, left;    // columns of the row from the thread's first on (left: none where its row is past the end)
   int dim;
+  int lanes, sub, packs;   // a row's lanes, the thread's row among the warp's, and those
   bool whole;       // all of the warp's columns are in the row
-  __device__ __forceinline__ explicit Cols(int columns) : dim(columns) {
+  __device__ __forceinline__ explicit Cols(int columns) : dim(columns), lanes(32), sub(0), packs(1) {
     lane = threadIdx.x & 31;
+    if constexpr (PK) {
+      while (lanes / 2 * V >= dim) lanes /= 2;
+      packs = 32 / lanes;
+      sub = lane / lanes;
+      lane &= lanes - 1;
+    }
     base = uniform((int)(threadIdx.x >> 5)) * 32 * kEach;
-    left = dim - base - (AL ? lane * V : lane);
-    whole = base + 32 * kEach <= dim;
+    all = left = dim - base - (AL ? lane * V : lane);
+    whole = base + lanes * kEach <= dim;
+  }
+  __device__ __forceinline__ void live(bool is) {
+    if constexpr (PK) left = is ? all : 0;
+  }
+  // Sum over the threads of a row, the same value in all of them.
+  __device__ __forceinline__ float sum(float v, float (*red)[32], int& turn) const {
+    if constexpr (PK) {
+      for (int o = lanes / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      return v;
+    } else {
+      return row_sum(v, red, turn);
+    }
   }
   // pieces: AL a vector, else a column
   static constexpr int kPieces = AL ? VPT : kEach;
@@ -110,6 +134,7 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
   static constexpr bool kTwice = !AL && kEach == 16;
   static constexpr int kStep = AL ? 32 * V : 32;   // columns from a thread's piece to its next
   __device__ __forceinline__ bool has(int k) const { return k * kStep < left; }
+  __device__ __forceinline__ uint32_t place() const { return (threadIdx.x & 31u) * 16; }   // in a slot
   __device__ __forceinline__ int first() const { return base + (AL ? lane * V : lane); }
 
   // Buffers are addressed by a row's offset in elements; the warp's (else) or
@@ -134,7 +159,7 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
     if constexpr (AL) {
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
-        if (has(k)) copy_async(slot + k * 512 + lane * 16, p + half * 16 + k * kStep * es);
+        if (k * kStep < all) copy_async(slot + k * 512 + place(), p + half * 16 + k * kStep * es);
     } else {
       constexpr int most = 32 * kEach / halves<E>();   // columns in a slot
       p += half * most * es;
@@ -176,7 +201,7 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
         uint4 w;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(slot + k * 512 + lane * 16)
+                     : "r"(slot + k * 512 + place())
                      : "memory");
         unpack<E>(w, reinterpret_cast<float*>(&x[k * (V / 2)]) + half * (V / n));
       }
@@ -197,12 +222,35 @@ template <class D, int VPT, bool AL, int MAXT> struct Cols {
     }
   }
 
-  // 0 in the columns past the row
+  // 0 in the columns past the row, and in rows past the end
   __device__ __forceinline__ void clear(float2 (&x)[kPairs]) const {
-    if (AL || whole) return;
+    if ((AL && !PK) || (!PK && whole)) return;
     float* f = reinterpret_cast<float*>(x);
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) f[e] = has(e) ? f[e] : 0.0f;
+    for (int e = 0; e < kEach; ++e) f[e] = has(PK ? 0 : e) ? f[e] : 0.0f;
+  }
+
+  // The rows of a warp (PK) summed, for its first one.
+  __device__ __forceinline__ void fold(float2 (&x)[kPairs]) {
+    if constexpr (PK) {
+      for (int o = lanes; o < 32; o *= 2) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+          x[i] = add2(x[i], make_float2(__shfl_xor_sync(0xFFFFFFFFu, x[i].x, o), __shfl_xor_sync(0xFFFFFFFFu, x[i].y, o)));
+      }
+      left = sub == 0 ? all : 0;
+    }
+  }
+
+  // The warp's columns, binary32, into shared memory, `to` the row's first.
+  __device__ __forceinline__ void keep(float* to, const float2 (&x)[kPairs]) const {
+    const float* f = reinterpret_cast<const float*>(x);
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      if (!has(k)) continue;
+#pragma unroll
+      for (int e = 0; e < kEach / kPieces; ++e) to[first() + k * kStep + e] = f[k * (kEach / kPieces) + e];
+    }
   }
 
   // Weights and gates, binary32 or of type D, which every row reads; 1 where there are none, 0 past the row.
@@ -284,8 +332,8 @@ template <class C> struct Ring {
     end = base + (uint32_t)C::kDepth * step;
     // vectors past the row are never copied: 0 for good (rows anywhere: see clear())
     if (C::kZeroed && !cols.whole)
-      for (uint32_t at = base + cols.lane * 16; at < end; at += part)
-        for (uint32_t k = 0; k + cols.lane * 16 < C::kWarpBytes; k += 512)
+      for (uint32_t at = base + cols.place(); at < end; at += part)
+        for (uint32_t k = 0; k + cols.place() < C::kWarpBytes; k += 512)
           asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + k), "r"(0) : "memory");
     __syncwarp();
     fill = base;
@@ -365,19 +413,20 @@ template <class C, class D, class RD> struct ForwardRows {
       : a(args), cols(c), row(first), step(every), item(0), items(args.R + kHalves) {}
   // the next step's tensors, `part` bytes apart
   __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
+    const int64_t mine = row + (C::kPacked ? cols.sub : 0);
     if (row >= a.rows) return;
     const bool inner = inner_row<D>(row, a.rows, a.dim);
 #pragma unroll(C::kUnroll)
     for (int q = 0; q < C::kQ; ++q, slot += part) {
       const int i = item + q;
-      if (i >= items) break;
+      if (i >= items || (C::kPacked && mine >= a.rows)) break;
       const bool rank = i < a.R;
       const void* buffer = rank ? a.in[i] : a.residual;
       const int64_t stride = rank ? a.in_stride : a.residual_stride;
       if (kHalves == 1 || rank)
-        cols.template fetch<D>(slot, buffer, row * stride, 0, inner, a.rows, stride);
+        cols.template fetch<D>(slot, buffer, mine * stride, 0, inner, a.rows, stride);
       else
-        cols.template fetch<RD>(slot, buffer, row * stride, i - a.R, inner, a.rows, stride);
+        cols.template fetch<RD>(slot, buffer, mine * stride, i - a.R, inner, a.rows, stride);
     }
     item += C::kQ;
     if (item < items) return;
@@ -386,20 +435,23 @@ template <class C, class D, class RD> struct ForwardRows {
   }
 };
 
-template <class D, class RD, int VPT, bool AL, int MAXT>
+template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constant__ NormForward a) {
-  using C = Cols<D, VPT, AL, MAXT>;
+  using C = Cols<D, VPT, AL, MAXT, PK>;
   constexpr int N = C::kPairs;
   __shared__ float red[2][32];
   after_predecessor();
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y), step = (int64_t)gridDim.x * blockDim.y;
-  const C cols(a.dim);
+  C cols(a.dim);
+  const int64_t first = ((int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y)) * cols.packs,
+                step = (int64_t)gridDim.x * blockDim.y * cols.packs;
   ForwardRows<C, D, RD> rows(a, cols, first, step);
   Ring<C> ring(cols);
   ring.start(rows);
-  for (int64_t row = first; row < a.rows; row += step) {
+  for (int64_t warp_row = first; warp_row < a.rows; warp_row += step) {
+    const int64_t row = warp_row + (PK ? cols.sub : 0);
+    cols.live(row < a.rows);
     float2 s[N], h[N], w[N];
     take_sum<D>(cols, ring, rows, a.in, a.R, row * a.in_stride, s);
     if (a.total) cols.template store<D>(a.total, row * a.total_stride, s);
@@ -408,7 +460,7 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constan
       float2 sq = splat(0.0f);
 #pragma unroll
       for (int i = 0; i < N; ++i) sq = fma2(s[i], s[i], sq);
-      f = r1 = rsqrtf(row_sum(sq.x + sq.y, red, turn) * inv_dim + a.eps);
+      f = r1 = rsqrtf(cols.sum(sq.x + sq.y, red, turn) * inv_dim + a.eps);
       cols.param(a.post_weight, 0, a.param_f32, w);
 #pragma unroll
       for (int i = 0; i < N; ++i) s[i] = mul2(mul2(s[i], splat(f)), w[i]);
@@ -428,12 +480,12 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constan
       sq = fma2(h[i], h[i], sq);
     }
     cols.template store<RD>(a.residual_out, row * a.residual_out_stride, h);
-    const float r2 = rsqrtf(row_sum(sq.x + sq.y, red, turn) * inv_dim + a.eps);
+    const float r2 = rsqrtf(cols.sum(sq.x + sq.y, red, turn) * inv_dim + a.eps);
     cols.param(a.weight, 0, a.param_f32, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) h[i] = mul2(mul2(h[i], splat(r2)), w[i]);
     for (int q = 0; q < a.outs; ++q) cols.template store<D>(a.out[q], row * a.out_stride, h);
-    if (a.rstd && threadIdx.x == 0) {
+    if (a.rstd && (PK ? cols.lane == 0 && cols.left > 0 : threadIdx.x == 0)) {
       st_g(a.rstd + row, r1);
       st_g(a.rstd + a.rows + row, r2);
     }
@@ -445,7 +497,7 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constan
 // taking unit w, w + workers, ...
 struct Deal {
   int64_t units, parts, rows_per_part;
-  int64_t workers;
+  int64_t workers, ctas;
 };
 
 // The rows of one worker, in order.
@@ -478,11 +530,12 @@ template <class C, class D, class RD> struct BackwardRows {
   }
   __device__ __forceinline__ void fetch(uint32_t slot, uint32_t part) {
     if (row.u >= d.units) return;
+    const int64_t mine = row.row + (C::kPacked ? cols.sub : 0);
     const bool inner = inner_row<D>(row.row, a.rows, a.dim);
 #pragma unroll(C::kUnroll)
     for (int q = 0; q < C::kQ; ++q, slot += part) {
       const int i = item + q;
-      if (i >= items) break;
+      if (i >= items || (C::kPacked && mine >= row.hi)) break;
       const bool residual = i >= a.grads && i < residuals;
       const void* buffer;
       int64_t stride;
@@ -498,31 +551,32 @@ template <class C, class D, class RD> struct BackwardRows {
         stride = grad ? a.grad_residual_out_stride : a.residual_out_stride;
       }
       if (kHalves == 1 || !residual)
-        cols.template fetch<D>(slot, buffer, row.row * stride, 0, inner, a.rows, stride);
+        cols.template fetch<D>(slot, buffer, mine * stride, 0, inner, a.rows, stride);
       else
-        cols.template fetch<RD>(slot, buffer, row.row * stride, (i - a.grads) & (kHalves - 1), inner, a.rows, stride);
+        cols.template fetch<RD>(slot, buffer, mine * stride, (i - a.grads) & (kHalves - 1), inner, a.rows, stride);
     }
     item += C::kQ;
     if (item < items) return;
     item = 0;
-    if (++row.row == row.hi) {
+    row.row += cols.packs;
+    if (row.row >= row.hi) {
       row.u += d.workers;
       row.open(a, d);
     }
   }
 };
 
-template <class D, class RD, int VPT, bool AL, int MAXT>
+template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_constant__ NormBackward a,
                                                              const __grid_constant__ Deal d) {
-  using C = Cols<D, VPT, AL, MAXT>;
+  using C = Cols<D, VPT, AL, MAXT, PK>;
   constexpr int N = C::kPairs, kHalves = C::template halves<RD>();
   __shared__ float red[2][32];
   after_predecessor();
   int turn = 0;
   const float inv_dim = 1.0f / (float)a.dim;
   const int64_t worker = (int64_t)blockIdx.x * blockDim.y + uniform((int)threadIdx.y);
-  const C cols(a.dim);
+  C cols(a.dim);
   BackwardRows<C, D, RD> rows(a, d, cols, worker);
   Ring<C> ring(cols);
   ring.start(rows);
@@ -536,14 +590,17 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
     float2 dg[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) dg[i] = splat(0.0f);
-    for (int64_t row = at.row; row < at.hi; ++row) {
+    for (int64_t warp_row = at.row; warp_row < at.hi; warp_row += cols.packs) {
+      const int64_t row = warp_row + (PK ? cols.sub : 0);
+      const bool live = !PK || row < at.hi;
+      cols.live(live);
       float2 z[N], x[N], w[N];
       take_sum<D>(cols, ring, rows, a.grad_out, a.grads, row * a.grad_out_stride, z);
       take<RD>(cols, ring, rows, a.grads,
                static_cast<const char*>(a.residual_out) + cols.template offset<RD>(row * a.residual_out_stride), x);
       cols.clear(x);
-      const float r2 = ld_g(a.rstd + a.rows + row);
-      const float r1 = a.post_weight ? ld_g(a.rstd + row) : 1.0f;
+      const float r2 = live ? ld_g(a.rstd + a.rows + row) : 0.0f;
+      const float r1 = !a.post_weight ? 1.0f : live ? ld_g(a.rstd + row) : 0.0f;
       cols.param(a.weight, 0, a.param_f32, w);
       float2 c = splat(0.0f);
 #pragma unroll
@@ -553,7 +610,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
         z[i] = mul2(z[i], w[i]);
         c = fma2(z[i], x[i], c);
       }
-      const float c2 = row_sum(c.x + c.y, red, turn) * inv_dim;
+      const float c2 = cols.sum(c.x + c.y, red, turn) * inv_dim;
       if (a.grad_residual_out) {
         take<RD>(cols, ring, rows, a.grads + kHalves,
                  static_cast<const char*>(a.grad_residual_out) +
@@ -593,7 +650,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
         c = fma2(z[i], x[i], c);
       }
       if (a.post_weight) {
-        const float c1 = row_sum(c.x + c.y, red, turn) * inv_dim;
+        const float c1 = cols.sum(c.x + c.y, red, turn) * inv_dim;
 #pragma unroll
         for (int i = 0; i < N; ++i) z[i] = mul2(splat(r1), fma2(splat(-c1), x[i], z[i]));
       }
@@ -603,17 +660,39 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_consta
     if (a.grad_gate) {
 #pragma unroll
       for (int i = 0; i < N; ++i) dg[i] = mul2(dg[i], splat(a.scale));
-      cols.template store<DF32>(d.parts == 1 ? a.grad_gate : a.work + 2 * d.workers * a.dim, at.u * a.dim, dg);
+      cols.fold(dg);
+      cols.template store<DF32>(d.parts == 1 ? a.grad_gate : a.work + 2 * d.ctas * a.dim, at.u * a.dim, dg);
     }
   }
-  if (a.grad_weight) cols.template store<DF32>(a.work, worker * a.dim, dw);
-  if (a.grad_post_weight) cols.template store<DF32>(a.work, (d.workers + worker) * a.dim, dp);
+  cols.fold(dw);
+  cols.fold(dp);
+  if (blockDim.y == 1) {
+    if (a.grad_weight) cols.template store<DF32>(a.work, (int64_t)blockIdx.x * a.dim, dw);
+    if (a.grad_post_weight) cols.template store<DF32>(a.work, (d.ctas + blockIdx.x) * a.dim, dp);
+    return;
+  }
+  // a warp a row, or several: the warps' sums are added here, each warp's in its own ring
+  static_assert(C::kDepth * C::kQ * C::kWarpBytes >= 2 * 32 * C::kEach * 4, "two binary32 rows");
+  const int ring_floats = (int)(C::kDepth * ring.step / 4);
+  float* shared = reinterpret_cast<float*>(g_ring);
+  __syncwarp();
+  cols.keep(shared + threadIdx.y * ring_floats, dw);
+  cols.keep(shared + threadIdx.y * ring_floats + a.dim, dp);
+  __syncthreads();
+  for (int c = threadIdx.y * 32 + threadIdx.x; c < 2 * a.dim; c += 32 * blockDim.y) {
+    const bool post = c >= a.dim;
+    if (!(post ? a.grad_post_weight : a.grad_weight)) continue;
+    float s = 0.0f;
+    for (int y = 0; y < (int)blockDim.y; ++y) s += shared[y * ring_floats + c];
+    st_g(a.work + (post ? d.ctas + blockIdx.x : (int64_t)blockIdx.x) * a.dim + (post ? c - a.dim : c), s);
+  }
 }
 
 // How a row of `dim` columns is spread: threads, 16-byte vectors per thread,
-// rows per CTA, and the kernel's most threads.
+// warps of rows per CTA, the kernel's most threads, and the rows that share a
+// warp where all rows are aligned (Cols: PK).
 struct Shape {
-  int threads, groups, rows, most;
+  int threads, groups, rows, most, packs;
 };
 
 inline Shape spread(int dim, int vec, int groups, int most) {
@@ -623,6 +702,8 @@ inline Shape spread(int dim, int vec, int groups, int most) {
   s.most = most;
   s.threads = ((vectors + groups - 1) / groups + 31) / 32 * 32;
   s.rows = s.threads == 32 ? kWarpRows : 1;
+  s.packs = 1;
+  while (s.packs < 32 && vectors * 2 * s.packs <= 32) s.packs *= 2;
   return s;
 }
 
@@ -685,11 +766,13 @@ cudaError_t run_forward(const Shape& s, bool aligned, const NormForward& a, unsi
   return with_groups<D>(s.groups, [&](auto g) {
     constexpr int kGroups = decltype(g)::value;
     auto launch = [&](auto kernel, auto al) {
-      size_t smem;
+      size_t smem;   // (a packed row's slots are a vector a lane, too)
       const cudaError_t e2 = ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, 1024>>(kernel, s, &smem);
       if (e2 != cudaSuccess) return e2;
       return launch_after(kernel, dim3(grid), dim3(s.threads, s.rows), smem, st, 1, a);
     };
+    if constexpr (kGroups == 1)
+      if (aligned && s.packs > 1) return launch(norm_forward_kernel<D, RD, 1, true, 1024, true>, IntC<1>{});
     if (aligned) return launch(norm_forward_kernel<D, RD, kGroups, true, 1024>, IntC<1>{});
     return launch(norm_forward_kernel<D, RD, kGroups, false, 1024>, IntC<0>{});
   });
@@ -716,6 +799,9 @@ cudaError_t run_backward(const Shape& s, bool aligned, const NormBackward& a, co
       }
     }
     constexpr int kMost = backward_most(kGroups * D::kVec, false);
+    if constexpr (kGroups == 1)
+      if (aligned && s.packs > 1)
+        return launch(norm_backward_kernel<D, RD, 1, true, kMost, true>, IntC<1>{}, IntC<kMost>{});
     if (aligned) return launch(norm_backward_kernel<D, RD, kGroups, true, kMost>, IntC<1>{}, IntC<kMost>{});
     return launch(norm_backward_kernel<D, RD, kGroups, false, kMost>, IntC<0>{}, IntC<kMost>{});
   });

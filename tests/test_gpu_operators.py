@@ -204,6 +204,13 @@ NORMS = [
     (2, 3, 16384, "f32", "f32", "f32", True, 1, 0),
     (1, 4, 16383, "f32", "f32", "f32", False, 2, 0),
     (2, 4, 12289, "f16", "f16", "f16", True, 0, 0),
+    # rows that share a warp
+    (3, 1003, 128, "bf16", "f32", "f32", True, 17, 0),
+    (4, 77, 40, "f16", "f16", "f16", True, 7, 8),
+    (2, 50, 16, "f32", "f32", "f32", False, 0, 0),
+    (2, 9, 8, "bf16", "bf16", "f32", True, 3, 8),
+    (6, 6000, 72, "bf16", "bf16", "bf16", True, 1, 0),
+    (5, 33, 64, "f32", "f32", "f32", True, 33, 4),
 ]
 
 
