@@ -891,12 +891,21 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   Walk<D> w(sh.rows, per, begin + (tid >> 5), end, n >> 5);
   if (w.more()) w.load(raw);
 
+  const float row_lse = ld_g(a.lse + row), row_g = ld_g(a.g + row);
+  int64_t target = 0;
+  float gh = 0.0f, H = 0.0f;
+  if (!DISTILL) {
+    target = ld_g(a.targets + row);
+    if (a.grad_entropy) {
+      gh = ld_g(a.grad_entropy + row);
+      H = ld_g(a.entropy + row);
+    }
+  }
   // The columns where the target or the teacher adds something are read
   // before any column is written (the gradient may stand in the logits' place).
   if (DISTILL) {
     load_teacher<D>(sh.teacher, a.x, a.ids, a.teacher, a.K, a.teacher_f32, row);
   } else if (tid == 0) {
-    const int64_t target = ld_g(a.targets + row);
     const bool some = target >= 0 && target < a.x.V;
     sh.teacher.id[0] = some ? (int)target : -1;
     sh.teacher.x[0] = some ? logit_at<D>(a.x, row, (int)target) : 0.0f;
@@ -904,7 +913,6 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   __syncthreads();
   // dL_j = p_j (A + B log p_j), plus that
   float A, B = 0.0f;
-  const float row_lse = ld_g(a.lse + row);
   // nothing left by the mask: -inf everywhere, or logits so low (the type's
   // lowest value) that lse cannot hold the logarithm of their sum beside them
   bool zero = row_lse < kNothingLeft;
@@ -915,7 +923,7 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   if constexpr (DISTILL) {
     const Softmax q(sh.teacher, a.K, inv_tau);
     zero = zero || !q.taught();
-    A = zero ? 0.0f : ld_g(a.g + row) * a.x.tau;
+    A = zero ? 0.0f : row_g * a.x.tau;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = tid + i * n;
@@ -946,10 +954,7 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
       repeated[i] = earlier;
     }
   } else {
-    const int64_t target = ld_g(a.targets + row);
-    const float g = target < 0 ? 0.0f : target >= a.x.V ? NAN : ld_g(a.g + row);
-    const float gh = a.grad_entropy ? ld_g(a.grad_entropy + row) : 0.0f;
-    const float H = a.grad_entropy ? ld_g(a.entropy + row) : 0.0f;
+    const float g = target < 0 ? 0.0f : target >= a.x.V ? NAN : row_g;
     A = -(g + gh * H) * inv_tau;
     B = -gh * inv_tau;
     fixed[0] = g * inv_tau;
