@@ -33,6 +33,8 @@
 // index arithmetic within a chunk.
 #include "ra_ops.cuh"
 
+#include <type_traits>
+
 namespace ra {
 namespace {
 
@@ -423,21 +425,32 @@ constexpr int kMaxParts = 8;   // CTAs of a portable cluster
 constexpr int kGroups = 12;    // a warp's chunks, in this many groups at most
 constexpr int kCandidates = 256;   // at least 32 of each part of a row
 
-struct ForwardShared {
+struct RowShared {
   RowShards rows;
   Stats warp[kMaxThreads / 32];
   Stats block;                         // for the other CTAs of the row
-  uint64_t lists[kMaxThreads / 32][32];
-  uint32_t largest[kMaxThreads / 32][kGroups][32];   // the lanes' largest logits of each group of chunks, ordered()
-  uint32_t again[kMaxThreads / 32][32];   // the groups and lanes to read again
-  uint64_t candidates[kCandidates];
-  int found;
-  int lowest;                             // a logit of the type's lowest value was seen
+};
+struct DistillShared : RowShared {
   Teacher teacher;
 };
+struct TopShared : RowShared {
+  int target;                          // -1: none, -2: one that is no column
+  float target_logit;
+  int found;
+  int lowest;                          // a logit of the type's lowest value was seen
+  uint64_t lists[kMaxThreads / 32][32];
+  uint64_t candidates[kCandidates];
+};
+// and for the top K, as many as there are warps: with static ones of eight
+// warps' size an SM held fewer of the small CTAs that short rows take
+struct WarpTop {
+  uint32_t largest[kGroups][32];   // the lanes' largest logits of each group of chunks, ordered()
+  uint32_t again[32];              // the groups and lanes to read again
+};
+extern __shared__ WarpTop g_warp_top[];
 
 // The block's statistics, the same in every thread (and of every CTA of the row).
-__device__ __noinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts) {
+__device__ __noinline__ Stats block_stats(Stats st, RowShared& sh, int parts) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;   // four or eight
   st = warp_stats(st, 32);
   if (lane == 0) sh.warp[threadIdx.x >> 5] = st;
@@ -457,7 +470,7 @@ __device__ __noinline__ Stats block_stats(Stats st, ForwardShared& sh, int parts
 // logit m first, then t = (x - m) scale.  Rare, so it reads the row twice
 // more; m comes back as `largest`.
 template <class D>
-__device__ __noinline__ Stats lowest_stats(const VocabForward& a, ForwardShared& sh, int per, int begin, int end,
+__device__ __noinline__ Stats lowest_stats(const VocabForward& a, RowShared& sh, int per, int begin, int end,
                                            int parts, float scale, float* largest) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float m = -INFINITY;
@@ -503,7 +516,7 @@ __device__ __noinline__ Stats lowest_stats(const VocabForward& a, ForwardShared&
 // The lanes' slots, elements [lo, hi) of each: those that reach the bound
 // become candidates, as far as there is room.
 template <class D>
-__device__ __noinline__ void collect(ForwardShared& sh, uint4 raw, int lo, int hi, int column, uint32_t bound) {
+__device__ __noinline__ void collect(TopShared& sh, uint4 raw, int lo, int hi, int column, uint32_t bound) {
   const int lane = threadIdx.x & 31;
   float x[D::kVec];
   unpack<D>(raw, x);
@@ -545,7 +558,7 @@ __device__ __forceinline__ int column_of(const RowShards& s, int q, int per, int
 
 // lists[0]: the `top` largest of the candidates (0: none), falling; all keys
 // but 0 differ.
-__device__ __noinline__ void rank_candidates(ForwardShared& sh, int n, int top) {
+__device__ __noinline__ void rank_candidates(TopShared& sh, int n, int top) {
   if (threadIdx.x < 32) sh.lists[0][threadIdx.x] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -564,7 +577,7 @@ __device__ __noinline__ void rank_candidates(ForwardShared& sh, int n, int top) 
 // comes after that is beaten by K logits.  What comes before it is read again;
 // what is equal to it lies in its chunk.
 template <class D>
-__device__ __noinline__ void top_of_many(ForwardShared& sh, uint32_t best, int best_at, int top, int C, int per,
+__device__ __noinline__ void top_of_many(TopShared& sh, uint32_t best, int best_at, int top, int C, int per,
                                          int begin, int end) {
   constexpr int V = D::kVec;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -625,7 +638,7 @@ template <class D, bool DISTILL>
 __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __grid_constant__ VocabForward a,
                                                                        int parts) {
   constexpr int V = D::kVec;
-  __shared__ ForwardShared sh;
+  __shared__ typename std::conditional<DISTILL, DistillShared, TopShared>::type sh;
   after_predecessor();
   const int64_t row = blockIdx.x / parts;
   const int part = parts > 1 ? (int)cluster_rank() : 0;
@@ -635,7 +648,8 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const int share = (chunks + parts - 1) / parts;
   const int begin = part * share, end = min(chunks, begin + share);
   load_row<D>(a.x, row, sh.rows);
-  if (!DISTILL && tid == 0) sh.found = sh.lowest = 0;
+  if constexpr (!DISTILL)
+    if (tid == 0) sh.found = sh.lowest = 0;
   __syncthreads();
 
   Stats st{kNoRef, 0.0f, 0.0f};
@@ -662,7 +676,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       }
       ++in_group;
       group_best = max(group_best, o);
-      sh.largest[warp][group][lane] = group_best;
+      g_warp_top[warp].largest[group][lane] = group_best;
     }
     if (largest * scale > st.ref + kLag) {
       st.s = s2.x + s2.y;
@@ -693,13 +707,12 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
     if (w.more()) some_one = w.load(one);
     // what is needed at the end, beside the row's first logits
     if (part == 0) {
-      if (DISTILL) {
+      if constexpr (DISTILL) {
         load_teacher<D>(sh.teacher, a.x, a.ids, a.teacher, a.K, a.teacher_f32, row);
       } else if (tid == 0) {
         const int64_t target = ld_g(a.targets + row);
-        // no target: -1; one that is no column: -2
-        sh.teacher.id[0] = target < 0 ? -1 : target >= a.x.V ? -2 : 0;
-        sh.teacher.x[0] = target < 0 || target >= a.x.V ? 0.0f : logit_at<D>(a.x, row, (int)target);
+        sh.target = target < 0 ? -1 : target >= a.x.V ? -2 : 0;
+        sh.target_logit = target < 0 || target >= a.x.V ? 0.0f : logit_at<D>(a.x, row, (int)target);
       }
     }
     while (w.more()) {
@@ -751,8 +764,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
     }
   } else {
     if (first && tid == 0) {
-      const int target = sh.teacher.id[0];
-      st_g(a.logprob + row, target == -1 ? 0.0f : target == -2 ? NAN : log_prob(sh.teacher.x[0]));
+      st_g(a.logprob + row, sh.target == -1 ? 0.0f : sh.target == -2 ? NAN : log_prob(sh.target_logit));
       if (a.entropy) st_g(a.entropy + row, empty ? 0.0f : kLn2 * (log2_s - st.u / st.s));
     }
     if (a.top > 0) {
@@ -766,12 +778,12 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       // type's lowest value): only that is read again.
       const bool masked = bound <= NegInf<D>::lowest;
       if (masked) bound = NegInf<D>::lowest + 1;
-      uint32_t* again = sh.again[warp];   // group << 5 | lane
+      uint32_t* again = g_warp_top[warp].again;   // group << 5 | lane
       const int groups = in_group ? group + 1 : 0;
       for (int g = 0; g < groups;) {
         int n = 0;
         for (; g < groups; ++g) {   // a group's lanes, and the next ones' while they fit
-          const uint32_t largest = sh.largest[warp][g][lane];
+          const uint32_t largest = g_warp_top[warp].largest[g][lane];
           const unsigned hits = __ballot_sync(0xFFFFFFFFu, largest >= bound);
           if (largest == NegInf<D>::lowest) sh.lowest = 1;
           if (n + __popc(hits) > 32) break;
@@ -1059,8 +1071,9 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
     int parts = 1;
     if (!many)
       while (parts < kMaxParts && a.x.rows * parts * 6 <= 5 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
+    const size_t smem = a.top > 0 ? threads / 32 * sizeof(WarpTop) : 0;   // 13 KB at most
     auto kernel = a.ids ? vocab_forward_kernel<D, true> : vocab_forward_kernel<D, false>;
-    return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), 0, st, parts, a, parts);
+    return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), smem, st, parts, a, parts);
   });
 }
 
