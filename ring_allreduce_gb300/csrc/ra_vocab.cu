@@ -879,6 +879,9 @@ struct BackwardShared {
   RowShards rows;
   uintptr_t grad[kMaxRanks];
   Teacher teacher;
+  // what the target or the teacher adds, and at which column (-1: nowhere); each thread's own tokens
+  float add[kTeacherMax];
+  int at[kTeacherMax];
 };
 
 template <class D, bool DISTILL>
@@ -929,18 +932,13 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   // lowest value) that lse cannot hold the logarithm of their sum beside them
   bool zero = row_lse < kNothingLeft;
   const float lse = zero ? 0.0f : row_lse;
-  // what is added for tokens tid and tid + n (at least 128 threads, at most 256 tokens)
-  float fixed[2] = {0.0f, 0.0f};
-  bool repeated[2] = {false, false};
   if constexpr (DISTILL) {
     const Softmax q(sh.teacher, a.K, inv_tau);
     zero = zero || !q.taught();
     A = zero ? 0.0f : row_g * a.x.tau;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = tid + i * n;
-      if (k >= a.K || zero) continue;
+    for (int k = tid; k < a.K && !zero; k += n) {
       const int c = sh.teacher.id[k];
+      sh.at[k] = -1;
       if (c < 0) continue;
       // Of equal tokens the first one adds for all.  They are rare, so they
       // are counted four at a time first (6783 x 12160 f16, 85 tokens: the
@@ -962,14 +960,18 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
           sum += expf((sh.teacher.t[o] - q.m) * inv_tau) / q.s;
         }
       }
-      fixed[i] = -A * sum;
-      repeated[i] = earlier;
+      if (earlier) continue;
+      sh.add[k] = -A * sum;
+      sh.at[k] = c;
     }
   } else {
     const float g = target < 0 ? 0.0f : target >= a.x.V ? NAN : row_g;
     A = -(g + gh * H) * inv_tau;
     B = -gh * inv_tau;
-    fixed[0] = g * inv_tau;
+    if (tid == 0) {
+      sh.add[0] = g * inv_tau;
+      sh.at[0] = sh.teacher.id[0];
+    }
   }
   if (zero) A = B = 0.0f;
   // binary32 outputs show the exponent's rounding: expf there
@@ -1028,17 +1030,14 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   }
   __syncthreads();
   const int tokens = zero ? 0 : DISTILL ? a.K : 1;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int k = tid + i * n;
-    if (k >= tokens) continue;
-    const int c = sh.teacher.id[k];
-    if (c < 0 || repeated[i]) continue;
+  for (int k = tid; k < tokens; k += n) {
+    const int c = sh.at[k];
+    if (c < 0) continue;
     const int r = c / a.x.C, e = c - r * a.x.C;
     const int chunk = r * per + ((int)((sh.rows.first[r] & kLine) / sizeof(T)) + e) / (V * kChunk);
     if (chunk < begin || chunk >= end) continue;   // another CTA's part of the row
     st_g(reinterpret_cast<T*>(sh.grad[r]) + e,
-         narrow<D>(gradient(make_float2(sh.teacher.x[k], 0.0f)).x + fixed[i]));
+         narrow<D>(gradient(make_float2(sh.teacher.x[k], 0.0f)).x + sh.add[k]));
   }
 }
 
@@ -1083,10 +1082,16 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
   return with_float(dtype, [&](auto d) {
     using D = decltype(d);
     const int chunks = chunks_per_shard(a.x) * a.x.shards;
-    const int threads = 128, warps = threads / 32;
+    // Many rows: CTAs of 128 threads at most, four chunks a warp (loss gradient
+    // of 20000 x 8192 bf16, eight chunks a row: 110 us in CTAs of two warps, 116
+    // of four, 151 of one; of 5184 x 503 f32, two chunks: 26 us of one, 28 of four).
     // Few rows: split each until there are four CTAs of 128 threads to an SM, a
     // chunk a warp at least.  (Every part reads the teacher's tokens again:
     // loss and gradient of 129 x 32003 f16 take 12.9 us so, 14.3 with eight.)
+    const bool many = a.x.rows >= 4 * (int64_t)sms;
+    int threads = many ? 32 : 128;
+    while (threads < 128 && threads / 32 * 4 < chunks) threads *= 2;
+    const int warps = threads / 32;
     int64_t parts = ((int64_t)4 * sms + a.x.rows - 1) / a.x.rows;
     const int64_t most = (chunks + warps - 1) / warps;
     if (parts > most) parts = most;
