@@ -1063,10 +1063,13 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
     // threads, a chunk a warp, and clusters that split a row
     // while less than five sixths of the SMs are covered, eight chunks a CTA
     // at least (61 x 50021, 20 alternatives: 10.9 us in four parts, 11.4 in
-    // two; 129 x 32003: 11.1 in two, 9.8 in one).
+    // two; 129 x 32003: 11.1 in two, 9.8 in one).  Two threads an alternative
+    // at least: the bound is one of the threads' maxima, and a low one lets
+    // many logits through (20000 x 8192 bf16, 32 alternatives: 155 us with two
+    // warps, 325 with one; with 20, 131 and 122).
     const bool many = a.x.rows >= 4 * (int64_t)sms;
     int threads = 32;
-    while (threads < (many ? 128 : 256) && threads / 32 * (many ? 8 : 1) < chunks) threads *= 2;
+    while (threads < (many ? 128 : 256) && (threads / 32 * (many ? 8 : 1) < chunks || threads < 2 * a.top)) threads *= 2;
     int parts = 1;
     if (!many)
       while (parts < kMaxParts && a.x.rows * parts * 6 <= 5 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
