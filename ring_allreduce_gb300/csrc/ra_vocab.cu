@@ -738,12 +738,14 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const float lse = empty ? -INFINITY
                     : low ? __fmaf_rn(lowest, a.x.inv_tau, kLn2 * log2_s)
                           : kLn2 * (st.ref + log2_s);
-  auto log_prob = [&](float x) {
+  // log p of a logit, or tau times that
+  auto log_prob = [&](float x, bool by_tau = false) {
     if (empty) return -INFINITY;
     const float d = low ? x - lowest : x;
     const float t = __fmaf_rn(d, scale, low ? 0.0f : -st.ref);
     // a masked logit near the type's lowest value leaves binary32's range in t before it does so itself
-    return t == -INFINITY && log2_s == log2_s ? d * a.x.inv_tau : kLn2 * (t - log2_s);
+    return t == -INFINITY && log2_s == log2_s ? (by_tau ? d : d * a.x.inv_tau)
+                                                  : (by_tau ? kLn2 * a.x.tau : kLn2) * (t - log2_s);
   };
   const bool first = part == 0;
   if (first && tid == 0) st_g(a.lse + row, lse);
@@ -756,11 +758,12 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       float loss = 0.0f;
       for (int k = lane; k < a.K; k += 32) {
         if (t.id[k] < 0) continue;
-        const float d = (t.t[k] - q.m) * a.x.inv_tau, p = expf(d) / q.s;
-        if (p != 0.0f) loss += p * ((d - log_s) - log_prob(t.x[k]));   // NaN included
+        const float d = t.t[k] - q.m, p = expf(d * a.x.inv_tau) / q.s;
+        // tau (log q - log p): within binary32's range wherever the logits are.  (NaN included)
+        if (p != 0.0f) loss += p * ((d - a.x.tau * log_s) - log_prob(t.x[k], true));
       }
       loss = warp_sum(loss);
-      if (lane == 0) st_g(a.loss + row, q.taught() ? loss * a.x.tau * a.x.tau : 0.0f);
+      if (lane == 0) st_g(a.loss + row, q.taught() ? loss * a.x.tau : 0.0f);
     }
   } else {
     if (first && tid == 0) {

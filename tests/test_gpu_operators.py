@@ -399,6 +399,10 @@ HEADS = [
     (1, 615, 300, "f32", 32, 1.0, True, 0, 1),
     (2, 640, 20000, "f16", 5, 0.7, True, 0, 0),
     (3, 700, 9000, "bf16", 32, 1.0, False, 0, 0),
+    # many short rows: CTAs of a warp or two
+    (2, 700, 503, "f32", 32, 0.7, True, 0, 0),
+    (3, 650, 1000, "f16", 20, 1.0, False, 1, 1),
+    (4, 620, 4096, "bf16", 32, 1.3, True, 8, 3),
 ]
 
 
