@@ -24,6 +24,8 @@ using namespace norm;
 // The CTAs' column partials joined, in their order (a gate row's: the units'): blockIdx.y 0 the pre
 // norm's weight, 1 the post norm's, 2.. the gate rows.
 // Warp w of a CTA's 32 columns sums every blockDim.y-th partial, then a column's slices are summed by a warp.
+// 147 partials of 8192 columns, two weights and a gate: 13 us with nothing in L2, 14 MB of reads; a few us
+// behind the kernel that wrote them.
 __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormBackward a,
                                                          const __grid_constant__ Deal d) {
   __shared__ float part[32][33];

@@ -435,6 +435,12 @@ template <class C, class D, class RD> struct ForwardRows {
   }
 };
 
+// Measured, as parts of a copy's 6.8 TB/s for the bytes that have to move:
+// 8192 x 4096, four ranks, bf16 with a binary32 residual, post norm, gate, the
+// sum kept and four copies out: 143 us, 0.90; 1023 x 5001 binary32, three
+// ranks, no row aligned: 30 us, 0.70 (seven rows an SM, the last ones alone);
+// one row of 4096 from eight ranks: 4.4 us, two dependent reads and two sums
+// over a block after the launch.
 template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constant__ NormForward a) {
   using C = Cols<D, VPT, AL, MAXT, PK>;
@@ -566,6 +572,12 @@ template <class C, class D, class RD> struct BackwardRows {
   }
 };
 
+// Measured: 4096 x 8192 bf16, eight partial gradients, post norm and gate:
+// 162 us with the join of the column sums, 0.79 of the copy bandwidth.  The
+// registers bound it: a row's values and three sums per column leave one
+// CTA of 16 warps to an SM, whose waits for its own sums nothing else fills
+// (DRAM 64 % busy, each scheduler with four warps to choose from).  96 x 1538
+// fp16, two ranks, eight gate rows: 9.6 us, two launches' latency.
 template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_constant__ NormBackward a,
                                                              const __grid_constant__ Deal d) {
