@@ -260,8 +260,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // `mine`'s place in the shared memory of CTA `rank`
 __device__ __forceinline__ uint32_t in_cta(const void* mine, uint32_t rank) {
@@ -269,15 +272,14 @@ __device__ __forceinline__ uint32_t in_cta(const void* mine, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(mine)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ float far_float(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+// What another CTA is to read is stored into its shared memory before the
+// barrier: read from here after it, a few rows waited for the way there and
+// back once more (one row of 131072, 20 alternatives: 8.6 us, 8.8 that way).
+__device__ __forceinline__ void far_store(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
-__device__ __forceinline__ uint64_t far_u64(uint32_t a) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void far_store(uint32_t a, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
 // ---------------------------------------------- lists of a warp's 32 largest
@@ -428,7 +430,7 @@ constexpr int kCandidates = 256;   // at least 32 of each part of a row
 struct RowShared {
   RowShards rows;
   Stats warp[kMaxThreads / 32];
-  Stats block;                         // for the other CTAs of the row
+  Stats block[kMaxParts];              // what the row's CTAs found, stored here by each of them
 };
 struct DistillShared : RowShared {
   Teacher teacher;
@@ -443,24 +445,31 @@ struct TopShared : RowShared {
 };
 // and for the top K, as many as there are warps: with static ones of eight
 // warps' size an SM held fewer of the small CTAs that short rows take
-struct WarpTop {
+struct alignas(16) WarpTop {
   uint32_t largest[kGroups][32];   // the lanes' largest logits of each group of chunks, ordered()
   uint32_t again[32];              // the groups and lanes to read again
 };
 extern __shared__ WarpTop g_warp_top[];
+// behind them, where CTAs share a row: the K largest of each, stored into the first one's
+using PartLists = uint64_t[kMaxParts][32];
 
 // The block's statistics, the same in every thread (and of every CTA of the row).
-__device__ __noinline__ Stats block_stats(Stats st, RowShared& sh, int parts) {
+__device__ __noinline__ Stats block_stats(Stats st, RowShared& sh, int part, int parts) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;   // four or eight
   st = warp_stats(st, 32);
   if (lane == 0) sh.warp[threadIdx.x >> 5] = st;
   __syncthreads();
   st = warp_stats(sh.warp[lane & (warps - 1)], warps);
   if (parts > 1) {   // a power of two, too
-    if (threadIdx.x == 0) sh.block = st;
+    if ((int)threadIdx.x < parts) {
+      const uint32_t a = in_cta(&sh.block[part], threadIdx.x);
+      far_store(a, st.ref);
+      far_store(a + 4, st.s);
+      far_store(a + 8, st.u);
+    }
+    __syncwarp();
     cluster_sync();
-    const uint32_t a = in_cta(&sh.block, (uint32_t)(lane & (parts - 1)));
-    st = warp_stats(Stats{far_float(a), far_float(a + 4), far_float(a + 8)}, parts);
+    st = warp_stats(sh.block[lane & (parts - 1)], parts);
   }
   return st;
 }
@@ -471,7 +480,7 @@ __device__ __noinline__ Stats block_stats(Stats st, RowShared& sh, int parts) {
 // more; m comes back as `largest`.
 template <class D>
 __device__ __noinline__ Stats lowest_stats(const VocabForward& a, RowShared& sh, int per, int begin, int end,
-                                           int parts, float scale, float* largest) {
+                                           int part, int parts, float scale, float* largest) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float m = -INFINITY;
   uint4 raw[kPerLane];
@@ -487,9 +496,10 @@ __device__ __noinline__ Stats lowest_stats(const VocabForward& a, RowShared& sh,
   m = warp_max_nan(lane < warps ? sh.warp[lane].s : -INFINITY);
   if (parts > 1) {
     cluster_sync();   // sh.block is read no more
-    if (threadIdx.x == 0) sh.block.s = m;
+    if ((int)threadIdx.x < parts) far_store(in_cta(&sh.block[part], threadIdx.x) + 4, m);
+    __syncwarp();
     cluster_sync();
-    m = lane < parts ? far_float(in_cta(&sh.block, (uint32_t)lane) + 4) : -INFINITY;
+    m = lane < parts ? sh.block[lane].s : -INFINITY;
     m = warp_max_nan(m);
     cluster_sync();
   }
@@ -510,7 +520,7 @@ __device__ __noinline__ Stats lowest_stats(const VocabForward& a, RowShared& sh,
       }
     }
   }
-  return block_stats(st, sh, parts);
+  return block_stats(st, sh, part, parts);
 }
 
 // The lanes' slots, elements [lo, hi) of each: those that reach the bound
@@ -638,7 +648,7 @@ __device__ __noinline__ void top_of_many(TopShared& sh, uint32_t best, int best_
 // x 131072 bf16 in eight shards, 64 teacher tokens: 161 us, 0.98; log
 // probabilities, entropy and five alternatives: 184 us, 0.86 (the entropy's
 // multiply and the largest of every group of chunks: issue slots); one row
-// with 20 alternatives: 9.0 us, 4 us of them the choice of the alternatives
+// with 20 alternatives: 8.8 us, 4 us of them the choice of the alternatives
 // over a cluster of eight CTAs.  Short rows pay per row for the alternatives:
 // 20000 x 8192 bf16 55 us without, 88 with five.
 template <class D, bool DISTILL>
@@ -649,6 +659,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   after_predecessor();
   const int64_t row = blockIdx.x / parts;
   const int part = parts > 1 ? (int)cluster_rank() : 0;
+  if (parts > 1) cluster_arrive();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const float scale = kLog2e * a.x.inv_tau;
   const int per = chunks_per_shard(a.x), chunks = per * a.x.shards;
@@ -736,10 +747,11 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   }
   st.s = s2.x + s2.y;
   st.u = u2.x + u2.y;
-  st = block_stats(st, sh, parts);
+  if (parts > 1) cluster_wait();   // every CTA of the row has begun
+  st = block_stats(st, sh, part, parts);
   float lowest = 0.0f;
   const bool low = st.s == 0.0f;   // no logit above kNoRef
-  if (low) st = lowest_stats<D>(a, sh, per, begin, end, parts, scale, &lowest);
+  if (low) st = lowest_stats<D>(a, sh, per, begin, end, part, parts, scale, &lowest);
   const bool empty = low && lowest == -INFINITY;   // nothing but -inf
   const float log2_s = log2f(st.s);                // NaN where the row has +inf or NaN
   const float lse = empty ? -INFINITY
@@ -849,22 +861,21 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       // lists[0]: the K largest, falling
       if (parts > 1) {
         // the parts' lists, a warp each, joined in the first part
+        PartLists& of = *reinterpret_cast<PartLists*>(g_warp_top + warps);
+        if (first && warp >= parts) of[warp][lane] = 0;
+        if (warp == 0) far_store(in_cta(&of[part][lane], 0), sh.lists[0][lane]);
         cluster_sync();
-        uint64_t key = 0;
-        if (first && warp < parts) key = far_u64(in_cta(&sh.lists[0][lane], (uint32_t)warp));
-        cluster_sync();   // after which the other parts may end
         if (first) {
-          sh.lists[warp][lane] = key;
-          __syncthreads();
+          const uint64_t key = of[warp][lane];
           // a key's place is the sum of what every list has before it; all lists searched at once
           int before[kMaxParts] = {};
 #pragma unroll
           for (int step = 16; step > 0; step >>= 1)
 #pragma unroll
-            for (int p = 0; p < kMaxParts; ++p) before[p] += sh.lists[p][before[p] + step - 1] > key ? step : 0;
+            for (int p = 0; p < kMaxParts; ++p) before[p] += of[p][before[p] + step - 1] > key ? step : 0;
           int rank = 0;
 #pragma unroll
-          for (int p = 0; p < kMaxParts; ++p) rank += before[p] + (sh.lists[p][before[p]] > key);
+          for (int p = 0; p < kMaxParts; ++p) rank += before[p] + (of[p][before[p]] > key);
           __syncthreads();
           if (threadIdx.x < 32) sh.lists[0][lane] = 0;
           __syncthreads();
@@ -879,8 +890,6 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
       }
     }
   }
-  // no CTA ends while its shared memory may be read
-  if (parts > 1 && (DISTILL || a.top == 0)) cluster_sync();
 }
 
 // ----------------------------------------------------------------- backward
@@ -1088,7 +1097,7 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
     int parts = 1;
     if (!many)
       while (parts < kMaxParts && a.x.rows * parts * 6 <= 5 * (int64_t)sms && chunks >= 16 * parts) parts *= 2;
-    const size_t smem = a.top > 0 ? threads / 32 * sizeof(WarpTop) : 0;   // 13 KB at most
+    const size_t smem = a.top > 0 ? threads / 32 * sizeof(WarpTop) + (parts > 1 ? sizeof(PartLists) : 0) : 0;   // 15 KB at most
     auto kernel = a.ids ? vocab_forward_kernel<D, true> : vocab_forward_kernel<D, false>;
     return launch_after(kernel, dim3((unsigned)(a.x.rows * parts)), dim3((unsigned)threads), smem, st, parts, a, parts);
   });
