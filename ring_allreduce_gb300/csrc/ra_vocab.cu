@@ -14,6 +14,12 @@
 // log2(e) that the thread saw, and s and u are moved when it is passed by more
 // (rare after the first vectors), so 2^t never leaves its range.  Then lse =
 // ln2 (ref + log2 s) and H = ln2 (log2 s - u / s).  All statistics are binary32.
+// ref is the rounded x log2(e) of a logit, t the exact one less ref, so t of
+// that very logit is half a unit of ref's last place: |ref| is held to 2^24,
+// where that is 1 at most.  (At 1e10 it would be 2^8, and 2^t infinite: a mask
+// of such a value over a thread's first logits would take the row with it.)
+// What lies below counts for nothing beside a logit above; a row that lies
+// beyond it altogether has its largest logit taken off exactly (far_stats).
 //
 // The top K come out of the same pass without a comparison per element
 // against a list: each thread also keeps the largest logit it saw, and its
@@ -43,7 +49,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFarBelow = -200.0f;   // 2^-200 is 0 in binary32: exponents that are multiplied with their power
                                        // are held above this, so that it stays 0 (not 0 * inf)
 constexpr float kLag = 4.0f;
-constexpr float kNoRef = -8.5e37f;     // ref before the first finite logit
+constexpr float kFar = 16777216.0f;    // 2^24: a row whose ref would be further from zero is a far one
+constexpr float kNoRef = -kFar;        // ref before the first logit above it
 
 constexpr float kNothingLeft = -1e30f;
 
@@ -474,13 +481,13 @@ __device__ __noinline__ Stats block_stats(Stats st, RowShared& sh, int part, int
   return st;
 }
 
-// Rows without a logit above kNoRef: -inf everywhere, or the type's lowest
-// value in places (near -3e38, where x scale is out of range).  Their largest
-// logit m first, then t = (x - m) scale.  Rare, so it reads the row twice
-// more; m comes back as `largest`.
+// Far rows: no thread's ref has moved from kNoRef (-inf everywhere, or a mask's
+// low value), or one lies above kFar.  Their largest logit m first, then t = (x - m) scale, which
+// is 0 where x is m and exact wherever 2^t counts.  Rare, so it reads the row
+// twice more; m comes back as `largest`.
 template <class D>
-__device__ __noinline__ Stats lowest_stats(const VocabForward& a, RowShared& sh, int per, int begin, int end,
-                                           int part, int parts, float scale, float* largest) {
+__device__ __noinline__ Stats far_stats(const VocabForward& a, RowShared& sh, int per, int begin, int end, int part,
+                                        int parts, float scale, float* largest) {
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float m = -INFINITY;
   uint4 raw[kPerLane];
@@ -505,7 +512,7 @@ __device__ __noinline__ Stats lowest_stats(const VocabForward& a, RowShared& sh,
   }
   __syncthreads();
   *largest = m;
-  Stats st{0.0f, 0.0f, 0.0f};   // relative to m
+  Stats st{0.0f, m < INFINITY ? 0.0f : NAN, 0.0f};   // relative to m
   for (Walk<D> w(sh.rows, per, begin + (int)(threadIdx.x >> 5), end, warps); w.more() && m > -INFINITY; w.next()) {
     w.load(raw);
 #pragma unroll
@@ -749,19 +756,19 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   st.u = u2.x + u2.y;
   if (parts > 1) cluster_wait();   // every CTA of the row has begun
   st = block_stats(st, sh, part, parts);
-  float lowest = 0.0f;
-  const bool low = st.s == 0.0f;   // no logit above kNoRef
-  if (low) st = lowest_stats<D>(a, sh, per, begin, end, part, parts, scale, &lowest);
-  const bool empty = low && lowest == -INFINITY;   // nothing but -inf
+  float row_max = 0.0f;   // of a far row
+  const bool far = st.ref <= kNoRef || st.ref > kFar;   // ref is the largest of the threads' now
+  if (far) st = far_stats<D>(a, sh, per, begin, end, part, parts, scale, &row_max);
+  const bool empty = far && row_max == -INFINITY;   // nothing but -inf
   const float log2_s = log2f(st.s);                // NaN where the row has +inf or NaN
   const float lse = empty ? -INFINITY
-                    : low ? __fmaf_rn(lowest, a.x.inv_tau, kLn2 * log2_s)
+                    : far ? __fmaf_rn(row_max, a.x.inv_tau, kLn2 * log2_s)
                           : kLn2 * (st.ref + log2_s);
   // log p of a logit, or tau times that
   auto log_prob = [&](float x, bool by_tau = false) {
     if (empty) return -INFINITY;
-    const float d = low ? x - lowest : x;
-    const float t = __fmaf_rn(d, scale, low ? 0.0f : -st.ref);
+    const float d = far ? x - row_max : x;
+    const float t = __fmaf_rn(d, scale, far ? 0.0f : -st.ref);
     // a masked logit near the type's lowest value leaves binary32's range in t before it does so itself
     return t == -INFINITY && log2_s == log2_s ? (by_tau ? d : d * a.x.inv_tau)
                                                   : (by_tau ? kLn2 * a.x.tau : kLn2) * (t - log2_s);

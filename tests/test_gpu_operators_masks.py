@@ -1,0 +1,129 @@
+"""The vocabulary head on rows whose logits are far from zero: masks of an
+ordinary large value (-1e9, -1e10, -1e30, ...) over part or all of a row, rows
+that lie far above zero, and temperatures that take logits there.  Against the
+definitions in 64 bits, which take a row's largest logit off first.
+
+What binary32 loses, beside the one rounding of an output (E its unit
+roundoff): a row's sum of powers is good to 2^-21 (2^x: 2^-22, its exponent:
+the weighted sum of |t| E over the terms, at most log2 V and a few) and loses at
+most one E an addition, V / 32 of them a thread in the smallest CTAs and 64 in
+the joins.  A value x / tau or x - max is good to a few roundings (the
+reciprocal of tau, its product with log2 e, the product with x, the last sum and
+product): 8 E of its size covers them."""
+
+import math
+
+import pytest
+
+from test_gpu_operators import E, gen, logits, randn, same, shards_of, stats64, top_ids64
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+FILLS = {"f32": (-1e5, -1e7, -1e9, -1e10, -1e20, -1e30, -1e37, -3e38),
+         "bf16": (-1e5, -1e7, -1e9, -1e10, -1e20, -1e30, -1e37, -3e38), "f16": (-1e3, -2e4, -6e4)}
+KINDS = 7
+# R, V, times the rows are there, pad, off: few rows, split over CTAs; many short ones
+SHAPES = [(3, 50021, 1, 0, 1), (4, 1501, 24, 3, 0)]
+CASES = [(s, d, tau) for s in SHAPES for d in FILLS for tau in (0.7, 1.0, 2.0, 1e-3)]
+
+
+@pytest.fixture(scope="module")
+def ops():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from ring_allreduce_gb300 import build
+    build.build()
+    from ring_allreduce_gb300 import operators
+    return operators
+
+
+def far_rows(g, V, dtype, times):
+    """Seven rows for each value: filled with it, all but one token, the first two thirds, nine tenths in places;
+    spread around it; and filled with, or spread around, its negative."""
+    x, _ = logits(g, KINDS * len(FILLS[dtype]) * times, V, dtype)
+    most = torch.finfo(x.dtype).max
+    for t in range(x.shape[0]):
+        fill, kind = FILLS[dtype][t // KINDS % len(FILLS[dtype])], t % KINDS
+        if kind == 1:
+            keep = x[t, t * 31 % V].clone()
+            x[t] = fill
+            x[t, t * 31 % V] = keep
+        elif kind == 2:
+            x[t, :2 * V // 3] = fill
+        elif kind == 3:
+            x[t, torch.rand(V, generator=g, device="cuda") < 0.9] = fill
+        else:
+            spread = 2.0 ** -6 * torch.randn(V, generator=g, device="cuda") if kind in (4, 6) else torch.zeros_like(x[t])
+            sign = -1.0 if kind > 4 else 1.0
+            x[t] = (sign * fill * (1.0 + spread.float())).clamp(-most, most).to(x.dtype)
+    return x
+
+
+def sum_loss(V):
+    return 2.0 ** -21 + (V / 32 + 64) * E
+
+
+def size(v):
+    return torch.where(torch.isfinite(v), v.abs(), 0.0)
+
+
+def in_f32(v):
+    """Values divided by tau may leave binary32's range: rounded to it."""
+    return v.float().double()
+
+
+def case(spec):
+    (R, V, times, pad, off), dtype, tau = spec
+    g = gen(101)
+    x = far_rows(g, V, dtype, times)
+    T = x.shape[0]
+    targets = torch.where(torch.rand(T, generator=g, device="cuda") < 0.5, x.float().argmax(1),
+                          torch.randint(V, (T,), generator=g, device="cuda"))
+    return g, x, targets, shards_of(x, R, pad, off)
+
+
+@pytest.mark.parametrize("spec", CASES, ids=lambda s: "-".join(map(str, (*s[0], *s[1:]))))
+def test_logprobs_of_far_rows(ops, spec):
+    (R, V, *_), dtype, tau = spec
+    g, x, targets, sh = case(spec)
+    T, K = x.shape[0], 20
+    op = ops.VocabHead(R, V, dtype, temperature=tau)
+    lp, lse, H = (torch.full((T,), 9.0, device="cuda") for _ in range(3))
+    ids, tlp = torch.full((T, K), -7, device="cuda"), torch.full((T, K), 9.0, device="cuda")
+    op.logprobs(sh, targets, lp, lse, H, ids, tlp)
+    logp, lse64, H64 = stats64(x, tau)
+    same(lse, in_f32(lse64), sum_loss(V) + 8 * E * size(lse64), "lse")
+    want = logp.gather(1, targets[:, None])[:, 0]
+    same(lp, in_f32(want), sum_loss(V) + 8 * E * size(want), "logprob")
+    same(H, H64, (sum_loss(V) + 8 * E) * (2 + math.log(V)), "entropy")
+    assert torch.equal(ids, top_ids64(x, K))
+    want = logp.gather(1, ids)
+    same(tlp, in_f32(want), sum_loss(V) + 8 * E * size(want), "top")
+
+
+def teacher(g, T, V, K):
+    ids = torch.randint(V, (T, K), generator=g, device="cuda")
+    return ids, randn(g, T, K, sigma=3.0)
+
+
+@pytest.mark.parametrize("spec", CASES, ids=lambda s: "-".join(map(str, (*s[0], *s[1:]))))
+def test_distill_of_far_rows(ops, spec):
+    (R, V, *_), dtype, tau = spec
+    g, x, _, sh = case(spec)
+    T, K = x.shape[0], 16
+    ids, t = teacher(g, T, V, K)
+    op = ops.VocabHead(R, V, dtype, temperature=tau)
+    loss, lse = (torch.full((T,), 9.0, device="cuda") for _ in range(2))
+    op.distill(sh, ids, t, loss, lse)
+    logp, lse64, _ = stats64(x, tau)
+    same(lse, in_f32(lse64), sum_loss(V) + 8 * E * size(lse64), "lse")
+    logq = torch.log_softmax(t.double() / tau, 1)
+    q, at = logq.exp(), logp.gather(1, ids)
+    terms = torch.where(q > 0, q * (logq - at), 0.0)
+    mags = torch.where(q > 0, q * (logq.abs() + at.abs()), 0.0)
+    mag, tmag = mags.sum(1), t.double().abs().amax(1) / tau
+    # shares: exp of (t - max) / tau, good to 8 E of that, and lost where they are below binary32's normal range;
+    # terms: K additions and a few products
+    lost = torch.where(q < 2.0 ** -126, 2 * mags, 0.0).sum(1)
+    tol = tau ** 2 * (sum_loss(V) + (K + 64) * E * (1 + mag) + 8 * E * tmag * (1 + mag) + lost)
+    same(loss, in_f32(terms.sum(1) * tau ** 2), tol, "loss")
