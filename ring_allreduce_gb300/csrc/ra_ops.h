@@ -108,6 +108,7 @@ struct VocabBackward {
   const void* teacher;
   int K;
   int teacher_f32;
+  float lift, by_lift;         // a whole number and 2^-lift: see the kernel
 };
 
 cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cudaStream_t st);

@@ -466,6 +466,14 @@ static void set_rows(const ra_vocab_ctx* h, size_t rows, const void* const* shar
   x->inv_tau = 1.0f / h->tau;
 }
 
+// The powers of two that what a probability is multiplied with may reach:
+// `factor`, and a log p of up to 2^7.  (2^lift has to be in binary32's range.)
+static void set_lift(float factor, ra::VocabBackward* a) {
+  const float most = 120.0f, lift = 7.0f + (factor > 1.0f ? std::ceil(std::log2(factor)) : 0.0f);
+  a->lift = lift < most ? lift : most;
+  a->by_lift = std::ldexp(1.0f, -(int)a->lift);
+}
+
 static ra_status vocab_logprobs(ra_vocab_handle h, const ra_vocab_logprobs_args* g, cudaStream_t st) {
   if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
   if (!g) return record_error(RA_ERR_INVALID, "NULL arguments");
@@ -526,6 +534,7 @@ static ra_status vocab_logprobs_backward(ra_vocab_handle h, const ra_vocab_logpr
   a.entropy = g->entropy;
   a.grad_entropy = g->grad_entropy;
   a.g = g->grad_logprob;
+  set_lift(a.x.inv_tau, &a);
   const cudaError_t e = ra::launch_vocab_backward(h->dtype, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "log probabilities' gradient launch");
 }
@@ -584,6 +593,7 @@ static ra_status vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distil
   for (int r = 0; r < h->shards; ++r) a.grad[r] = g->grads[r];
   a.lse = g->lse;
   a.g = g->grad_loss;
+  set_lift(h->tau, &a);
   a.ids = g->teacher_ids;
   a.teacher = g->teacher_logits;
   a.K = g->teacher_k;

@@ -1005,9 +1005,17 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
     }
   }
   if (zero) A = B = 0.0f;
-  // binary32 outputs show the exponent's rounding: expf there
+  // binary32 outputs show the exponent's rounding: expf there.  The others'
+  // 2^t is 0 below 2^-126, where bf16 may still have the product with g / tau and
+  // log p: it takes 2^(t + lift), and the factors 2^-lift.
   constexpr float kUnit = sizeof(T) == 4 ? 1.0f : kLog2e;
-  const float scale = inv_tau * kUnit, ref = -lse * kUnit, slope = B / kUnit;
+  const float lift = std::is_same<D, DBF16>::value ? a.lift : 0.0f;
+  const float scale = inv_tau * kUnit, ref = __fmaf_rn(-lse, kUnit, lift);
+  float slope = B / kUnit;
+  if (std::is_same<D, DBF16>::value) {
+    A = __fmaf_rn(-slope, lift, A) * a.by_lift;   // slope's t below is lift larger
+    slope *= a.by_lift;
+  }
   auto gradient = [&](float2 x) {
     const float2 t = __ffma2_rn(x, make_float2(scale, scale), make_float2(ref, ref));   // log p, in units of kUnit
     const float2 p = sizeof(T) == 4 ? make_float2(expf(t.x), expf(t.y)) : make_float2(exp2_fast(t.x), exp2_fast(t.y));

@@ -15,7 +15,7 @@ import math
 
 import pytest
 
-from test_gpu_operators import E, gen, logits, randn, same, shards_of, stats64, top_ids64
+from test_gpu_operators import E, close, gen, logits, randn, same, shards_of, stats64, top_ids64
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -127,3 +127,27 @@ def test_distill_of_far_rows(ops, spec):
     lost = torch.where(q < 2.0 ** -126, 2 * mags, 0.0).sum(1)
     tol = tau ** 2 * (sum_loss(V) + (K + 64) * E * (1 + mag) + 8 * E * tmag * (1 + mag) + lost)
     same(loss, in_f32(terms.sum(1) * tau ** 2), tol, "loss")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tau", [1e-3, 0.7])
+def test_gradients_of_small_probabilities(ops, dtype, tau):
+    """Probabilities below binary32's normal range, which over a small tau are numbers of the output's type again."""
+    T, V = 9, 1000
+    g = gen(103)
+    x = (tau * (-86.0 - 12.0 * torch.rand((T, V), generator=g, device="cuda"))).to(logits(g, 1, 8, dtype)[0].dtype)
+    x[:, 5] = 0.0
+    sh, targets = shards_of(x, 3), torch.full((T,), 7, device="cuda")
+    op = ops.VocabHead(3, V, dtype, temperature=tau)
+    lp, lse, H = (torch.full((T,), 9.0, device="cuda") for _ in range(3))
+    op.logprobs(sh, targets, lp, lse, H)
+    glp, gH = randn(g, T), randn(g, T, sigma=0.3)
+    grads = [torch.full_like(s, 9.0) for s in sh]
+    op.logprobs_backward(sh, targets, lse, glp, grads, entropy=H, grad_entropy=gH)
+    logp, _, _ = stats64(x, tau)
+    p, gl, gh, h = logp.exp(), *(v.double()[:, None] for v in (glp, gH, H))
+    hit = torch.zeros_like(p).scatter_(1, targets[:, None], gl)
+    want = (hit - p * (gl + gh * h) - gh * p * logp) / tau
+    mag = (hit.abs() + p * (gl.abs() + gh.abs() * (h.abs() + logp.abs() + 1))) / tau
+    # x / tau is below 128 and lse below E: their roundings are 8 E of 128; log p stands as a factor too
+    close(torch.cat(grads, 1), want, mag * (sum_loss(V) + 8 * E * 128), dtype, "logits' gradient")
