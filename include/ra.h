@@ -612,8 +612,11 @@ ra_status ra_vocab_logprobs(ra_vocab_handle h, const ra_vocab_logprobs_args* arg
 /* grads = the gradient of sum_t (grad_logprob_t logprob_t + grad_entropy_t
  * entropy_t) with respect to the logits; lse and entropy are what forward
  * wrote.  Zero in a row that a mask leaves nothing of: lse below -1e30 (-inf
- * everywhere, or the lowest value of RA_F32 or RA_BF16).  grads[r] == shards[r] (same
- * stride) is allowed. */
+ * everywhere, or the lowest value of RA_F32 or RA_BF16).  In any other row with
+ * |lse| above 2^14 (one masked everywhere with -1e9, logits far above zero)
+ * binary32 does not tell the probabilities apart by lse: they are taken from
+ * the logits again, at the price of two more passes by a CTA.
+ * grads[r] == shards[r] (same stride) is allowed. */
 typedef struct ra_vocab_logprobs_backward_args {
   size_t rows;
   const void* const* shards;
@@ -649,7 +652,8 @@ ra_status ra_vocab_distill(ra_vocab_handle h, const ra_vocab_distill_args* args,
 
 /* grads = the gradient of sum_t grad_loss_t loss_t with respect to the
  * student's logits, grad_loss_t temperature (p - q); lse is what forward
- * wrote.  Zero in a row without teacher tokens and in one with lse below -1e30.
+ * wrote.  Zero in a row without teacher tokens and in one with lse below -1e30;
+ * |lse| above 2^14 as for ra_vocab_logprobs_backward.
  * grads[r] == shards[r] (same stride) is allowed. */
 typedef struct ra_vocab_distill_backward_args {
   size_t rows;

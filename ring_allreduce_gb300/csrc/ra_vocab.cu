@@ -53,6 +53,7 @@ constexpr float kFar = 16777216.0f;    // 2^24: a row whose ref would be further
 constexpr float kNoRef = -kFar;        // ref before the first logit above it
 
 constexpr float kNothingLeft = -1e30f;
+constexpr float kSharp = 16384.0f;     // 2^14: binary32 holds an lse of that size to 2^-10, and with it every probability
 
 template <class D> struct NegInf;
 // -inf, and the type's lowest value, ordered()
@@ -908,7 +909,73 @@ struct BackwardShared {
   // what the target or the teacher adds, and at which column (-1: nowhere); each thread's own tokens
   float add[kTeacherMax];
   int at[kTeacherMax];
+  float by_warp[4];                    // of a far row
 };
+
+// A row whose lse is too far from zero to tell its probabilities apart (all of
+// it masked with -1e9, say: lse is good to 32 there).  One CTA takes its
+// largest logit m and log sum e^{(x - m) / tau} again, in two passes, and
+// writes its gradient p (A + B log p) in a third, the tokens' parts on top.
+// (Called, not inlined: rare, and other rows have no register to spare for it.)
+template <class D>
+__device__ __noinline__ void far_gradient(const VocabRows& x, BackwardShared& sh, int tokens, float A, float B) {
+  using T = typename D::T;
+  constexpr int V = D::kVec;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int per = chunks_per_shard(x), chunks = per * x.shards;
+  const float inv_tau = x.inv_tau;
+  uint4 raw[kPerLane];
+  float m = -INFINITY;
+  for (Walk<D> w(sh.rows, per, warp, chunks, warps); w.more(); w.next()) {
+    w.load(raw);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) m = max_nan(m, word_value<D>(vector_max<D>(raw[i])));
+  }
+  m = warp_max_nan(m);
+  if (lane == 0) sh.by_warp[warp] = m;
+  __syncthreads();
+  m = warp_max_nan(lane < warps ? sh.by_warp[lane] : -INFINITY);
+  __syncthreads();
+  float s = 0.0f;
+  for (Walk<D> w(sh.rows, per, warp, chunks, warps); w.more(); w.next()) {
+    w.load(raw);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      float v[V];
+      unpack<D>(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += expf((v[e] - m) * inv_tau);
+    }
+  }
+  s = warp_sum(s);
+  if (lane == 0) sh.by_warp[warp] = s;
+  __syncthreads();
+  const float log_s = logf(warp_sum(lane < warps ? sh.by_warp[lane] : 0.0f));
+  auto gradient = [&](float v) {
+    const float t = __fmaf_rn(v - m, inv_tau, -log_s);
+    return expf(t) * __fmaf_rn(B, fmaxf(t, kFarBelow), A);
+  };
+  for (Walk<D> w(sh.rows, per, warp, chunks, warps); w.more(); w.next()) {
+    w.load(raw);
+    T* out = reinterpret_cast<T*>(sh.grad[w.r]);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      const Slot<D> at = w.at(i);
+      float v[V];
+      unpack<D>(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e >= at.lo && e < at.hi) st_g(out + at.e0 + e, narrow<D>(gradient(v[e])));
+    }
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < tokens; k += blockDim.x) {
+    const int c = sh.at[k];
+    if (c < 0) continue;
+    const int r = c / x.C;
+    st_g(reinterpret_cast<T*>(sh.grad[r]) + (c - r * x.C), narrow<D>(gradient(sh.teacher.x[k]) + sh.add[k]));
+  }
+}
 
 // Every logit is read and its gradient written, element by element; what the
 // target or the teacher adds is put on top after the CTA's columns are
@@ -959,10 +1026,8 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
   __syncthreads();
   // dL_j = p_j (A + B log p_j), plus that
   float A, B = 0.0f;
-  // nothing left by the mask: -inf everywhere, or logits so low (the type's
-  // lowest value) that lse cannot hold the logarithm of their sum beside them
+  // nothing left by the mask: -inf everywhere, or the type's lowest value
   bool zero = row_lse < kNothingLeft;
-  const float lse = zero ? 0.0f : row_lse;
   if constexpr (DISTILL) {
     const Softmax q(sh.teacher, a.K, inv_tau);
     zero = zero || !q.taught();
@@ -1005,6 +1070,13 @@ __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_con
     }
   }
   if (zero) A = B = 0.0f;
+  const float lse = zero ? 0.0f : row_lse;
+  if (fabsf(lse) > kSharp) {
+    // A far row is its first CTA's alone: the others' columns would have to be
+    // read before they are written, where the gradient stands in the logits' place.
+    if (part == 0) far_gradient<D>(a.x, sh, DISTILL ? a.K : 1, A, B);
+    return;
+  }
   // binary32 outputs show the exponent's rounding: expf there.  The others'
   // 2^t is 0 below 2^-126, where bf16 may still have the product with g / tau and
   // log p: it takes 2^(t + lift), and the factors 2^-lift.

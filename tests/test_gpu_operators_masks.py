@@ -20,6 +20,7 @@ from test_gpu_operators import E, close, gen, logits, randn, same, shards_of, st
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
+NO_GRADIENT = -1e30   # rows with a smaller lse have none
 FILLS = {"f32": (-1e5, -1e7, -1e9, -1e10, -1e20, -1e30, -1e37, -3e38),
          "bf16": (-1e5, -1e7, -1e9, -1e10, -1e20, -1e30, -1e37, -3e38), "f16": (-1e3, -2e4, -6e4)}
 KINDS = 7
@@ -127,6 +128,84 @@ def test_distill_of_far_rows(ops, spec):
     lost = torch.where(q < 2.0 ** -126, 2 * mags, 0.0).sum(1)
     tol = tau ** 2 * (sum_loss(V) + (K + 64) * E * (1 + mag) + 8 * E * tmag * (1 + mag) + lost)
     same(loss, in_f32(terms.sum(1) * tau ** 2), tol, "loss")
+
+
+def p_loss(x, tau, lse, logp, V):
+    """What a probability loses, relative: the sum's loss and, where lse tells probabilities apart (|lse| up to 2^14),
+    the roundings of x / tau and lse; else those of x - max alone."""
+    sharp = (lse.abs() <= 2.0 ** 14)[:, None]
+    far = torch.where(sharp, size(x.double() / tau) + size(lse.double())[:, None], 0.0)
+    return torch.clamp(sum_loss(V) + 8 * E * (far + 1 + size(logp).clamp(max=150.0)), max=1.0)
+
+
+@pytest.mark.parametrize("spec", CASES, ids=lambda s: "-".join(map(str, (*s[0], *s[1:]))))
+def test_logprob_gradient_of_far_rows(ops, spec):
+    """The gradient from the rows' own softmax in 64 bits, not from the lse that forward wrote."""
+    (R, V, *_), dtype, tau = spec
+    g, x, targets, sh = case(spec)
+    T = x.shape[0]
+    op = ops.VocabHead(R, V, dtype, temperature=tau)
+    lp, lse, H = (torch.full((T,), 9.0, device="cuda") for _ in range(3))
+    op.logprobs(sh, targets, lp, lse, H)
+    glp, gH = randn(g, T), randn(g, T, sigma=0.3)
+    grads = [torch.full_like(s, 9.0) for s in sh]
+    op.logprobs_backward(sh, targets, lse, glp, grads, entropy=H, grad_entropy=gH)
+
+    logp, _, _ = stats64(x, tau)
+    none = (lse < NO_GRADIENT)[:, None]
+    p = torch.where(none, 0.0, logp.exp())
+    gl, gh, h = (v.double()[:, None] for v in (glp, gH, H))
+    plogp = torch.where(p > 0, p * logp, 0.0)
+    hit = torch.where(none, 0.0, torch.zeros_like(p).scatter_(1, targets[:, None], gl))
+    want = (hit - p * (gl + gh * h) - gh * plogp) / tau
+    mag = (hit.abs() + p * (gl.abs() + gh.abs() * h.abs()) + gh.abs() * plogp.abs() + gh.abs() * p) / tau
+    close(torch.cat(grads, 1), want, mag * p_loss(x, tau, lse, logp, V), dtype, "logits' gradient")
+    keep = torch.cat(grads, 1)
+    op.logprobs_backward(sh, targets, lse, glp, sh, entropy=H, grad_entropy=gH)
+    assert torch.equal(torch.cat(sh, 1), keep)
+
+
+@pytest.mark.parametrize("spec", CASES, ids=lambda s: "-".join(map(str, (*s[0], *s[1:]))))
+def test_distill_gradient_of_far_rows(ops, spec):
+    (R, V, *_), dtype, tau = spec
+    g, x, _, sh = case(spec)
+    T, K = x.shape[0], 16
+    ids, t = teacher(g, T, V, K)
+    op = ops.VocabHead(R, V, dtype, temperature=tau)
+    loss, lse = (torch.full((T,), 9.0, device="cuda") for _ in range(2))
+    op.distill(sh, ids, t, loss, lse)
+    gl = randn(g, T, mean=1.0, sigma=0.2)
+    grads = [torch.full_like(s, 9.0) for s in sh]
+    op.distill_backward(sh, ids, t, lse, gl, grads)
+
+    logp, _, _ = stats64(x, tau)
+    none = (lse < NO_GRADIENT)[:, None]
+    p = torch.where(none, 0.0, logp.exp())
+    q = torch.softmax(t.double() / tau, 1)
+    qs = torch.where(none, 0.0, torch.zeros_like(p).scatter_add_(1, ids, q))
+    c = gl.double()[:, None] * tau
+    tmag = (t.double().abs().amax(1) / tau)[:, None]
+    slack = p * p_loss(x, tau, lse, logp, V) + torch.clamp((K + 64 + 8 * tmag) * E, max=1.0) * qs + 4 * E * (p + qs)
+    close(torch.cat(grads, 1), c * (p - qs), c.abs() * slack, dtype, "logits' gradient")
+    keep = torch.cat(grads, 1)
+    op.distill_backward(sh, ids, t, lse, gl, sh)
+    assert torch.equal(torch.cat(sh, 1), keep)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_far_row_alone(ops, dtype):
+    """One row over many CTAs, nothing left by a mask of -1e10: its gradient is that of equal probabilities, in place too."""
+    V, R = 131072, 8
+    x = torch.full((1, V), -1e10, device="cuda").to(logits(gen(1), 1, 8, dtype)[0].dtype)
+    sh, targets = shards_of(x, R), torch.tensor([77777], device="cuda")
+    op = ops.VocabHead(R, V, dtype)
+    lp, lse, one = (torch.ones(1, device="cuda") for _ in range(3))
+    op.logprobs(sh, targets, lp, lse)
+    assert abs(lp.item() + math.log(V)) <= 1e-5
+    op.logprobs_backward(sh, targets, lse, one, sh)
+    want = torch.full((1, V), -1.0 / V, dtype=torch.float64, device="cuda")
+    want[0, 77777] += 1.0
+    close(torch.cat(sh, 1), want, sum_loss(V) * want.abs(), dtype, "logits' gradient")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
