@@ -593,7 +593,8 @@ ra_status ra_vocab_set_option(ra_vocab_handle h, int key, long long value);   /*
  * x_target - lse (0 where the target is negative, NaN where it is no column);
  * entropy = -sum_j p_j log p_j; the `top` largest logits' columns in falling
  * order (equal ones: the lower column first; -0 equals +0, NaN is largest)
- * and their log probabilities.  A row of nothing but -inf has lse -inf, log
+ * and their log probabilities.  No log probability is above 0 and no entropy
+ * below it.  A row of nothing but -inf has lse -inf, log
  * probabilities -inf and entropy 0; a row with +inf or NaN has NaN. */
 typedef struct ra_vocab_logprobs_args {
   size_t rows;

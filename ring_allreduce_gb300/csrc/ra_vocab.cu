@@ -765,6 +765,9 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const float lse = empty ? -INFINITY
                     : far ? __fmaf_rn(row_max, a.x.inv_tau, kLn2 * log2_s)
                           : kLn2 * (st.ref + log2_s);
+  // A row of one token has log2 s - t of a rounding's size, on either side of 0:
+  // what cannot be below 0 is held there.  (NaN stays.)
+  auto not_below = [](float v) { return v < 0.0f ? 0.0f : v; };
   // log p of a logit, or tau times that
   auto log_prob = [&](float x, bool by_tau = false) {
     if (empty) return -INFINITY;
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
     const float t = __fmaf_rn(d, scale, far ? 0.0f : -st.ref);
     // a masked logit near the type's lowest value leaves binary32's range in t before it does so itself
     return t == -INFINITY && log2_s == log2_s ? (by_tau ? d : d * a.x.inv_tau)
-                                                  : (by_tau ? kLn2 * a.x.tau : kLn2) * (t - log2_s);
+                                                  : (by_tau ? kLn2 * a.x.tau : kLn2) * -not_below(log2_s - t);
   };
   const bool first = part == 0;
   if (first && tid == 0) st_g(a.lse + row, lse);
@@ -795,7 +798,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   } else {
     if (first && tid == 0) {
       st_g(a.logprob + row, sh.target == -1 ? 0.0f : sh.target == -2 ? NAN : log_prob(sh.target_logit));
-      if (a.entropy) st_g(a.entropy + row, empty ? 0.0f : kLn2 * (log2_s - st.u / st.s));
+      if (a.entropy) st_g(a.entropy + row, empty ? 0.0f : kLn2 * not_below(log2_s - st.u / st.s));
     }
     if (a.top > 0) {
       // A bound that K threads' maxima reach: their K-th largest, cut to 16

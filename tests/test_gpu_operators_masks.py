@@ -230,3 +230,26 @@ def test_gradients_of_small_probabilities(ops, dtype, tau):
     mag = (hit.abs() + p * (gl.abs() + gh.abs() * (h.abs() + logp.abs() + 1))) / tau
     # x / tau is below 128 and lse below E: their roundings are 8 E of 128; log p stands as a factor too
     close(torch.cat(grads, 1), want, mag * (sum_loss(V) + 8 * E * 128), dtype, "logits' gradient")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.3])
+def test_no_entropy_below_zero_and_no_probability_above_one(ops, dtype, tau):
+    """Rows with one allowed token (constrained decoding), and rows where one token leaves the others next to nothing."""
+    T, V, R = 512, 4099, 4
+    g = gen(111)
+    x = randn(g, T, V, dtype=dtype)
+    targets = torch.randint(V, (T,), generator=g, device="cuda")
+    rows = torch.arange(T, device="cuda")
+    own = x[rows, targets].clone()
+    x[: T // 2] = -math.inf
+    x[rows, targets] = torch.where(rows < T // 2, own, (own.float() + 30.0).to(x.dtype))
+    op = ops.VocabHead(R, V, dtype, temperature=tau)
+    lp, lse, H = (torch.full((T,), 9.0, device="cuda") for _ in range(3))
+    ids, tlp = torch.zeros((T, 3), dtype=torch.int64, device="cuda"), torch.zeros((T, 3), device="cuda")
+    op.logprobs(shards_of(x, R), targets, lp, lse, H, ids, tlp)
+    assert (H >= 0).all() and (lp <= 0).all() and (tlp <= 0).all(), (H.min(), lp.max(), tlp.max())
+    assert torch.equal(ids[:, 0], targets) and torch.equal(tlp[:, 0], lp)
+    logp, _, H64 = stats64(x, tau)
+    same(lp, logp[rows, targets], sum_loss(V), "logprob")
+    same(H, H64, (sum_loss(V) + 8 * E) * (2 + math.log(V)), "entropy")
