@@ -497,7 +497,8 @@ ra_status ra_debug_bounds_report(unsigned long long* count, unsigned long long* 
  * whole 16-byte vectors are fastest.  An output may not overlap another
  * buffer of the call, except where a call says so; buffers with the same
  * stride whose columns are disjoint (column slices of one matrix) do not
- * overlap.  Calls with no rows return RA_OK.  The types are RA_F32, RA_BF16 and RA_F16 (others:
+ * overlap.  Calls with no rows return RA_OK; ra_norm_backward then writes
+ * zeros to the sums over the rows that it is given.  The types are RA_F32, RA_BF16 and RA_F16 (others:
  * RA_ERR_UNSUPPORTED); sums, statistics and log probabilities are held in
  * binary32 and every output is rounded once (the sum over ranks runs in rank
  * order in binary32, not in the ring's order with its rounding at every hop).
@@ -553,7 +554,8 @@ ra_status ra_norm_forward(ra_norm_handle h, const ra_norm_forward_args* args, vo
  * next projections give (`grads` of them, summed here), grad_residual_out that
  * of residual_out.  grad_residual == grad_residual_out (same stride) and
  * grad_in[q] == grad_out[q] (same stride) are allowed.  Weight and gate
- * gradients are binary32 sums over the rows, in a fixed order; each may be NULL. */
+ * gradients are binary32 sums over the rows (of no rows: zero, for gate_rows
+ * gate rows), in a fixed order; each may be NULL. */
 typedef struct ra_norm_backward_args {
   size_t rows;
   const void* const* grad_out;     /* `grads` buffers [rows][dim] of dtype */

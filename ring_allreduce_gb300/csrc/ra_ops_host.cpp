@@ -323,19 +323,40 @@ static ra_status norm_forward(ra_norm_handle h, const ra_norm_forward_args* g, c
   return e == cudaSuccess ? RA_OK : cuda_error(e, "norm forward launch");
 }
 
+// The sums over no rows: zeros, in every gate row there is.
+static ra_status norm_backward_no_rows(ra_norm_handle h, const ra_norm_backward_args* g, cudaStream_t st) {
+  const size_t dim = (size_t)h->dim;
+  if (g->grad_gate) RA_TRY(check_rows(g->gate_rows));
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+  const struct { const char* name; float* p; size_t count; } sums[3] = {
+      {"grad_weight", g->grad_weight, dim},
+      {"grad_post_weight", g->grad_post_weight, dim},
+      {"grad_gate", g->gate_rows ? g->grad_gate : nullptr, g->gate_rows * dim}};
+  Buffers buf(h->device, h->check_pointers, 1);
+  for (const auto& s : sums)
+    if (s.p) RA_TRY(buf.flat(s.name, s.p, 4, s.count, true));
+  RA_TRY(buf.check());
+  for (const auto& s : sums) {
+    const cudaError_t e = s.p ? cudaMemsetAsync(s.p, 0, s.count * sizeof(float), st) : cudaSuccess;
+    if (e != cudaSuccess) return cuda_error(e, s.name);
+  }
+  return RA_OK;
+}
+
 static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g, cudaStream_t st) {
   if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
   if (!g) return record_error(RA_ERR_INVALID, "NULL arguments");
   const size_t dim = (size_t)h->dim;
-  if (g->rows == 0) return RA_OK;
+  if (g->grad_post_weight && !g->post_weight)
+    return record_error(RA_ERR_INVALID, "grad_post_weight without post_weight");
+  if (g->grad_gate && !g->gate) return record_error(RA_ERR_INVALID, "grad_gate without gate");
+  if (g->rows == 0) return norm_backward_no_rows(h, g, st);
   RA_TRY(check_rows(g->rows));
   RA_TRY(check_gate(g->gate, g->gate_rows, g->rows));
   RA_TRY(check_ranks("grads", g->grads, h->R));
   RA_TRY(check_ranks("outs", g->outs, h->R));
   if (!g->grad_out || !g->grad_in) return record_error(RA_ERR_INVALID, "NULL pointer array");
-  if (g->grad_post_weight && !g->post_weight)
-    return record_error(RA_ERR_INVALID, "grad_post_weight without post_weight");
-  if (g->grad_gate && !g->gate) return record_error(RA_ERR_INVALID, "grad_gate without gate");
   const bool need_total = g->post_weight || g->grad_gate;
   OnDevice on(h->device);
   if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");

@@ -160,7 +160,7 @@ class BlockNorm(_Handle):
         post_weight or grad_gate).  Writes grad_ins, 1 or R x [T, dim] (the
         gradient of every rank's partial), grad_residual [T, dim], and, in
         float32, grad_weight [dim], grad_post_weight [dim] and grad_gate
-        [G, dim] where given.  grad_residual may be grad_residual_out, and
+        [G, dim] where given: sums over the rows, zero where T is 0.  grad_residual may be grad_residual_out, and
         grad_ins may be grad_outs."""
         args = (grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins, grad_residual, grad_weight,
                 post_weight, gate, total, grad_post_weight, grad_gate)
