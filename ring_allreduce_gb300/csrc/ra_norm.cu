@@ -6,9 +6,10 @@ namespace ra {
 namespace norm {
 
 #define RA_NORM_EXTERN(D, RD)                                                                                      \
-  extern template cudaError_t run_forward<D, RD>(const Shape&, bool, const NormForward&, unsigned, cudaStream_t);   \
-  extern template cudaError_t run_backward<D, RD>(const Shape&, bool, const NormBackward&, const Deal&, unsigned,   \
-                                                  cudaStream_t);
+  extern template cudaError_t run_forward<D, RD>(const Shape&, bool, const NormForward&, OptedIn&, unsigned,        \
+                                                 cudaStream_t);                                                     \
+  extern template cudaError_t run_backward<D, RD>(const Shape&, bool, const NormBackward&, const Deal&, OptedIn&,   \
+                                                  unsigned, cudaStream_t);
 RA_NORM_EXTERN(DF32, DF32)
 RA_NORM_EXTERN(DBF16, DBF16)
 RA_NORM_EXTERN(DBF16, DF32)
@@ -98,21 +99,23 @@ size_t norm_workspace_floats(int dim, int sms) {
   return 4 * most * (size_t)dim;
 }
 
-cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormForward& a, int sms, cudaStream_t st) {
+cudaError_t launch_norm_forward(int dtype, int rdtype, bool aligned, const NormForward& a, int sms, OptedIn& opted,
+                                cudaStream_t st) {
   const Shape s = forward_shape(a.dim, vec_of(dtype), a.rows >= 2 * (int64_t)sms);
   const int64_t per = s.rows * (aligned ? s.packs : 1), want = (a.rows + per - 1) / per, most = most_ctas(s, sms);
   const unsigned grid = (unsigned)(want < most ? want : most);
   return with_types(dtype, rdtype, [&](auto d, auto r) {
-    return run_forward<decltype(d), decltype(r)>(s, aligned, a, grid, st);
+    return run_forward<decltype(d), decltype(r)>(s, aligned, a, opted, grid, st);
   });
 }
 
-cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const NormBackward& a, int sms, cudaStream_t st) {
+cudaError_t launch_norm_backward(int dtype, int rdtype, bool aligned, const NormBackward& a, int sms, OptedIn& opted,
+                                 cudaStream_t st) {
   const Shape s = backward_shape(a.dim, vec_of(dtype), a.rows >= 2 * (int64_t)sms);
   const Deal dl = make_deal(a, s, sms);
   const unsigned grid = (unsigned)dl.ctas;
   cudaError_t e = with_types(dtype, rdtype, [&](auto d, auto r) {
-    return run_backward<decltype(d), decltype(r)>(s, aligned, a, dl, grid, st);
+    return run_backward<decltype(d), decltype(r)>(s, aligned, a, dl, opted, grid, st);
   });
   if (e != cudaSuccess) return e;
   const bool gates = a.grad_gate && dl.parts > 1;

@@ -764,24 +764,33 @@ template <class D, class F> cudaError_t with_groups(int groups, F&& f) {
   return cudaErrorInvalidValue;
 }
 
-// The ring's shared memory, opted in to.
-template <class C, class K> cudaError_t ring_bytes(K kernel, const Shape& s, size_t* bytes) {
-  *bytes = (size_t)C::kDepth * C::kQ * C::kWarpBytes * (s.threads / 32) * s.rows;
-  if (*bytes <= 40 * 1024) return cudaSuccess;   // 48 KB, the static part included, need no opt-in
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*bytes);
+// One launch, with the ring's shared memory.  The kernel is opted in to the
+// most that its CTAs may ask for, once a handle, and never to less: the
+// attribute is the kernel's, and calls of other widths may be on their way from
+// other host threads.
+template <class C, class... P, class... A>
+cudaError_t launch_ring(void (*kernel)(P...), const Shape& s, int most, OptedIn& opted, unsigned grid, cudaStream_t st,
+                        const A&... args) {
+  constexpr size_t warp = (size_t)C::kDepth * C::kQ * C::kWarpBytes;
+  const size_t bytes = warp * (s.threads / 32) * s.rows;
+  if (bytes > 40 * 1024 && !opted.has((const void*)kernel)) {   // 48 KB, the static part included, need no opt-in
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(warp * (most / 32)));
+    if (e != cudaSuccess) return e;
+    opted.add((const void*)kernel);
+  }
+  return launch_after(kernel, dim3(grid), dim3(s.threads, s.rows), bytes, st, 1, args...);
 }
 
 template <class D, class RD>
-cudaError_t run_forward(const Shape& s, bool aligned, const NormForward& a, unsigned grid, cudaStream_t st) {
+cudaError_t run_forward(const Shape& s, bool aligned, const NormForward& a, OptedIn& opted, unsigned grid,
+                        cudaStream_t st) {
   cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
   return with_groups<D>(s.groups, [&](auto g) {
     constexpr int kGroups = decltype(g)::value;
-    auto launch = [&](auto kernel, auto al) {
-      size_t smem;   // (a packed row's slots are a vector a lane, too)
-      const cudaError_t e2 = ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, 1024>>(kernel, s, &smem);
-      if (e2 != cudaSuccess) return e2;
-      return launch_after(kernel, dim3(grid), dim3(s.threads, s.rows), smem, st, 1, a);
+    auto launch = [&](auto kernel, auto al) {   // (a packed row's slots are a vector a lane, too)
+      return launch_ring<Cols<D, kGroups, decltype(al)::value != 0, 1024>>(kernel, s, 1024, opted, grid, st, a);
     };
     if constexpr (kGroups == 1)
       if (aligned && s.packs > 1) return launch(norm_forward_kernel<D, RD, 1, true, 1024, true>, IntC<1>{});
@@ -791,18 +800,15 @@ cudaError_t run_forward(const Shape& s, bool aligned, const NormForward& a, unsi
 }
 
 template <class D, class RD>
-cudaError_t run_backward(const Shape& s, bool aligned, const NormBackward& a, const Deal& d, unsigned grid,
-                         cudaStream_t st) {
+cudaError_t run_backward(const Shape& s, bool aligned, const NormBackward& a, const Deal& d, OptedIn& opted,
+                         unsigned grid, cudaStream_t st) {
   cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
   return with_groups<D>(s.groups, [&](auto g) {
     constexpr int kGroups = decltype(g)::value;
     auto launch = [&](auto kernel, auto al, auto most) {
-      size_t smem;
-      const cudaError_t e2 =
-          ring_bytes<Cols<D, kGroups, decltype(al)::value != 0, decltype(most)::value>>(kernel, s, &smem);
-      if (e2 != cudaSuccess) return e2;
-      return launch_after(kernel, dim3(grid), dim3(s.threads, s.rows), smem, st, 1, a, d);
+      constexpr int kMost = decltype(most)::value;
+      return launch_ring<Cols<D, kGroups, decltype(al)::value != 0, kMost>>(kernel, s, kMost, opted, grid, st, a, d);
     };
     if constexpr (kGroups * D::kVec == 16) {
       if (s.most == 1024) {

@@ -5,9 +5,10 @@
 namespace ra {
 namespace norm {
 
-template cudaError_t run_forward<RA_INST_D, RA_INST_RD>(const Shape&, bool, const NormForward&, unsigned, cudaStream_t);
-template cudaError_t run_backward<RA_INST_D, RA_INST_RD>(const Shape&, bool, const NormBackward&, const Deal&, unsigned,
-                                                         cudaStream_t);
+template cudaError_t run_forward<RA_INST_D, RA_INST_RD>(const Shape&, bool, const NormForward&, OptedIn&, unsigned,
+                                                        cudaStream_t);
+template cudaError_t run_backward<RA_INST_D, RA_INST_RD>(const Shape&, bool, const NormBackward&, const Deal&, OptedIn&,
+                                                         unsigned, cudaStream_t);
 
 }  // namespace norm
 }  // namespace ra

@@ -58,11 +58,26 @@ struct NormBackward {
   float scale;
 };
 
+// The kernels that a handle has opted in to their shared memory: a forward and
+// a backward one for few and for many rows, aligned or not.
+struct OptedIn {
+  const void* kernels[8] = {};
+  int count = 0;
+  bool has(const void* k) const {
+    for (int i = 0; i < count; ++i)
+      if (kernels[i] == k) return true;
+    return false;
+  }
+  void add(const void* k) {
+    if (count < 8) kernels[count++] = k;
+  }
+};
+
 // aligned: every row of every buffer starts on a 16-byte boundary and holds whole 16-byte vectors
 cudaError_t launch_norm_forward(int dtype, int residual_dtype, bool aligned, const NormForward& a, int sms,
-                                cudaStream_t st);
+                                OptedIn& opted, cudaStream_t st);
 cudaError_t launch_norm_backward(int dtype, int residual_dtype, bool aligned, const NormBackward& a, int sms,
-                                 cudaStream_t st);
+                                 OptedIn& opted, cudaStream_t st);
 // Floats of column partials a backward call of this width may use.
 size_t norm_workspace_floats(int dim, int sms);
 

@@ -20,6 +20,7 @@ struct ra_norm_ctx {
   float eps, scale;
   bool check_pointers = true;
   float* work = nullptr;   // column partials of the weights' gradients, from the first backward call on
+  ra::OptedIn opted;
 };
 
 struct ra_vocab_ctx {
@@ -319,7 +320,7 @@ static ra_status norm_forward(ra_norm_handle h, const ra_norm_forward_args* g, c
   a.param_f32 = h->param_dtype == RA_F32;
   a.eps = h->eps;
   a.scale = h->scale;
-  const cudaError_t e = ra::launch_norm_forward(h->dtype, h->residual_dtype, aligned, a, h->sms, st);
+  const cudaError_t e = ra::launch_norm_forward(h->dtype, h->residual_dtype, aligned, a, h->sms, h->opted, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "norm forward launch");
 }
 
@@ -429,7 +430,7 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
   a.dim = h->dim;
   a.param_f32 = h->param_dtype == RA_F32;
   a.scale = h->scale;
-  const cudaError_t e = ra::launch_norm_backward(h->dtype, h->residual_dtype, aligned, a, h->sms, st);
+  const cudaError_t e = ra::launch_norm_backward(h->dtype, h->residual_dtype, aligned, a, h->sms, h->opted, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "norm backward launch");
 }
 

@@ -1,5 +1,8 @@
 """How the model operators may be called."""
 
+import ctypes
+import threading
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +53,47 @@ def test_refusals_without_rows(ops):
         with pytest.raises(RAError) as err:
             op.backward([e], None, e, r, w, [e], e, **kw)
         assert err.value.status == Status.ERR_INVALID
+
+
+class ForwardArgs(ctypes.Structure):   # ra_norm_forward_args
+    _fields_ = [(n, ctypes.c_int if n == "outs" else ctypes.c_size_t if n == "rows" or n.endswith("stride") or
+                 n == "gate_rows" else ctypes.c_void_p) for n in
+                ("rows in in_stride residual residual_stride weight post_weight gate gate_rows out out_stride outs "
+                 "residual_out residual_out_stride total total_stride rstd").split()]
+
+
+def test_widths_from_two_host_threads(ops):
+    """Handles of one type and two widths, each called from a host thread of its own through the C entries: their
+    launches need different amounts of shared memory of one kernel."""
+    from ring_allreduce_gb300 import binding
+    lib, T = binding._lib, 320
+    failures = []
+
+    def work(dim):
+        h, st = ctypes.c_void_p(), torch.cuda.Stream()
+        assert lib.ra_norm_create(1, dim, 1, 1, 1, 1e-6, 1.0, ctypes.byref(h)) == 0
+        with torch.cuda.stream(st):
+            b = [torch.ones((T, dim), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+            w = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+        st.synchronize()
+        ins, outs = (ctypes.c_void_p * 1)(b[0].data_ptr()), (ctypes.c_void_p * 1)(b[1].data_ptr())
+        a = ForwardArgs(rows=T, in_stride=dim, residual=b[2].data_ptr(), residual_stride=dim, weight=w.data_ptr(),
+                        out=ctypes.addressof(outs), out_stride=dim, outs=1, residual_out=b[3].data_ptr(),
+                        residual_out_stride=dim)
+        setattr(a, "in", ctypes.addressof(ins))
+        for _ in range(3000):
+            status = lib.ra_norm_forward(h, ctypes.addressof(a), st.cuda_stream)
+            if status:
+                failures.append((dim, status, binding.ra_last_error()))
+                break
+        st.synchronize()
+        if not (b[3] == 2).all():
+            failures.append((dim, "residual_out"))
+        lib.ra_norm_destroy(h)
+
+    threads = [threading.Thread(target=work, args=(dim,)) for dim in (8192, 16384, 12288)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
