@@ -504,7 +504,8 @@ ra_status ra_debug_bounds_report(unsigned long long* count, unsigned long long* 
  * order in binary32, not in the ring's order with its rounding at every hop).
  * Results are the same on every run.  Calls are asynchronous on `stream` and
  * may be captured into CUDA graphs, except the first ra_norm_backward of a
- * handle, which allocates its workspace.  A handle is used by one host thread
+ * handle, which allocates its workspace; a graph shares in that and may be
+ * replayed when the handle is destroyed.  A handle is used by one host thread
  * at a time; ra_norm_backward calls of one handle must be ordered (they share
  * that workspace), all other calls may overlap. */
 typedef struct ra_norm_ctx* ra_norm_handle;
@@ -516,7 +517,8 @@ typedef struct ra_vocab_ctx* ra_vocab_handle;
  * multiplies the block's contribution to the residual stream. */
 ra_status ra_norm_create(int R, int dim, ra_dtype dtype, ra_dtype residual_dtype, ra_dtype param_dtype, float eps,
                          float scale, ra_norm_handle* out);
-/* Free the handle after synchronising the device.  NULL is a no-op. */
+/* Free the handle after synchronising the device; the workspace goes with the
+ * last graph that captured a backward call.  NULL is a no-op. */
 ra_status ra_norm_destroy(ra_norm_handle h);
 
 /* RA_OPT_CHECK_POINTERS as for ra_set_option: 1 (default), every call checks

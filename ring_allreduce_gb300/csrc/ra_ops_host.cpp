@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 #include <new>
 
 #include "ra.h"
@@ -14,12 +15,59 @@ namespace ra {
 ra_status record_error(ra_status s, const char* fmt, ...);   // ra_host.cpp
 }
 
+namespace {
+
+// Device memory of a handle.  Graphs that captured a call which uses it share
+// it with the handle (`shared`, once there are any), and may be replayed when
+// the handle is gone.  The last of them to go hands it over to retire(), on a
+// thread of the driver's that may call nothing of CUDA: it waits in a list until
+// a later call frees it.
+struct Workspace {
+  void* p = nullptr;
+  cudaUserObject_t shared = nullptr;
+  Workspace* next = nullptr;
+};
+
+struct Retired {
+  std::mutex lock;
+  Workspace* first = nullptr;
+};
+Retired& retired() {
+  static Retired* r = new Retired;   // never destroyed: the driver's thread may outlive static objects
+  return *r;
+}
+
+void CUDART_CB retire(void* w) {
+  Retired& r = retired();
+  std::lock_guard<std::mutex> hold(r.lock);
+  static_cast<Workspace*>(w)->next = r.first;
+  r.first = static_cast<Workspace*>(w);
+}
+
+void free_retired() {
+  Workspace* w;
+  {
+    Retired& r = retired();
+    std::lock_guard<std::mutex> hold(r.lock);
+    w = r.first;
+    r.first = nullptr;
+  }
+  while (w) {
+    Workspace* next = w->next;
+    cudaFree(w->p);
+    delete w;
+    w = next;
+  }
+}
+
+}  // namespace
+
 struct ra_norm_ctx {
   int R, dim, device, sms;
   ra_dtype dtype, residual_dtype, param_dtype;
   float eps, scale;
   bool check_pointers = true;
-  float* work = nullptr;   // column partials of the weights' gradients, from the first backward call on
+  Workspace* work = nullptr;   // column partials of the weights' gradients, from the first backward call on
   ra::OptedIn opted;
 };
 
@@ -390,20 +438,31 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
   if (g->grad_post_weight) RA_TRY(buf.flat("grad_post_weight", g->grad_post_weight, 4, dim, true));
   RA_TRY(buf.flat("rstd", g->rstd, 4, 2 * g->rows, false));
   const size_t work_bytes = ra::norm_workspace_floats(h->dim, h->sms) * sizeof(float);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaGraph_t graph = nullptr;
+  cudaError_t e = cudaStreamGetCaptureInfo(st, &cap, nullptr, &graph, nullptr, nullptr, nullptr);
+  if (e != cudaSuccess) return cuda_error(e, "cudaStreamGetCaptureInfo");
   if (!h->work) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(st, &cap);
-    if (e != cudaSuccess) return cuda_error(e, "cudaStreamIsCapturing");
     if (cap != cudaStreamCaptureStatusNone)
       return record_error(RA_ERR_UNSUPPORTED, "the first backward call allocates: make it before the capture");
-    e = cudaMalloc(&h->work, work_bytes);
+    free_retired();
+    Workspace* w = new (std::nothrow) Workspace();
+    if (!w) return record_error(RA_ERR_OOM, "host allocation failed");
+    e = cudaMalloc(&w->p, work_bytes);
     if (e != cudaSuccess) {
-      h->work = nullptr;
+      delete w;
       return cuda_error(e, "column partials allocation");
     }
+    h->work = w;
   }
-  RA_TRY(buf.flat("workspace", h->work, 4, work_bytes / 4, true));
+  RA_TRY(buf.flat("workspace", h->work->p, 4, work_bytes / 4, true));
   RA_TRY(buf.check());
+  if (cap == cudaStreamCaptureStatusActive) {
+    cudaUserObject_t& shared = h->work->shared;
+    e = shared ? cudaSuccess : cudaUserObjectCreate(&shared, h->work, retire, 1, cudaUserObjectNoDestructorSync);
+    if (e == cudaSuccess) e = cudaGraphRetainUserObject(graph, shared, 1, 0);
+    if (e != cudaSuccess) return cuda_error(e, "the graph's share in the workspace");
+  }
   a.grad_residual_out = g->grad_residual_out;
   a.residual_out = g->residual_out;
   a.total = need_total ? g->total : nullptr;
@@ -415,7 +474,7 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
   a.grad_weight = g->grad_weight;
   a.grad_post_weight = g->grad_post_weight;
   a.grad_gate = g->grad_gate;
-  a.work = h->work;
+  a.work = static_cast<float*>(h->work->p);
   a.rows = (int64_t)g->rows;
   a.grad_out_stride = (int64_t)go_stride;
   a.grad_in_stride = (int64_t)gi_stride;
@@ -430,7 +489,7 @@ static ra_status norm_backward(ra_norm_handle h, const ra_norm_backward_args* g,
   a.dim = h->dim;
   a.param_f32 = h->param_dtype == RA_F32;
   a.scale = h->scale;
-  const cudaError_t e = ra::launch_norm_backward(h->dtype, h->residual_dtype, aligned, a, h->sms, h->opted, st);
+  e = ra::launch_norm_backward(h->dtype, h->residual_dtype, aligned, a, h->sms, h->opted, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "norm backward launch");
 }
 
@@ -646,7 +705,13 @@ ra_status ra_norm_destroy(ra_norm_handle h) {
     {
       OnDevice on(h->device);
       const cudaError_t e = h->work ? cudaDeviceSynchronize() : cudaSuccess;
-      if (h->work) cudaFree(h->work);
+      if (h->work && h->work->shared) {
+        cudaUserObjectRelease(h->work->shared, 1);   // graphs may have it still
+      } else if (h->work) {
+        cudaFree(h->work->p);
+        delete h->work;
+        free_retired();
+      }
       if (e != cudaSuccess) s = cuda_error(e, "synchronise before destroy");
     }
     delete h;

@@ -1,6 +1,7 @@
 """How the model operators may be called."""
 
 import ctypes
+import gc
 import threading
 
 import pytest
@@ -97,3 +98,57 @@ def test_widths_from_two_host_threads(ops):
     for t in threads:
         t.join()
     assert not failures, failures
+
+
+def backward_case(R, T, D):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")   # noqa: E731
+    return ([r(T, D) for _ in range(R)], r(T, D), r(T, D), r(2, T).abs(), r(D)), ([r(T, D)], r(T, D), r(D))
+
+
+def test_a_graph_outlives_its_handle(ops):
+    """A captured backward pass keeps the handle's workspace: the handle may be closed, and other handles made."""
+    args, want = backward_case(2, 700, 512)
+    outs = [want[0][0], want[1], want[2]]
+    got = [torch.zeros_like(o) for o in outs]
+    op = ops.BlockNorm(2, 512, "f32")
+    op.backward(*args, want[0], want[1], want[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.backward(*args, [got[0]], got[1], got[2])
+    op.close()
+    del op
+    gc.collect()
+    other = ops.BlockNorm(2, 512, "f32")
+    sums = torch.zeros_like(want[2])
+    for _ in range(3):
+        for t in got:
+            t.fill_(9.0)
+        graph.replay()
+        other.backward(*[[2 * p for p in args[0]], *args[1:]], [torch.empty_like(want[1])], torch.empty_like(want[1]), sums)
+        for a, b in zip(got, outs):
+            assert torch.equal(a, b)
+
+
+def test_workspaces_are_given_back(ops):
+    """Closed handles and dropped graphs leave no device memory behind (a workspace here has 40 MB)."""
+    args, (gin, gh, gw) = backward_case(1, 4, 16384)
+    graph = None
+
+    def one():
+        nonlocal graph
+        op = ops.BlockNorm(1, 16384, "f32")
+        op.backward(*args, gin, gh, gw)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            op.backward(*args, gin, gh, gw)
+            op.backward(*args, gin, gh, gw)
+        op.close()
+        graph.replay()
+        torch.cuda.synchronize()
+
+    one()
+    before = torch.cuda.mem_get_info()[0]
+    for _ in range(40):
+        one()
+    assert before - torch.cuda.mem_get_info()[0] < 400 << 20
