@@ -14,7 +14,8 @@ the gradients of both.
 The caller owns every buffer, outputs included.  Where R rank buffers are
 asked for, a list of R tensors or one tensor with a leading axis of R will do.
 Rows may be strided; the last axis is contiguous.  Calls run on the current
-stream, or on `stream`.  A wrong shape, type, device or stride raises
+stream, or on `stream`; what one call writes and another reads or writes is the
+caller's to order between streams.  A wrong shape, type, device or stride raises
 ValueError, what the library refuses raises RAError; nothing is launched then.
 """
 
@@ -123,7 +124,14 @@ class BlockNorm(_Handle):
     dtype: the partials' and the normalised rows' type; residual_dtype,
     param_dtype: the residual stream's and the weights' (and the gate's), "f32"
     or dtype, which is their default.  eps is added to the mean square; scale
-    multiplies the block's contribution to the residual stream."""
+    multiplies the block's contribution to the residual stream.
+
+    backward calls of one BlockNorm share its workspace: calls on several
+    streams, and replays of graphs that captured one, have to be ordered (by
+    events or wait_stream) as dependent work is; for backward passes that
+    overlap, take a BlockNorm each.  forward calls may overlap.  The first
+    backward call allocates the workspace and cannot be captured; a graph that
+    captured a later one may be replayed when the BlockNorm is closed."""
 
     _destroy, _set_option = staticmethod(_lib.ra_norm_destroy), staticmethod(_lib.ra_norm_set_option)
 
