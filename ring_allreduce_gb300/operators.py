@@ -65,16 +65,16 @@ class _Handle:
         binding._check(self._set_option(h, binding.Option.CHECK_POINTERS, 0))
         self._config = (h.value, self.device, R, *config)
 
-    def _stream(self, stream, *tensors):
-        if stream is None:
-            return _current_stream(self.device)
-        _keep(tensors, stream, self.device)
-        return binding._stream(stream)
-
-    def _call(self, fn, *args):
+    def _call(self, fn, stream, *args):
         if self._config is None:
             raise ValueError("the handle is closed")
-        status = fn(*self._config, *args)
+        if stream is None:
+            status = fn(*self._config, *args, _current_stream(self.device))
+        else:
+            args = [_listed(a) for a in args]
+            status = fn(*self._config, *args, binding._stream(stream))
+            if not status:
+                _keep(args, stream, self.device)   # now that the extension has seen that they are tensors that fit
         if status:
             raise RAError(status, binding.ra_last_error())
 
@@ -102,7 +102,17 @@ def _code(name, dtype):
     return _CODE[dtype]
 
 
-def _keep(tensors, stream, device):
+def _listed(arg):
+    """An argument that can be gone through twice."""
+    if arg is None or isinstance(arg, (torch.Tensor, list, tuple)):
+        return arg
+    try:
+        return tuple(arg)
+    except TypeError:
+        return arg
+
+
+def _keep(args, stream, device):
     """Tell torch's allocator that a stream of the caller's choice uses the
     tensors, so that their memory is not handed out again before it is done."""
     if isinstance(stream, int):
@@ -110,12 +120,10 @@ def _keep(tensors, stream, device):
             stream = torch.cuda.default_stream(device)
         else:
             stream = torch.cuda.ExternalStream(stream, device=device)
-    for t in tensors:
-        if isinstance(t, torch.Tensor):
-            t.record_stream(stream)
-        elif t is not None:
-            for x in t:
-                x.record_stream(stream)
+    for arg in args:
+        for t in arg if isinstance(arg, (list, tuple)) else (arg,):
+            if isinstance(t, torch.Tensor) and t.is_cuda:   # what a call does not look at may be anything
+                t.record_stream(stream)
 
 
 class BlockNorm(_Handle):
@@ -154,8 +162,7 @@ class BlockNorm(_Handle):
         residual, residual_out: [T, dim], may be one tensor; gate: [G, dim], G
         divides T, row t is gated by row t // (T / G).  total [T, dim] and rstd
         [2, T] (float32) keep what backward reads: S, and the two norms' factors."""
-        self._call(_ext.norm_forward, parts, residual, weight, outs, residual_out, post_weight, gate, total, rstd,
-                   self._stream(stream, parts, residual, weight, outs, residual_out, post_weight, gate, total, rstd))
+        self._call(_ext.norm_forward, stream, parts, residual, weight, outs, residual_out, post_weight, gate, total, rstd)
 
     def backward(self, grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins, grad_residual,
                  grad_weight=None, post_weight=None, gate=None, total=None, grad_post_weight=None, grad_gate=None,
@@ -170,9 +177,8 @@ class BlockNorm(_Handle):
         float32, grad_weight [dim], grad_post_weight [dim] and grad_gate
         [G, dim] where given: sums over the rows, zero where T is 0.  grad_residual may be grad_residual_out, and
         grad_ins may be grad_outs."""
-        args = (grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins, grad_residual, grad_weight,
-                post_weight, gate, total, grad_post_weight, grad_gate)
-        self._call(_ext.norm_backward, *args, self._stream(stream, *args))
+        self._call(_ext.norm_backward, stream, grad_outs, grad_residual_out, residual_out, rstd, weight, grad_ins,
+                   grad_residual, grad_weight, post_weight, gate, total, grad_post_weight, grad_gate)
 
 
 class VocabHead(_Handle):
@@ -197,16 +203,14 @@ class VocabHead(_Handle):
         negative, NaN where beyond the vocabulary), lse = log sum exp, entropy,
         and the K = top_ids.shape[1] largest logits' columns (int64, equal ones
         lowest first) with their log probabilities, K at most 32."""
-        args = (shards, targets, logprob, lse, entropy, top_ids, top_logprobs)
-        self._call(_ext.logprobs, *args, self._stream(stream, *args))
+        self._call(_ext.logprobs, stream, shards, targets, logprob, lse, entropy, top_ids, top_logprobs)
 
     def logprobs_backward(self, shards, targets, lse, grad_logprob, grads, entropy=None, grad_entropy=None,
                           stream=None):
         """grads (R shards, may be the logits' own) = the logits' gradient of
         sum(grad_logprob * logprob) + sum(grad_entropy * entropy); lse and
         entropy are what logprobs wrote."""
-        args = (shards, targets, lse, grad_logprob, grads, entropy, grad_entropy)
-        self._call(_ext.logprobs_backward, *args, self._stream(stream, *args))
+        self._call(_ext.logprobs_backward, stream, shards, targets, lse, grad_logprob, grads, entropy, grad_entropy)
 
     def distill(self, shards, teacher_ids, teacher_logits, loss, lse, stream=None):
         """Per row: q = softmax(teacher_logits / temperature) over the row's K
@@ -214,11 +218,9 @@ class VocabHead(_Handle):
         loss = temperature^2 sum q (log q - log p), lse = log sum exp of the
         student's logits / temperature.  teacher_ids: int64 [T, K];
         teacher_logits: float32 or the logits' type."""
-        args = (shards, teacher_ids, teacher_logits, loss, lse)
-        self._call(_ext.distill, *args, self._stream(stream, *args))
+        self._call(_ext.distill, stream, shards, teacher_ids, teacher_logits, loss, lse)
 
     def distill_backward(self, shards, teacher_ids, teacher_logits, lse, grad_loss, grads, stream=None):
         """grads (R shards, may be the logits' own) = the logits' gradient of
         sum(grad_loss * loss); lse is what distill wrote."""
-        args = (shards, teacher_ids, teacher_logits, lse, grad_loss, grads)
-        self._call(_ext.distill_backward, *args, self._stream(stream, *args))
+        self._call(_ext.distill_backward, stream, shards, teacher_ids, teacher_logits, lse, grad_loss, grads)

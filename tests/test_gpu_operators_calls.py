@@ -152,3 +152,33 @@ def test_workspaces_are_given_back(ops):
     for _ in range(40):
         one()
     assert before - torch.cuda.mem_get_info()[0] < 400 << 20
+
+
+def test_what_does_not_fit_beside_a_stream(ops):
+    """ValueError whether or not the caller names a stream; what a call does not look at may be anything."""
+    op = ops.BlockNorm(2, 64, "f32")
+    x, y, z, h = (torch.zeros((6, 64), device="cuda") for _ in range(4))
+    w = torch.ones(64, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (None, side, side.cuda_stream):
+        for bad in ([x, 7], [x, None], [x, y.cpu()], [x], 7, [x, y.half()], x.cpu()):
+            with pytest.raises(ValueError):
+                op.forward(bad, z, w, [h], torch.empty_like(z), stream=stream)
+        with pytest.raises(ValueError):
+            op.forward([x, y], z, w, [h], torch.empty_like(z), rstd=5, stream=stream)
+        op.forward((t for t in (x, y)), z, w, [h], torch.empty_like(z), stream=stream)
+    # five columns over four ranks: the last shard has none and is not looked at
+    head = ops.VocabHead(4, 5, "f32")
+    assert head.widths == [2, 2, 1, 0]
+    s = [torch.zeros((6, 2), device="cuda"), torch.zeros((6, 2), device="cuda"), torch.zeros((6, 1), device="cuda")]
+    t, lp, lse = torch.zeros(6, dtype=torch.int64, device="cuda"), torch.zeros(6, device="cuda"), torch.zeros(6, device="cuda")
+    for last in (None, torch.zeros(6, 0), 3):
+        for stream in (None, side, side.cuda_stream):
+            lse.zero_()
+            torch.cuda.synchronize()
+            head.logprobs([*s, last], t, lp, lse, stream=stream)
+            # entropy without its gradient is not looked at either
+            head.logprobs_backward([*s, last], t, lse, lp, [*(torch.zeros_like(q) for q in s), last], entropy=lp.cpu(),
+                                   stream=stream)
+            torch.cuda.synchronize()
+            assert torch.allclose(lse, torch.full_like(lse, 5.0).log())
