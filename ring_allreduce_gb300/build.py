@@ -102,7 +102,10 @@ def _stamp(extra):
 
 def _torch_dir():
     import importlib.util
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    return spec.submodule_search_locations[0]
 
 
 def _build_torch_ext(force=False):
@@ -129,16 +132,29 @@ def _build_torch_ext(force=False):
     tmp = TORCH_EXT_PATH + ".tmp"
     res = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
     if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"build of {TORCH_EXT}.so failed")
+        raise RuntimeError("the compiler failed\n" + res.stdout + res.stderr)
     os.replace(tmp, TORCH_EXT_PATH)
     with open(stamp_file, "w") as f:
         f.write(h.hexdigest())
 
 
+def _try_torch_ext(force=False):
+    """Build the extension; why it could not be, or None.  The library serves C
+    callers too and needs neither torch nor Python's headers; an extension of
+    another header is worse than none."""
+    try:
+        _build_torch_ext(force)
+        return None
+    except Exception as e:
+        if os.path.exists(TORCH_EXT_PATH):
+            os.remove(TORCH_EXT_PATH)
+        return f"{TORCH_EXT}.so (for BlockNorm and VocabHead on torch tensors) was not built: {e}\n"
+
+
 def build(force=False, verbose=None, jobs=None, debug=False):
     """Compile and link the library (the bounds-checked one with debug=True);
-    returns its path."""
+    returns its path.  The Python extension is built beside it; that it could
+    not be is written to stderr, and importing the operators then fails."""
     verbose = os.environ.get("RA_PTXAS_VERBOSE") == "1" if verbose is None else verbose
     extra = (["-Xptxas", "-v"] if verbose else []) + (["-DRA_DEBUG_BOUNDS"] if debug else [])
     build_dir, lib_path = (DEBUG_BUILD_DIR, DEBUG_LIB_PATH) if debug else (BUILD_DIR, LIB_PATH)
@@ -147,7 +163,7 @@ def build(force=False, verbose=None, jobs=None, debug=False):
     if not force and os.path.exists(lib_path) and os.path.exists(stamp_file):
         with open(stamp_file) as f:
             if f.read().strip() == stamp:
-                _build_torch_ext()
+                sys.stderr.write(_try_torch_ext() or "")
                 return lib_path
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -161,9 +177,9 @@ def build(force=False, verbose=None, jobs=None, debug=False):
         return stem, obj, res
 
     with ThreadPoolExecutor(max_workers=jobs or min(len(UNITS) + 1, os.cpu_count() or 4)) as ex:
-        ext = ex.submit(_build_torch_ext, force)
+        ext = ex.submit(_try_torch_ext, force)
         results = list(ex.map(compile_one, UNITS))
-        ext.result()
+        sys.stderr.write(ext.result() or "")
     failed = [(s, r) for s, _, r in results if r.returncode != 0]
     for s, _, r in results:
         if verbose or r.returncode != 0:
