@@ -588,7 +588,7 @@ ra_status ra_norm_backward(ra_norm_handle h, const ra_norm_backward_args* args, 
 /* A head of V columns (1..2^30) held as R shards: shard r has the columns of
  * chunk r of ra_chunk_plan(R, V), [r C, min((r+1) C, V)), C = ceil(V / R); the
  * pointers of empty shards are not looked at.  The logits are divided by
- * temperature > 0 in every call. */
+ * temperature > 0 in every call (1.5 / temperature has to be finite in binary32). */
 ra_status ra_vocab_create(int R, size_t V, ra_dtype dtype, float temperature, ra_vocab_handle* out);
 ra_status ra_vocab_destroy(ra_vocab_handle h);
 ra_status ra_vocab_set_option(ra_vocab_handle h, int key, long long value);   /* as ra_norm_set_option */

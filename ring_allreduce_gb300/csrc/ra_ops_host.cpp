@@ -500,7 +500,8 @@ static ra_status vocab_create(int R, size_t V, ra_dtype dtype, float temperature
   if (R < 1 || R > kMaxRanks) return record_error(RA_ERR_INVALID, "R=%d outside [1, %d]", R, kMaxRanks);
   if (V < 1 || V > ((size_t)1 << 30)) return record_error(RA_ERR_INVALID, "V=%zu outside [1, 2^30]", V);
   if (!is_float(dtype)) return record_error(RA_ERR_UNSUPPORTED, "dtype %d: f32, bf16 or f16 expected", (int)dtype);
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+  // the kernels' factor is log2(e) / temperature, log2(e) below 1.5
+  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.5f / temperature))
     return record_error(RA_ERR_INVALID, "temperature=%g", (double)temperature);
   int dev = -1, sms = 0;
   RA_TRY(device_of(&dev, &sms));

@@ -74,3 +74,11 @@ def test_vocab_create_refuses(ops, args, status):
     h = ctypes.c_void_p()
     assert ops._lib.ra_vocab_create(*args, ctypes.byref(h)) == status
     assert not h.value
+
+
+@pytest.mark.parametrize("tau,status", [(4e-39, 1), (2.9e-39, 1)])
+def test_vocab_create_refuses_a_temperature_whose_factor_is_infinite(ops, tau, status):
+    """log2(e) / temperature has to be a binary32 number, not 1 / temperature alone."""
+    h = ctypes.c_void_p()
+    assert ops._lib.ra_vocab_create(2, 64, 0, tau, ctypes.byref(h)) == status
+    assert not h.value
