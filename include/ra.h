@@ -641,7 +641,7 @@ ra_status ra_vocab_logprobs_backward(ra_vocab_handle h, const ra_vocab_logprobs_
  * temperature^2 sum_k q_k (log q_k - log p_{id_k}).  A token with an id that
  * is no column, or a teacher logit of -inf, is absent; a row without tokens
  * has loss 0.  A token may occur twice.  Student logits of -inf give a loss
- * of +inf where q > 0. */
+ * of +inf where q, in binary32, is above 0. */
 typedef struct ra_vocab_distill_args {
   size_t rows;
   const void* const* shards;

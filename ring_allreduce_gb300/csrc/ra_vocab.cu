@@ -428,6 +428,25 @@ struct Softmax {
   __device__ __forceinline__ bool taught() const { return m != -INFINITY; }
 };
 
+// A row's loss where the sum over its tokens left binary32's range: tokens at
+// the type's lowest value, whose mean over tau is out of it though tau times
+// that is not, or whose shares add up to a little more than 1.  The mean is no
+// larger than the largest term.  Called by one warp, and not inlined: rare.
+// (m, s: Softmax; base, ref, log2_s: tau log p = tau ln2 ((x - base) log2(e) / tau - ref - log2_s).)
+__device__ __noinline__ float largest_loss(const Teacher& t, int K, float tau, float inv_tau, float m, float s,
+                                           float base, float ref, float log2_s) {
+  float loss = 0.0f, most = 0.0f;
+  for (int k = threadIdx.x & 31; k < K; k += 32) {
+    const float d = t.t[k] - m, p = t.id[k] < 0 ? 0.0f : expf(d * inv_tau) / s;
+    if (p == 0.0f) continue;
+    const float x = t.x[k] - base, e = __fmaf_rn(x, kLog2e * inv_tau, -ref);
+    const float v = d - tau * logf(s) - (e == -INFINITY ? x : kLn2 * tau * (e - log2_s));
+    loss += p * tau * v;   // the weight first: tau v may be out of the range, too
+    most = fmaxf(most, v);
+  }
+  return fminf(warp_sum(loss), warp_max_nan(most) * tau);
+}
+
 // ------------------------------------------------------------------ forward
 
 constexpr int kMaxThreads = 256;
@@ -774,8 +793,8 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
     const float d = far ? x - row_max : x;
     const float t = __fmaf_rn(d, scale, far ? 0.0f : -st.ref);
     // a masked logit near the type's lowest value leaves binary32's range in t before it does so itself
-    return t == -INFINITY && log2_s == log2_s ? (by_tau ? d : d * a.x.inv_tau)
-                                                  : (by_tau ? kLn2 * a.x.tau : kLn2) * -not_below(log2_s - t);
+    if (t == -INFINITY && log2_s == log2_s) return by_tau ? d : d * a.x.inv_tau;
+    return by_tau ? kLn2 * a.x.tau * (t - log2_s) : kLn2 * -not_below(log2_s - t);
   };
   const bool first = part == 0;
   if (first && tid == 0) st_g(a.lse + row, lse);
@@ -792,8 +811,10 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
         // tau (log q - log p): within binary32's range wherever the logits are.  (NaN included)
         if (p != 0.0f) loss += p * ((d - a.x.tau * log_s) - log_prob(t.x[k], true));
       }
-      loss = warp_sum(loss);
-      if (lane == 0) st_g(a.loss + row, q.taught() ? loss * a.x.tau : 0.0f);
+      loss = warp_sum(loss) * a.x.tau;
+      if (loss == INFINITY && !empty)
+        loss = largest_loss(t, a.K, a.x.tau, a.x.inv_tau, q.m, q.s, far ? row_max : 0.0f, far ? 0.0f : st.ref, log2_s);
+      if (lane == 0) st_g(a.loss + row, q.taught() ? loss : 0.0f);
     }
   } else {
     if (first && tid == 0) {

@@ -253,3 +253,25 @@ def test_no_entropy_below_zero_and_no_probability_above_one(ops, dtype, tau):
     logp, _, H64 = stats64(x, tau)
     same(lp, logp[rows, targets], sum_loss(V), "logprob")
     same(H, H64, (sum_loss(V) + 8 * E) * (2 + math.log(V)), "entropy")
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.0, 2.0])
+def test_loss_of_tokens_at_the_lowest_value(ops, tau):
+    """Every token that the teacher knows at binary32's lowest value: the loss is that value's size times tau, a number
+    up to tau = 1, whatever the rounded shares add up to."""
+    T, V, K = 700, 300, 33
+    g = gen(121)
+    x, _ = logits(g, T, V, "f32")
+    ids = torch.rand((T, V), generator=g, device="cuda").argsort(1)[:, :K].contiguous()
+    t = randn(g, T, K, sigma=3.0)
+    x.scatter_(1, ids, torch.finfo(torch.float32).min)
+    op = ops.VocabHead(3, V, "f32", temperature=tau)
+    loss, lse = (torch.full((T,), 9.0, device="cuda") for _ in range(2))
+    op.distill(shards_of(x, 3), ids, t, loss, lse)
+    logp, _, _ = stats64(x, tau)
+    logq = torch.log_softmax(t.double() / tau, 1)
+    want = in_f32(tau ** 2 * (logq.exp() * (logq - logp.gather(1, ids))).sum(1))
+    assert torch.isfinite(want).all() == (tau <= 1)
+    # shares are good to 8 E of (t - max) / tau and their sum, K of them to K E: all relative here
+    tmag = (t.double().amax(1) - t.double().amin(1)) / tau
+    same(loss, want, (K + 64 + 8 * tmag) * E * size(want), "loss")
