@@ -79,7 +79,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 //        are not used).
 //   PK   AL, and a row has sixteen vectors at most: as many rows as fit share a
 //        warp, a power of two of lanes each (65536 x 128 bf16, eight ranks:
-//        36 us forward, 60 backward; a warp a row 62 and 118).
+//        37 us forward, 63 backward; a warp a row 67 and 100).
 template <class D, int VPT, bool AL, int MAXT, bool PK = false> struct Cols {
   static_assert(!PK || (AL && VPT == 1), "rows that share a warp");
   using T = typename D::T;
@@ -128,9 +128,10 @@ template <class D, int VPT, bool AL, int MAXT, bool PK = false> struct Cols {
   static constexpr bool kZeroed = AL;
   static constexpr int kUnroll = AL ? 4 : 1;
   // Columns one by one are loaded and stored without a test each by the warps
-  // that are whole, which doubles that code: where there are many rows (sixteen
-  // columns a thread) 4096 x 5001 bf16 took 102 us without and 82 us with it, but
-  // a call of 96 rows, whose time is its code's way into the cache, 10.7 and 12.7.
+  // that are whole, which doubles that code: so only where there are many rows
+  // (sixteen columns a thread).  4096 x 5001 bf16 of three ranks takes 67 us so, 83
+  // without; for few rows it is nearly one (96 x 5001: 6.3 us, 6.0 with it; 96 x 1538
+  // fp16 of two ranks backward: 9.3 and 9.1).
   static constexpr bool kTwice = !AL && kEach == 16;
   static constexpr int kStep = AL ? 32 * V : 32;   // columns from a thread's piece to its next
   __device__ __forceinline__ bool has(int k) const { return k * kStep < left; }
@@ -438,8 +439,8 @@ template <class C, class D, class RD> struct ForwardRows {
 // Measured, as parts of a copy's 6.8 TB/s for the bytes that have to move:
 // 8192 x 4096, four ranks, bf16 with a binary32 residual, post norm, gate, the
 // sum kept and four copies out: 143 us, 0.90; 1023 x 5001 binary32, three
-// ranks, no row aligned: 30 us, 0.70 (seven rows an SM, the last ones alone);
-// one row of 4096 from eight ranks: 4.4 us, two dependent reads and two sums
+// ranks, no row aligned: 30 us, 0.71 (seven rows an SM, the last ones alone);
+// one row of 4096 from eight ranks: 4.5 us, two dependent reads and two sums
 // over a block after the launch.
 template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_forward_kernel(const __grid_constant__ NormForward a) {
@@ -576,8 +577,9 @@ template <class C, class D, class RD> struct BackwardRows {
 // 162 us with the join of the column sums, 0.79 of the copy bandwidth.  The
 // registers bound it: a row's values and three sums per column leave one
 // CTA of 16 warps to an SM, whose waits for its own sums nothing else fills
-// (DRAM 64 % busy, each scheduler with four warps to choose from).  96 x 1538
-// fp16, two ranks, eight gate rows: 9.6 us, two launches' latency.
+// (DRAM 62 % busy, each scheduler with four warps to choose from).  96 x 1538
+// fp16, two ranks, eight gate rows: 9.7 us, two launches' latency.  Above 8192
+// columns 64 registers a thread spill: 4096 x 16384 550 us, 0.47.
 template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_constant__ NormBackward a,
                                                              const __grid_constant__ Deal d) {

@@ -281,8 +281,8 @@ __device__ __forceinline__ uint32_t in_cta(const void* mine, uint32_t rank) {
   return a;
 }
 // What another CTA is to read is stored into its shared memory before the
-// barrier: read from here after it, a few rows waited for the way there and
-// back once more (one row of 131072, 20 alternatives: 8.6 us, 8.8 that way).
+// barrier: read from here after it, a few rows would wait for the way there and
+// back once more.
 __device__ __forceinline__ void far_store(uint32_t a, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
@@ -482,7 +482,7 @@ using PartLists = uint64_t[kMaxParts][32];
 
 // The block's statistics, the same in every thread (and of every CTA of the row).
 __device__ __noinline__ Stats block_stats(Stats st, RowShared& sh, int part, int parts) {
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;   // four or eight
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;   // a power of two
   st = warp_stats(st, 32);
   if (lane == 0) sh.warp[threadIdx.x >> 5] = st;
   __syncthreads();
@@ -672,12 +672,13 @@ __device__ __noinline__ void top_of_many(TopShared& sh, uint32_t best, int best_
 }
 
 // Measured, as parts of a copy's 6.8 TB/s for the logits' bytes: loss of 4096
-// x 131072 bf16 in eight shards, 64 teacher tokens: 161 us, 0.98; log
-// probabilities, entropy and five alternatives: 184 us, 0.86 (the entropy's
+// x 131072 bf16 in eight shards, 64 teacher tokens: 161 us, 0.99; log
+// probabilities, entropy and five alternatives: 185 us, 0.86 (the entropy's
 // multiply and the largest of every group of chunks: issue slots); one row
-// with 20 alternatives: 8.8 us, 4 us of them the choice of the alternatives
+// with 20 alternatives: 8.9 us, 4 us of them the choice of the alternatives
 // over a cluster of eight CTAs.  Short rows pay per row for the alternatives:
-// 20000 x 8192 bf16 55 us without, 88 with five.
+// 20000 x 8192 bf16 59 us without, 93 with five.  2048 x 131072 binary32:
+// 154 us, 1.03, and 168, 0.94.
 template <class D, bool DISTILL>
 __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __grid_constant__ VocabForward a,
                                                                        int parts) {
@@ -1005,7 +1006,8 @@ __device__ __noinline__ void far_gradient(const VocabRows& x, BackwardShared& sh
 // target or the teacher adds is put on top after the CTA's columns are
 // written.  Measured: log probabilities and entropy of 2048 x 65536 fp16: 85
 // us, 0.93 of the copy bandwidth; distillation of 4096 x 100003 bf16 in eight
-// shards, no row aligned: 269 us, 0.90.  Memory bounds both.
+// shards, no row aligned: 269 us, 0.90; 2048 x 131072 binary32, with expf: 323
+// and 327 us, 0.98 and 0.97.  Memory bounds them all.
 template <class D, bool DISTILL>
 __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_constant__ VocabBackward a, int parts) {
   constexpr int V = D::kVec;
@@ -1194,14 +1196,17 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
     using D = decltype(d);
     const int chunks = chunks_per_shard(a.x) * a.x.shards;
     // Many rows: CTAs of 128 threads at most, eight chunks a warp, so that
-    // one's sums and lists overlap the others' reading.  Few rows: up to 256
-    // threads, a chunk a warp, and clusters that split a row
+    // one's sums and lists overlap the others' reading (log probabilities with
+    // five alternatives, and loss, in 128 and in 256 threads: 4096 x 131072
+    // bf16 188 and 195 us, 162 and 162; 1200 rows 59 and 64, 51 and 53; 620 rows
+    // 54 and 46, 33 and 37; of 50021 f32 34 and 36, 23 and 29).  Few rows: up to
+    // 256 threads, a chunk a warp, and clusters that split a row
     // while less than five sixths of the SMs are covered, eight chunks a CTA
-    // at least (61 x 50021, 20 alternatives: 10.9 us in four parts, 11.4 in
-    // two; 129 x 32003: 11.1 in two, 9.8 in one).  Two threads an alternative
+    // at least (61 x 50021 f32, 20 alternatives: 10.6 us in four parts, 12.0 in
+    // two; 129 x 32003 f16: 11.8 in two, 10.6 in one).  Two threads an alternative
     // at least: the bound is one of the threads' maxima, and a low one lets
-    // many logits through (20000 x 8192 bf16, 32 alternatives: 155 us with two
-    // warps, 325 with one; with 20, 131 and 122).
+    // many logits through (20000 x 8192 bf16, 32 alternatives: 162 us with two
+    // warps, 327 with one; with 20, 137 and 128).
     const bool many = a.x.rows >= 4 * (int64_t)sms;
     int threads = 32;
     while (threads < (many ? 128 : 256) && (threads / 32 * (many ? 8 : 1) < chunks || threads < 2 * a.top)) threads *= 2;
@@ -1221,11 +1226,11 @@ cudaError_t launch_vocab_backward(int dtype, const VocabBackward& a, int sms, cu
     using D = decltype(d);
     const int chunks = chunks_per_shard(a.x) * a.x.shards;
     // Many rows: CTAs of 128 threads at most, four chunks a warp (loss gradient
-    // of 20000 x 8192 bf16, eight chunks a row: 110 us in CTAs of two warps, 116
-    // of four, 151 of one; of 5184 x 503 f32, two chunks: 26 us of one, 28 of four).
+    // of 20000 x 8192 bf16, eight chunks a row: 129 us in CTAs of two warps, 133
+    // of four, 172 of one; of 5184 x 503 f32, two chunks: 26 us of one, 28 of four).
     // Few rows: split each until there are four CTAs of 128 threads to an SM, a
     // chunk a warp at least.  (Every part reads the teacher's tokens again:
-    // loss and gradient of 129 x 32003 f16 take 12.9 us so, 14.3 with eight.)
+    // loss and gradient of 129 x 32003 f16 take 11.7 us so, 13.9 with eight.)
     const bool many = a.x.rows >= 4 * (int64_t)sms;
     int threads = many ? 32 : 128;
     while (threads < 128 && threads / 32 * 4 < chunks) threads *= 2;
