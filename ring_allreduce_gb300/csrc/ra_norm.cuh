@@ -577,9 +577,9 @@ template <class C, class D, class RD> struct BackwardRows {
 // 162 us with the join of the column sums, 0.79 of the copy bandwidth.  The
 // registers bound it: a row's values and three sums per column leave one
 // CTA of 16 warps to an SM, whose waits for its own sums nothing else fills
-// (DRAM 62 % busy, each scheduler with four warps to choose from).  96 x 1538
+// (DRAM 63 % busy, each scheduler with four warps to choose from).  96 x 1538
 // fp16, two ranks, eight gate rows: 9.7 us, two launches' latency.  Above 8192
-// columns 64 registers a thread spill: 4096 x 16384 550 us, 0.47.
+// columns 64 registers a thread spill: 4096 x 16384 551 us, 0.47.
 template <class D, class RD, int VPT, bool AL, int MAXT, bool PK = false>
 __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const __grid_constant__ NormBackward a,
                                                              const __grid_constant__ Deal d) {

@@ -14,6 +14,7 @@ namespace ra {
 constexpr int kNormMaxDim = 16384;
 constexpr int kTopMax = 32;       // alternatives per row: one per lane of a warp
 constexpr int kTeacherMax = 256;  // teacher tokens per row
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Block end, forward.  Strides in elements; pointers of absent tensors NULL.
 struct NormForward {
@@ -90,6 +91,8 @@ struct VocabRows {
   int V, C;
   int slots;                   // 16-byte slots that a shard's columns touch at most
   float tau, inv_tau;
+  float scale;                 // log2(e) / tau, rounded
+  float unit, unit_rest;       // 1 / (tau scale) in two parts: what 1 in the scaled logits is in x / tau
 };
 
 struct VocabForward {

@@ -546,6 +546,10 @@ static void set_rows(const ra_vocab_ctx* h, size_t rows, const void* const* shar
   x->C = h->C;
   x->tau = h->tau;
   x->inv_tau = 1.0f / h->tau;
+  x->scale = ra::kLog2e * x->inv_tau;
+  const double unit = 1.0 / ((double)h->tau * (double)x->scale);
+  x->unit = (float)unit;
+  x->unit_rest = (float)(unit - (double)x->unit);
 }
 
 // The powers of two that what a probability is multiplied with may reach:

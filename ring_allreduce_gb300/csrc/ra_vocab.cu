@@ -13,7 +13,9 @@
 // keeps s = sum 2^t and u = sum t 2^t; ref is at most kLag below the largest x
 // log2(e) that the thread saw, and s and u are moved when it is passed by more
 // (rare after the first vectors), so 2^t never leaves its range.  Then lse =
-// ln2 (ref + log2 s) and H = ln2 (log2 s - u / s).  All statistics are binary32.
+// ref unit + ln2 log2 s, unit = 1 / (tau scale) of the rounded factor (ln2 but for
+// that) in two parts so that lse is rounded once, and H = ln2 (log2 s - u / s).
+// All statistics are binary32.
 // ref is the rounded x log2(e) of a logit, t the exact one less ref, so t of
 // that very logit is half a unit of ref's last place: |ref| is held to 2^24,
 // where that is 1 at most.  (At 1e10 it would be 2^8, and 2^t infinite: a mask
@@ -44,7 +46,6 @@
 namespace ra {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFarBelow = -200.0f;   // 2^-200 is 0 in binary32: exponents that are multiplied with their power
                                        // are held above this, so that it stays 0 (not 0 * inf)
@@ -689,7 +690,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const int part = parts > 1 ? (int)cluster_rank() : 0;
   if (parts > 1) cluster_arrive();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const float scale = kLog2e * a.x.inv_tau;
+  const float scale = a.x.scale;
   const int per = chunks_per_shard(a.x), chunks = per * a.x.shards;
   const int share = (chunks + parts - 1) / parts;
   const int begin = part * share, end = min(chunks, begin + share);
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kMaxThreads, 4) vocab_forward_kernel(const __g
   const float log2_s = log2f(st.s);                // NaN where the row has +inf or NaN
   const float lse = empty ? -INFINITY
                     : far ? __fmaf_rn(row_max, a.x.inv_tau, kLn2 * log2_s)
-                          : kLn2 * (st.ref + log2_s);
+                          : __fmaf_rn(st.ref, a.x.unit, __fmaf_rn(st.ref, a.x.unit_rest, kLn2 * log2_s));
   // A row of one token has log2 s - t of a rounding's size, on either side of 0:
   // what cannot be below 0 is held there.  (NaN stays.)
   auto not_below = [](float v) { return v < 0.0f ? 0.0f : v; };
@@ -1006,8 +1007,8 @@ __device__ __noinline__ void far_gradient(const VocabRows& x, BackwardShared& sh
 // target or the teacher adds is put on top after the CTA's columns are
 // written.  Measured: log probabilities and entropy of 2048 x 65536 fp16: 85
 // us, 0.93 of the copy bandwidth; distillation of 4096 x 100003 bf16 in eight
-// shards, no row aligned: 269 us, 0.90; 2048 x 131072 binary32, with expf: 323
-// and 327 us, 0.98 and 0.97.  Memory bounds them all.
+// shards, no row aligned: 269 us, 0.90; 2048 x 131072 binary32, with expf: 322
+// and 326 us, 0.98 and 0.97.  Memory bounds them all.
 template <class D, bool DISTILL>
 __global__ void __launch_bounds__(128, 8) vocab_backward_kernel(const __grid_constant__ VocabBackward a, int parts) {
   constexpr int V = D::kVec;
@@ -1198,15 +1199,15 @@ cudaError_t launch_vocab_forward(int dtype, const VocabForward& a, int sms, cuda
     // Many rows: CTAs of 128 threads at most, eight chunks a warp, so that
     // one's sums and lists overlap the others' reading (log probabilities with
     // five alternatives, and loss, in 128 and in 256 threads: 4096 x 131072
-    // bf16 188 and 195 us, 162 and 162; 1200 rows 59 and 64, 51 and 53; 620 rows
-    // 54 and 46, 33 and 37; of 50021 f32 34 and 36, 23 and 29).  Few rows: up to
+    // bf16 188 and 195 us, 162 and 164; 1200 rows 59 and 64, 51 and 53; 620 rows
+    // 54 and 46, 33 and 37; of 50021 f32 34 and 36, 24 and 29).  Few rows: up to
     // 256 threads, a chunk a warp, and clusters that split a row
     // while less than five sixths of the SMs are covered, eight chunks a CTA
     // at least (61 x 50021 f32, 20 alternatives: 10.6 us in four parts, 12.0 in
     // two; 129 x 32003 f16: 11.8 in two, 10.6 in one).  Two threads an alternative
     // at least: the bound is one of the threads' maxima, and a low one lets
-    // many logits through (20000 x 8192 bf16, 32 alternatives: 162 us with two
-    // warps, 327 with one; with 20, 137 and 128).
+    // many logits through (20000 x 8192 bf16, 32 alternatives: 163 us with two
+    // warps, 327 with one; with 20, 138 and 128).
     const bool many = a.x.rows >= 4 * (int64_t)sms;
     int threads = 32;
     while (threads < (many ? 128 : 256) && (threads / 32 * (many ? 8 : 1) < chunks || threads < 2 * a.top)) threads *= 2;

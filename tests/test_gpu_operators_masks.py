@@ -275,3 +275,21 @@ def test_loss_of_tokens_at_the_lowest_value(ops, tau):
     # shares are good to 8 E of (t - max) / tau and their sum, K of them to K E: all relative here
     tmag = (t.double().amax(1) - t.double().amin(1)) / tau
     same(loss, want, (K + 64 + 8 * tmag) * E * size(want), "loss")
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.0, 2.0])
+@pytest.mark.parametrize("shift", [700.0, -700.0, 11.0])
+def test_lse_is_rounded_once(ops, tau, shift):
+    """lse within half a unit of its last place of the 64-bit one, and the loss of the row's sum: a gradient of binary32
+    logits has lse's error in every probability."""
+    T, V = 300, 1000
+    x = randn(gen(131), T, V, sigma=2.0, mean=shift)
+    op = ops.VocabHead(3, V, "f32", temperature=tau)
+    lp, lse, loss, lse2 = (torch.full((T,), 9.0, device="cuda") for _ in range(4))
+    op.logprobs(shards_of(x, 3), torch.zeros(T, dtype=torch.int64, device="cuda"), lp, lse)
+    ids = torch.arange(4, device="cuda").expand(T, 4).contiguous()
+    op.distill(shards_of(x, 3), ids, torch.zeros((T, 4), device="cuda"), loss, lse2)
+    _, want, _ = stats64(x, torch.tensor(tau, dtype=torch.float32).item())   # the handle's temperature is a binary32 one
+    half = 2.0 ** (torch.floor(torch.log2(want.abs())) - 24)
+    for got in (lse, lse2):
+        same(got, want, half + sum_loss(V), "lse")
