@@ -489,6 +489,11 @@ ra_status ra_debug_bounds_report(unsigned long long* count, unsigned long long* 
  *               logits: log probabilities of given tokens with entropy and
  *               top alternatives, distillation from a teacher's top logits,
  *               and the gradients of both
+ *   ra_ffn_*    the feed-forward block between two block ends: gated
+ *               projections, their product and the projection back, which
+ *               gives the R partial products that the next block end sums;
+ *               and its gradient
+ *   ra_ckpt_*   rows kept in 8 bits until the backward pass, and brought back
  *
  * Buffers are as above the caller's device memory, addressed by rows: a
  * stride is the number of elements between rows (at least the row's width;
@@ -674,6 +679,147 @@ typedef struct ra_vocab_distill_backward_args {
   const size_t* grad_strides;
 } ra_vocab_distill_backward_args;
 ra_status ra_vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distill_backward_args* args, void* stream);
+
+/* Feed-forward blocks of R ranks: `dim` columns outside (1..2^20), `inner`
+ * inside (1..2^24), of which rank r holds those of chunk r of
+ * ra_chunk_plan(R, inner), [r C, min((r+1) C, inner)), C = ceil(inner / R); its
+ * three weights are [width_r][dim], and the pointers of ranks without columns
+ * are not looked at.  dtype: RA_BF16 or RA_F16.  grad_dtype, the weights'
+ * gradients': dtype or RA_F32.
+ *
+ * Buffers may start on any element and have any stride, as for the operators
+ * above, but products run on the tensor cores only where the rows of both
+ * their operands start on 16-byte boundaries; otherwise on the CUDA cores,
+ * some thirty times slower.  (`dim` a multiple of 8, or padded rows: the
+ * inner width and the number of rows do not matter, as hidden, grad_gate and
+ * grad_up may have padded rows.) */
+typedef struct ra_ffn_ctx* ra_ffn_handle;
+typedef enum ra_activation { RA_SILU = 0, RA_GELU = 1 } ra_activation;   /* a / (1 + e^-a); a (1 + erf(a / sqrt 2)) / 2 */
+ra_status ra_ffn_create(int R, int dim, size_t inner, ra_dtype dtype, ra_activation activation, ra_dtype grad_dtype,
+                        ra_ffn_handle* out);
+ra_status ra_ffn_destroy(ra_ffn_handle h);
+ra_status ra_ffn_set_option(ra_ffn_handle h, int key, long long value);   /* as ra_norm_set_option */
+
+/* Whether a bounded device wait of the products gave up since the last call
+ * (RA_ERR_TIMEOUT, outputs undefined; one record a device, shared by all
+ * ra_ffn handles, and cleared by this call).  Synchronises `stream` first;
+ * err may be NULL. */
+ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_error* err);
+
+/* Per rank r: a = x w_gate_r^T, b = x w_up_r^T (binary32); hidden_r =
+ * activation(a) b, rounded to dtype; out_r = hidden_r w_down_r, rounded (of
+ * no columns: zeros).  keep_bits 8 or 16: a and b are kept for backward in gate
+ * and up, as 8-bit codes with their scales (see ra_ckpt_create) or rounded to
+ * dtype; 0: not at all, gate and up are not looked at. */
+typedef struct ra_ffn_forward_args {
+  size_t rows;
+  const void* const* x;          /* `xs` buffers [rows][dim] */
+  size_t x_stride;
+  int xs;                        /* 1, or R: one for every rank */
+  const void* const* w_gate;     /* R buffers [width_r][dim], and R strides; so the others */
+  const size_t* w_gate_strides;
+  const void* const* w_up;
+  const size_t* w_up_strides;
+  const void* const* w_down;
+  const size_t* w_down_strides;
+  void* const* hidden;           /* R buffers [rows][width_r] */
+  const size_t* hidden_strides;
+  void* const* out;              /* R buffers [rows][dim] */
+  size_t out_stride;
+  int keep_bits;                 /* 0, 8 or 16 */
+  void* const* gate;             /* R buffers [rows][width_r] of 8-bit codes, or of dtype */
+  const size_t* gate_strides;
+  void* const* up;
+  const size_t* up_strides;
+  float* const* gate_scales;     /* keep_bits 8: R buffers [rows][ceil(width_r / 128)] */
+  float* const* up_scales;
+} ra_ffn_forward_args;
+ra_status ra_ffn_forward(ra_ffn_handle h, const ra_ffn_forward_args* args, void* stream);
+
+/* The gradient, from the kept a and b.  With dh = grad_out w_down_r^T
+ * (binary32): grad_gate_r = dh b activation'(a), grad_up_r = dh activation(a),
+ * hidden_r = activation(a) b, each rounded to dtype; and from these, each only
+ * where it is asked for (not NULL), grad_x_r = grad_gate_r w_gate_r + grad_up_r w_up_r,
+ * grad_w_gate_r = grad_gate_r^T x, grad_w_up_r = grad_up_r^T x, grad_w_down_r =
+ * hidden_r^T grad_out (sums over no rows are zeros).  grad_out is the gradient of every rank's
+ * partial product.  hidden may be NULL without grad_w_down.  keep_bits 16:
+ * grad_gate[r] == gate[r] and grad_up[r] == up[r] (same stride) are allowed. */
+typedef struct ra_ffn_backward_args {
+  size_t rows;
+  const void* const* grad_out;   /* `grads` buffers [rows][dim] */
+  size_t grad_out_stride;
+  int grads;                     /* 1 or R */
+  const void* const* x;          /* as in forward; may be NULL without grad_w_gate and grad_w_up */
+  size_t x_stride;
+  int xs;
+  const void* const* w_gate;     /* w_gate and w_up may be NULL without grad_x */
+  const size_t* w_gate_strides;
+  const void* const* w_up;
+  const size_t* w_up_strides;
+  const void* const* w_down;
+  const size_t* w_down_strides;
+  int keep_bits;                 /* 8 or 16 */
+  const void* const* gate;       /* what forward kept */
+  const size_t* gate_strides;
+  const void* const* up;
+  const size_t* up_strides;
+  const float* const* gate_scales;
+  const float* const* up_scales;
+  void* const* hidden;           /* R buffers [rows][width_r] */
+  const size_t* hidden_strides;
+  void* const* grad_gate;
+  const size_t* grad_gate_strides;
+  void* const* grad_up;
+  const size_t* grad_up_strides;
+  void* const* grad_x;           /* R buffers [rows][dim], the ranks' partial gradients of x, or NULL */
+  size_t grad_x_stride;
+  void* const* grad_w_gate;      /* R buffers [width_r][dim] of grad_dtype, or NULL; so the others */
+  const size_t* grad_w_gate_strides;
+  void* const* grad_w_up;
+  const size_t* grad_w_up_strides;
+  void* const* grad_w_down;
+  const size_t* grad_w_down_strides;
+} ra_ffn_backward_args;
+ra_status ra_ffn_backward(ra_ffn_handle h, const ra_ffn_backward_args* args, void* stream);
+
+/* Rows of `dim` columns (1..2^24) kept in 8 bits: every 128 columns of a row
+ * from a multiple of 128 on are a group, whose scale is fl(m / 127), m its
+ * largest magnitude, and whose codes are the values times fl(127 / m), rounded to binary32
+ * and then to the nearest whole number (to even).  A code stands for
+ * code x scale.  A group with nothing above 2^-110 is kept as zeros; one with
+ * an infinity or a NaN comes back as NaN.  dtype: that of the rows; normed_dtype
+ * and param_dtype: those of the normalised rows and of their weight. */
+typedef struct ra_ckpt_ctx* ra_ckpt_handle;
+ra_status ra_ckpt_create(int dim, ra_dtype dtype, ra_dtype normed_dtype, ra_dtype param_dtype, ra_ckpt_handle* out);
+ra_status ra_ckpt_destroy(ra_ckpt_handle h);
+ra_status ra_ckpt_set_option(ra_ckpt_handle h, int key, long long value);   /* as ra_norm_set_option */
+
+typedef struct ra_ckpt_store_args {
+  size_t rows;
+  const void* values;            /* [rows][dim] of dtype */
+  size_t stride;
+  signed char* codes;            /* [rows][dim] */
+  size_t codes_stride;
+  float* scales;                 /* [rows][ceil(dim / 128)] */
+} ra_ckpt_store_args;
+ra_status ra_ckpt_store(ra_ckpt_handle h, const ra_ckpt_store_args* args, void* stream);
+
+/* values = code x scale, rounded to dtype; normed = (code x scale) rstd weight,
+ * rounded to normed_dtype: of a kept residual stream the normalised rows of
+ * ra_norm_forward, whose rstd[1] it takes.  Either may be NULL, not both. */
+typedef struct ra_ckpt_load_args {
+  size_t rows;
+  const signed char* codes;
+  size_t codes_stride;
+  const float* scales;
+  void* values;
+  size_t stride;
+  const float* rstd;             /* [rows] */
+  const void* weight;            /* [dim] of param_dtype */
+  void* normed;                  /* [rows][dim] of normed_dtype */
+  size_t normed_stride;
+} ra_ckpt_load_args;
+ra_status ra_ckpt_load(ra_ckpt_handle h, const ra_ckpt_load_args* args, void* stream);
 
 /* Text of the calling thread's last error ("" if none). */
 const char* ra_last_error(void);

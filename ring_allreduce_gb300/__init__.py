@@ -2,9 +2,11 @@
 
 The compute path is the CUDA library ``libra_gb300.so`` (``include/ra.h``);
 this package is its thin Python binding (ctypes marshalling, torch for device
-memory and streams).  ``BlockNorm`` and ``VocabHead`` (``operators.py``) are the
-model operators around those sums: a block's end with its norms, and the
-vocabulary-parallel head's log probabilities and distillation.
+memory and streams).  ``BlockNorm``, ``VocabHead``, ``FeedForward`` and
+``Checkpoint`` (``operators.py``) are the model operators around those sums: a
+block's end with its norms, the vocabulary-parallel head's log probabilities
+and distillation, the gated feed-forward block between two block ends, and
+rows kept in 8 bits for the backward pass.
 The binding is loaded on first use of one of its names,
 so ``ring_allreduce_gb300.inputs`` can be imported on a machine where the
 library has not been built.  Using the binding without the built library
@@ -19,7 +21,7 @@ _BINDING_NAMES = {
     "RingAllReduce", "PreparedCall", "RAError", "Status", "DType", "Op", "Variant", "Barrier", "Option",
     "DeviceError", "load_library", "library_path",
 }
-_OPERATOR_NAMES = {"BlockNorm", "VocabHead"}
+_OPERATOR_NAMES = {"BlockNorm", "VocabHead", "FeedForward", "Checkpoint"}
 
 
 def __getattr__(name):

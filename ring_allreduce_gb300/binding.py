@@ -143,6 +143,18 @@ EXPORTED = {
     "ra_vocab_logprobs_backward": (_ST, [_P, _P, _P]),
     "ra_vocab_distill": (_ST, [_P, _P, _P]),
     "ra_vocab_distill_backward": (_ST, [_P, _P, _P]),
+    "ra_ffn_create": (_ST, [ctypes.c_int, ctypes.c_int, _SZ, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                            ctypes.POINTER(_P)]),
+    "ra_ffn_destroy": (_ST, [_P]),
+    "ra_ffn_set_option": (_ST, [_P, ctypes.c_int, ctypes.c_longlong]),
+    "ra_ffn_get_device_status": (_ST, [_P, _P, ctypes.POINTER(DeviceError)]),
+    "ra_ffn_forward": (_ST, [_P, _P, _P]),
+    "ra_ffn_backward": (_ST, [_P, _P, _P]),
+    "ra_ckpt_create": (_ST, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_P)]),
+    "ra_ckpt_destroy": (_ST, [_P]),
+    "ra_ckpt_set_option": (_ST, [_P, ctypes.c_int, ctypes.c_longlong]),
+    "ra_ckpt_store": (_ST, [_P, _P, _P]),
+    "ra_ckpt_load": (_ST, [_P, _P, _P]),
     "ra_last_error": (ctypes.c_char_p, []),
     "ra_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }

@@ -32,7 +32,8 @@ DEBUG_BUILD_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(HERE, "libra_gb300_debug.so")
 
 SOURCES = ["ra_host.cpp", "ra_direct.cu", "ra_round.cu", "ra_persistent.cu", "ra_pipelined.cu", "ra_compact.cu",
-           "ra_bcast.cu", "ra_static.cu", "ra_local.cu", "ra_ll.cu", "ra_ops_host.cpp", "ra_norm.cu", "ra_vocab.cu"]
+           "ra_bcast.cu", "ra_static.cu", "ra_local.cu", "ra_ll.cu", "ra_ops_host.cpp", "ra_norm.cu", "ra_vocab.cu",
+           "ra_ffn_host.cpp", "ra_ffn_simple.cu", "ra_ckpt.cu"]
 # (source, object stem, preprocessor definitions): ra_direct_inst.cu is
 # compiled once per dtype so its instantiations build in parallel
 DTYPES = ["RA_F32", "RA_BF16", "RA_I32", "RA_F16", "RA_F64", "RA_I64"]
@@ -74,6 +75,8 @@ KERNEL_SOURCES = {
     "ll": ["ra_ll.cu", "ra_ll.h", "ra_device.cuh", "ra_internal.h"],
     "norm": ["ra_norm.cu", "ra_norm.cuh", "ra_norm_inst.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
     "vocab": ["ra_vocab.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
+    "ffn": ["ra_ffn_simple.cu", "ra_ffn.cuh", "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
+    "ckpt": ["ra_ckpt.cu", "ra_ffn.cuh", "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
 }
 
 
@@ -148,7 +151,7 @@ def _try_torch_ext(force=False):
     except Exception as e:
         if os.path.exists(TORCH_EXT_PATH):
             os.remove(TORCH_EXT_PATH)
-        return f"{TORCH_EXT}.so (for BlockNorm and VocabHead on torch tensors) was not built: {e}\n"
+        return f"{TORCH_EXT}.so (for the model operators on torch tensors) was not built: {e}\n"
 
 
 def build(force=False, verbose=None, jobs=None, debug=False):

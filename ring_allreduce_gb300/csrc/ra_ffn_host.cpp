@@ -1,0 +1,393 @@
+// ra_ffn_host.cpp -- host side of the feed-forward block and of rows kept in 8
+// bits (ra_ffn_*, ra_ckpt_* of include/ra.h): handles, argument checks, and
+// which kernel runs.
+#include "ra_ffn.h"
+#include "ra_ops_host.h"
+
+struct ra_ffn_ctx {
+  int R, dim, inner, C, ranks, device, sms;   // ranks: those that hold columns
+  ra_dtype dtype, grad_dtype;
+  int act;
+  bool check_pointers = true;
+};
+
+struct ra_ckpt_ctx {
+  int dim, device, sms;
+  ra_dtype dtype, normed_dtype, param_dtype;
+  bool check_pointers = true;
+};
+
+namespace {
+
+using namespace ra;
+
+constexpr int kMaxDim = 1 << 20, kMaxInner = 1 << 24;
+constexpr size_t kMaxFfnRows = (size_t)1 << 30;
+
+using FfnBuffers = BuffersOf<17 * kMaxRanks>;
+
+// Sharded buffers of a call: rank r's [rows][width_r], or, as a weight, [width_r][dim].
+struct Shards {
+  const char* name;
+  const void* const* at;
+  const size_t* strides;
+  size_t elem;
+  bool weight, output;
+  const void* const* twins = nullptr;
+};
+
+ra_status add_shards(const ra_ffn_ctx* h, FfnBuffers& buf, size_t rows, const Shards& s, void** at, int64_t* strides) {
+  if (!s.at || !s.strides) return record_error(RA_ERR_INVALID, "%s: NULL pointer array", s.name);
+  for (int r = 0; r < h->ranks; ++r) {
+    const size_t width = (size_t)(r + 1 < h->ranks ? h->C : h->inner - r * h->C);
+    size_t stride = s.strides[r];
+    if (s.weight)
+      RA_TRY(buf.add(s.name, r, s.at[r], s.elem, (size_t)h->dim, &stride, s.output, width));
+    else
+      RA_TRY(buf.add(s.name, r, s.at[r], s.elem, width, &stride, s.output, rows, s.twins ? s.twins[r] : nullptr));
+    at[r] = const_cast<void*>(s.at[r]);
+    strides[r] = (int64_t)stride;
+  }
+  return RA_OK;
+}
+
+// 1 or R buffers [rows][dim], taken as R.
+ra_status add_ranks(const ra_ffn_ctx* h, FfnBuffers& buf, const char* name, const void* const* p, int count,
+                    size_t stride, bool output, const void** at, int64_t* checked) {
+  if (!p) return record_error(RA_ERR_INVALID, "%s: NULL pointer array", name);
+  for (int r = 0; r < count; ++r)
+    RA_TRY(buf.add(name, r, p[r], 2, (size_t)h->dim, &stride, output));
+  for (int r = 0; r < h->R; ++r) at[r] = p[count == 1 ? 0 : r];
+  *checked = (int64_t)stride;
+  return RA_OK;
+}
+
+ra_status add_scales(const ra_ffn_ctx* h, FfnBuffers& buf, const char* name, size_t rows, const float* const* p,
+                     bool output, float** at) {
+  if (!p) return record_error(RA_ERR_INVALID, "%s: NULL pointer array", name);
+  for (int r = 0; r < h->ranks; ++r) {
+    const size_t width = (size_t)(r + 1 < h->ranks ? h->C : h->inner - r * h->C);
+    size_t stride = (width + kGroup - 1) / kGroup;
+    RA_TRY(buf.add(name, r, p[r], 4, stride, &stride, output));
+    at[r] = const_cast<float*>(p[r]);
+  }
+  return RA_OK;
+}
+
+ra_status add_kept(const ra_ffn_ctx* h, FfnBuffers& buf, size_t rows, int bits, bool output, const void* const* gate,
+                   const size_t* gate_strides, const void* const* up, const size_t* up_strides,
+                   const float* const* gate_scales, const float* const* up_scales, FfnArgs* a) {
+  const size_t elem = bits == 8 ? 1 : 2;
+  RA_TRY(add_shards(h, buf, rows, {"gate", gate, gate_strides, elem, false, output}, a->kept[0], a->kept_stride[0]));
+  RA_TRY(add_shards(h, buf, rows, {"up", up, up_strides, elem, false, output}, a->kept[1], a->kept_stride[1]));
+  if (bits == 8) {
+    RA_TRY(add_scales(h, buf, "gate_scales", rows, gate_scales, output, a->scales[0]));
+    RA_TRY(add_scales(h, buf, "up_scales", rows, up_scales, output, a->scales[1]));
+  }
+  return RA_OK;
+}
+
+FfnArgs args_of(const ra_ffn_ctx* h, size_t rows) {
+  FfnArgs a{};
+  a.rows = (int64_t)rows;
+  a.R = h->R;
+  a.dim = h->dim;
+  a.inner = h->inner;
+  a.C = h->C;
+  a.act = h->act;
+  a.grad_f32 = h->grad_dtype == RA_F32;
+  return a;
+}
+
+ra_status check_ffn(ra_ffn_handle h, const void* args) {
+  if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
+  if (!args) return record_error(RA_ERR_INVALID, "NULL arguments");
+  return RA_OK;
+}
+
+ra_status check_ffn_rows(size_t rows) {
+  if (rows > kMaxFfnRows) return record_error(RA_ERR_INVALID, "rows=%zu above 2^30", rows);
+  return RA_OK;
+}
+
+ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& a, cudaStream_t st) {
+  const cudaError_t e = launch_ffn_simple(h->dtype, stage, a, h->sms, st);
+  return e == cudaSuccess ? RA_OK : cuda_error(e, "feed-forward launch");
+}
+
+ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_dtype grad_dtype, ra_ffn_handle* out) {
+  if (!out) return record_error(RA_ERR_INVALID, "NULL handle pointer");
+  if (R < 1 || R > kMaxRanks) return record_error(RA_ERR_INVALID, "R=%d outside [1, %d]", R, kMaxRanks);
+  if (dim < 1 || dim > kMaxDim) return record_error(RA_ERR_INVALID, "dim=%d outside [1, %d]", dim, kMaxDim);
+  if (inner < 1 || inner > (size_t)kMaxInner)
+    return record_error(RA_ERR_INVALID, "inner=%zu outside [1, %d]", inner, kMaxInner);
+  if (dtype != RA_BF16 && dtype != RA_F16)
+    return record_error(RA_ERR_UNSUPPORTED, "dtype %d: bf16 or f16 expected", (int)dtype);
+  if (grad_dtype != RA_F32 && grad_dtype != dtype)
+    return record_error(RA_ERR_UNSUPPORTED, "gradient dtype %d: f32 or the block's type expected", (int)grad_dtype);
+  if (act != RA_SILU && act != RA_GELU) return record_error(RA_ERR_INVALID, "activation %d", act);
+  int dev = -1, sms = 0;
+  RA_TRY(device_of(&dev, &sms));
+  ra_ffn_ctx* h = new (std::nothrow) ra_ffn_ctx();
+  if (!h) return record_error(RA_ERR_OOM, "host allocation failed");
+  h->R = R;
+  h->dim = dim;
+  h->inner = (int)inner;
+  h->C = (h->inner + R - 1) / R;
+  h->ranks = (h->inner + h->C - 1) / h->C;
+  h->device = dev;
+  h->sms = sms;
+  h->dtype = dtype;
+  h->grad_dtype = grad_dtype;
+  h->act = act;
+  *out = h;
+  return RA_OK;
+}
+
+ra_status ffn_forward(ra_ffn_handle h, const ra_ffn_forward_args* g, cudaStream_t st) {
+  RA_TRY(check_ffn(h, g));
+  if (g->keep_bits != 0 && g->keep_bits != 8 && g->keep_bits != 16)
+    return record_error(RA_ERR_INVALID, "keep_bits=%d: 0, 8 or 16 expected", g->keep_bits);
+  RA_TRY(check_ranks("xs", g->xs, h->R));
+  if (g->rows == 0) return RA_OK;
+  RA_TRY(check_ffn_rows(g->rows));
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+  FfnArgs a = args_of(h, g->rows);
+  a.keep_bits = g->keep_bits;
+  FfnBuffers buf(h->device, h->check_pointers, g->rows);
+  RA_TRY(add_ranks(h, buf, "x", g->x, g->xs, g->x_stride, false, a.x, &a.x_stride));
+  const Shards weights[3] = {{"w_gate", g->w_gate, g->w_gate_strides, 2, true, false},
+                             {"w_up", g->w_up, g->w_up_strides, 2, true, false},
+                             {"w_down", g->w_down, g->w_down_strides, 2, true, false}};
+  for (int k = 0; k < 3; ++k)
+    RA_TRY(add_shards(h, buf, g->rows, weights[k], const_cast<void**>(a.w[k]), a.w_stride[k]));
+  RA_TRY(add_shards(h, buf, g->rows, {"hidden", (const void* const*)g->hidden, g->hidden_strides, 2, false, true},
+                    a.hidden, a.hidden_stride));
+  RA_TRY(add_ranks(h, buf, "out", (const void* const*)g->out, h->R, g->out_stride, true,
+                   const_cast<const void**>(a.out), &a.out_stride));
+  if (g->keep_bits)
+    RA_TRY(add_kept(h, buf, g->rows, g->keep_bits, true, (const void* const*)g->gate, g->gate_strides,
+                    (const void* const*)g->up, g->up_strides, (const float* const*)g->gate_scales,
+                    (const float* const*)g->up_scales, &a));
+  RA_TRY(buf.check());
+  RA_TRY(run(h, kFfnHidden, a, st));
+  return run(h, kFfnOut, a, st);
+}
+
+ra_status ffn_backward(ra_ffn_handle h, const ra_ffn_backward_args* g, cudaStream_t st) {
+  RA_TRY(check_ffn(h, g));
+  if (g->keep_bits != 8 && g->keep_bits != 16)
+    return record_error(RA_ERR_INVALID, "keep_bits=%d: 8 or 16 expected", g->keep_bits);
+  if (g->grad_w_down && !g->hidden) return record_error(RA_ERR_INVALID, "grad_w_down without hidden");
+  RA_TRY(check_ranks("grads", g->grads, h->R));
+  const bool need_x = g->grad_w_gate || g->grad_w_up;
+  if (need_x) RA_TRY(check_ranks("xs", g->xs, h->R));
+  RA_TRY(check_ffn_rows(g->rows));
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+  FfnArgs a = args_of(h, g->rows);
+  a.keep_bits = g->keep_bits;
+  const size_t gb = bytes_of(h->grad_dtype);
+  FfnBuffers buf(h->device, h->check_pointers, g->rows);
+  const Shards grads[3] = {{"grad_w_gate", (const void* const*)g->grad_w_gate, g->grad_w_gate_strides, gb, true, true},
+                           {"grad_w_up", (const void* const*)g->grad_w_up, g->grad_w_up_strides, gb, true, true},
+                           {"grad_w_down", (const void* const*)g->grad_w_down, g->grad_w_down_strides, gb, true, true}};
+  for (int k = 0; k < 3; ++k)
+    if (grads[k].at) RA_TRY(add_shards(h, buf, g->rows, grads[k], a.grad_w[k], a.grad_w_stride[k]));
+  const bool any_w = g->grad_w_gate || g->grad_w_up || g->grad_w_down;
+  if (g->rows) {
+    RA_TRY(add_ranks(h, buf, "grad_out", g->grad_out, g->grads, g->grad_out_stride, false, a.grad_out,
+                     &a.grad_out_stride));
+    if (need_x) RA_TRY(add_ranks(h, buf, "x", g->x, g->xs, g->x_stride, false, a.x, &a.x_stride));
+    const Shards weights[3] = {{"w_gate", g->w_gate, g->w_gate_strides, 2, true, false},
+                               {"w_up", g->w_up, g->w_up_strides, 2, true, false},
+                               {"w_down", g->w_down, g->w_down_strides, 2, true, false}};
+    for (int k = 0; k < 3; ++k)
+      if (k == 2 || g->grad_x)
+        RA_TRY(add_shards(h, buf, g->rows, weights[k], const_cast<void**>(a.w[k]), a.w_stride[k]));
+    RA_TRY(add_kept(h, buf, g->rows, g->keep_bits, false, g->gate, g->gate_strides, g->up, g->up_strides,
+                    g->gate_scales, g->up_scales, &a));
+    if (g->hidden)
+      RA_TRY(add_shards(h, buf, g->rows, {"hidden", (const void* const*)g->hidden, g->hidden_strides, 2, false, true},
+                        a.hidden, a.hidden_stride));
+    const bool in_place = g->keep_bits == 16;
+    RA_TRY(add_shards(h, buf, g->rows, {"grad_gate", (const void* const*)g->grad_gate, g->grad_gate_strides, 2, false,
+                                        true, in_place ? g->gate : nullptr},
+                      a.grad_pre[0], a.grad_pre_stride[0]));
+    RA_TRY(add_shards(h, buf, g->rows, {"grad_up", (const void* const*)g->grad_up, g->grad_up_strides, 2, false, true,
+                                        in_place ? g->up : nullptr},
+                      a.grad_pre[1], a.grad_pre_stride[1]));
+    if (g->grad_x)
+      RA_TRY(add_ranks(h, buf, "grad_x", (const void* const*)g->grad_x, h->R, g->grad_x_stride, true,
+                       const_cast<const void**>(a.out), &a.out_stride));
+  }
+  RA_TRY(buf.check());
+  if (g->rows) {
+    RA_TRY(run(h, kFfnGradHidden, a, st));
+    if (g->grad_x) RA_TRY(run(h, kFfnGradX, a, st));
+  }
+  return any_w ? run(h, kFfnGradW, a, st) : RA_OK;
+}
+
+// ---------------------------------------------------------------- kept rows
+
+ra_status ckpt_create(int dim, ra_dtype dtype, ra_dtype ndtype, ra_dtype pdtype, ra_ckpt_handle* out) {
+  if (!out) return record_error(RA_ERR_INVALID, "NULL handle pointer");
+  if (dim < 1 || dim > kMaxInner) return record_error(RA_ERR_INVALID, "dim=%d outside [1, %d]", dim, kMaxInner);
+  if (!is_float(dtype)) return record_error(RA_ERR_UNSUPPORTED, "dtype %d: f32, bf16 or f16 expected", (int)dtype);
+  if (!is_float(ndtype))
+    return record_error(RA_ERR_UNSUPPORTED, "normalised dtype %d: f32, bf16 or f16 expected", (int)ndtype);
+  if (pdtype != RA_F32 && pdtype != ndtype)
+    return record_error(RA_ERR_UNSUPPORTED, "parameter dtype %d: f32 or the normalised rows' type expected",
+                        (int)pdtype);
+  int dev = -1, sms = 0;
+  RA_TRY(device_of(&dev, &sms));
+  ra_ckpt_ctx* h = new (std::nothrow) ra_ckpt_ctx();
+  if (!h) return record_error(RA_ERR_OOM, "host allocation failed");
+  h->dim = dim;
+  h->device = dev;
+  h->sms = sms;
+  h->dtype = dtype;
+  h->normed_dtype = ndtype;
+  h->param_dtype = pdtype;
+  *out = h;
+  return RA_OK;
+}
+
+// Rows that start on 16-byte boundaries (codes: 8), whole groups of 8 columns.
+bool rows_wide(const void* p, size_t stride_bytes, size_t rows, size_t to) {
+  return ((uintptr_t)p | (rows > 1 ? stride_bytes : 0)) % to == 0;
+}
+
+ra_status ckpt_store(ra_ckpt_handle h, const ra_ckpt_store_args* g, cudaStream_t st) {
+  RA_TRY(!h ? record_error(RA_ERR_INVALID, "NULL handle") : RA_OK);
+  if (!g) return record_error(RA_ERR_INVALID, "NULL arguments");
+  if (g->rows == 0) return RA_OK;
+  RA_TRY(check_rows(g->rows));
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+  const size_t dim = (size_t)h->dim, b = bytes_of(h->dtype), groups = (dim + kGroup - 1) / kGroup;
+  size_t stride = g->stride, codes_stride = g->codes_stride;
+  Buffers buf(h->device, h->check_pointers, g->rows);
+  RA_TRY(buf.add("values", -1, g->values, b, dim, &stride, false));
+  RA_TRY(buf.add("codes", -1, g->codes, 1, dim, &codes_stride, true));
+  RA_TRY(buf.flat("scales", g->scales, 4, g->rows * groups, true));
+  RA_TRY(buf.check());
+  CkptArgs a{};
+  a.values = const_cast<void*>(g->values);
+  a.codes = reinterpret_cast<int8_t*>(g->codes);
+  a.scales = g->scales;
+  a.rows = (int64_t)g->rows;
+  a.stride = (int64_t)stride;
+  a.codes_stride = (int64_t)codes_stride;
+  a.dim = h->dim;
+  const bool wide = dim % 8 == 0 && rows_wide(g->values, stride * b, g->rows, 16) &&
+                    rows_wide(g->codes, codes_stride, g->rows, 8);
+  const cudaError_t e = launch_ckpt_store(h->dtype, wide, a, h->sms, st);
+  return e == cudaSuccess ? RA_OK : cuda_error(e, "checkpoint store launch");
+}
+
+ra_status ckpt_load(ra_ckpt_handle h, const ra_ckpt_load_args* g, cudaStream_t st) {
+  RA_TRY(!h ? record_error(RA_ERR_INVALID, "NULL handle") : RA_OK);
+  if (!g) return record_error(RA_ERR_INVALID, "NULL arguments");
+  if (g->rows == 0) return RA_OK;
+  if (!g->values && !g->normed) return record_error(RA_ERR_INVALID, "neither values nor normed");
+  RA_TRY(check_rows(g->rows));
+  OnDevice on(h->device);
+  if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+  const size_t dim = (size_t)h->dim, b = bytes_of(h->dtype), nb = bytes_of(h->normed_dtype),
+               pb = bytes_of(h->param_dtype), groups = (dim + kGroup - 1) / kGroup;
+  size_t stride = g->stride, codes_stride = g->codes_stride, normed_stride = g->normed_stride;
+  Buffers buf(h->device, h->check_pointers, g->rows);
+  RA_TRY(buf.add("codes", -1, g->codes, 1, dim, &codes_stride, false));
+  RA_TRY(buf.flat("scales", g->scales, 4, g->rows * groups, false));
+  bool wide = dim % 8 == 0 && rows_wide(g->codes, codes_stride, g->rows, 8);
+  CkptArgs a{};
+  if (g->values) {
+    RA_TRY(buf.add("values", -1, g->values, b, dim, &stride, true));
+    wide = wide && rows_wide(g->values, stride * b, g->rows, 16);
+  }
+  if (g->normed) {
+    RA_TRY(buf.flat("rstd", g->rstd, 4, g->rows, false));
+    RA_TRY(buf.flat("weight", g->weight, pb, dim, false));
+    RA_TRY(buf.add("normed", -1, g->normed, nb, dim, &normed_stride, true));
+    wide = wide && rows_wide(g->normed, normed_stride * nb, g->rows, 16) && (uintptr_t)g->weight % 16 == 0;
+    a.rstd = g->rstd;
+    a.weight = g->weight;
+  }
+  RA_TRY(buf.check());
+  a.values = g->values;
+  a.codes = reinterpret_cast<int8_t*>(const_cast<signed char*>(g->codes));
+  a.scales = const_cast<float*>(g->scales);
+  a.normed = g->normed;
+  a.rows = (int64_t)g->rows;
+  a.stride = (int64_t)stride;
+  a.codes_stride = (int64_t)codes_stride;
+  a.normed_stride = (int64_t)normed_stride;
+  a.dim = h->dim;
+  a.param_f32 = h->param_dtype == RA_F32;
+  const cudaError_t e = launch_ckpt_load(h->dtype, h->normed_dtype, h->param_dtype, wide, a, h->sms, st);
+  return e == cudaSuccess ? RA_OK : cuda_error(e, "checkpoint load launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+ra_status ra_ffn_create(int R, int dim, size_t inner, ra_dtype dtype, ra_activation activation, ra_dtype grad_dtype,
+                        ra_ffn_handle* out) {
+  return guarded([&] { return ffn_create(R, dim, inner, dtype, (int)activation, grad_dtype, out); });
+}
+
+ra_status ra_ffn_destroy(ra_ffn_handle h) {
+  delete h;
+  return RA_OK;
+}
+
+ra_status ra_ffn_set_option(ra_ffn_handle h, int key, long long value) {
+  return guarded([&] { return set_option(h, key, value); });
+}
+
+ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_error* err) {
+  return guarded([&]() -> ra_status {
+    if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
+    OnDevice on(h->device);
+    if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+    const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
+    if (err) std::memset(err, 0, sizeof(*err));
+    return RA_OK;
+  });
+}
+
+ra_status ra_ffn_forward(ra_ffn_handle h, const ra_ffn_forward_args* args, void* stream) {
+  return guarded([&] { return ffn_forward(h, args, static_cast<cudaStream_t>(stream)); });
+}
+
+ra_status ra_ffn_backward(ra_ffn_handle h, const ra_ffn_backward_args* args, void* stream) {
+  return guarded([&] { return ffn_backward(h, args, static_cast<cudaStream_t>(stream)); });
+}
+
+ra_status ra_ckpt_create(int dim, ra_dtype dtype, ra_dtype normed_dtype, ra_dtype param_dtype, ra_ckpt_handle* out) {
+  return guarded([&] { return ckpt_create(dim, dtype, normed_dtype, param_dtype, out); });
+}
+
+ra_status ra_ckpt_destroy(ra_ckpt_handle h) {
+  delete h;
+  return RA_OK;
+}
+
+ra_status ra_ckpt_set_option(ra_ckpt_handle h, int key, long long value) {
+  return guarded([&] { return set_option(h, key, value); });
+}
+
+ra_status ra_ckpt_store(ra_ckpt_handle h, const ra_ckpt_store_args* args, void* stream) {
+  return guarded([&] { return ckpt_store(h, args, static_cast<cudaStream_t>(stream)); });
+}
+
+ra_status ra_ckpt_load(ra_ckpt_handle h, const ra_ckpt_load_args* args, void* stream) {
+  return guarded([&] { return ckpt_load(h, args, static_cast<cudaStream_t>(stream)); });
+}
+
+}  // extern "C"

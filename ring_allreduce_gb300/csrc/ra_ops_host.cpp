@@ -2,18 +2,10 @@
 // (ra_norm_*, ra_vocab_*): handles, argument checks and launches.
 #include <cuda_runtime.h>
 
-#include <cmath>
-#include <cstdio>
-#include <cstring>
 #include <mutex>
-#include <new>
 
-#include "ra.h"
 #include "ra_ops.h"
-
-namespace ra {
-ra_status record_error(ra_status s, const char* fmt, ...);   // ra_host.cpp
-}
+#include "ra_ops_host.h"
 
 namespace {
 
@@ -80,203 +72,12 @@ struct ra_vocab_ctx {
 
 namespace {
 
-using ra::kMaxRanks;
-using ra::record_error;
-
-constexpr int64_t kMaxRows = 0x7FFFFFFF;
-
-ra_status cuda_error(cudaError_t e, const char* what) {
-  cudaGetLastError();   // clear a non-sticky error so the next call starts clean
-  return record_error(e == cudaErrorMemoryAllocation ? RA_ERR_OOM : RA_ERR_CUDA, "%s: %s (%s)", what,
-                      cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-// No C++ exception leaves the C entry points.
-template <class F> ra_status guarded(F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    return RA_ERR_OOM;   // the only ones there are: an error text that could not be stored
-  }
-}
-
-// The handle's device for the duration of a call.
-struct OnDevice {
-  int prev = -1;
-  cudaError_t status;
-  explicit OnDevice(int dev) {
-    status = cudaGetDevice(&prev);
-    if (status == cudaSuccess && prev != dev) {
-      status = cudaSetDevice(dev);
-    } else {
-      prev = -1;   // nothing to put back
-    }
-  }
-  ~OnDevice() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
-bool is_float(int d) { return d == RA_F32 || d == RA_BF16 || d == RA_F16; }
-size_t bytes_of(int d) { return d == RA_F32 ? 4 : 2; }
-
-// One buffer of a call: `rows` rows of `width` bytes, `stride` bytes apart.
-struct Buffer {
-  const char* name;
-  int index;               // -1: the only one of its name
-  uintptr_t lo;
-  size_t width, stride, span;
-  bool output;
-  const void* twin;        // an output may stand in this buffer's place (same address and stride)
-};
-
-// The buffers of one call and what has to hold of them.
-class Buffers {
- public:
-  Buffers(int device, bool check_pointers, size_t rows)
-      : device_(device), rows_(rows), check_pointers_(check_pointers) {}
-
-  // A buffer of rows() rows (or `rows` of them) of `width` elements; `stride`
-  // in elements, made the width where there is one row.  The checked stride comes back.
-  ra_status add(const char* name, int index, const void* p, size_t elem, size_t width, size_t* stride, bool output,
-                size_t rows, const void* twin = nullptr) {
-    if (!p) return record_error(RA_ERR_INVALID, "%s is NULL", label(name, index));
-    if ((uintptr_t)p % elem)
-      return record_error(RA_ERR_INVALID, "%s=%p is not aligned to its elements", label(name, index), p);
-    if (rows <= 1) *stride = width;
-    if (*stride < width)
-      return record_error(RA_ERR_INVALID, "%s: stride %zu below the row's %zu elements", label(name, index), *stride,
-                          width);
-    if (*stride > ((size_t)1 << 46) / rows)
-      return record_error(RA_ERR_INVALID, "%s: stride %zu too large", label(name, index), *stride);
-    if (count_ == kMost) return record_error(RA_ERR_INVALID, "too many buffers");
-    Buffer& b = b_[count_++];
-    b.name = name;
-    b.index = index;
-    b.lo = (uintptr_t)p;
-    b.width = width * elem;
-    b.stride = *stride * elem;
-    b.span = (rows - 1) * b.stride + b.width;
-    b.output = output;
-    b.twin = twin;
-    return RA_OK;
-  }
-  ra_status add(const char* name, int index, const void* p, size_t elem, size_t width, size_t* stride, bool output,
-                const void* twin = nullptr) {
-    return add(name, index, p, elem, width, stride, output, rows_, twin);
-  }
-  // `count` elements in a row
-  ra_status flat(const char* name, const void* p, size_t elem, size_t count, bool output) {
-    size_t stride = count;
-    return add(name, -1, p, elem, count, &stride, output, 1);
-  }
-
-  ra_status check() {
-    for (int i = 0; i < count_; ++i) {
-      if (b_[i].output)
-        for (int k = 0; k < count_; ++k)
-          if (k != i && !(b_[k].output && k < i) && overlap(b_[i], b_[k])) {
-            char other[32];
-            std::strncpy(other, label(b_[k].name, b_[k].index), sizeof(other) - 1);
-            other[sizeof(other) - 1] = 0;
-            return record_error(RA_ERR_INVALID, "output %s overlaps %s", label(b_[i].name, b_[i].index), other);
-          }
-      if (!check_pointers_) continue;
-      cudaPointerAttributes at;
-      const void* p = (const void*)b_[i].lo;
-      const cudaError_t e = cudaPointerGetAttributes(&at, p);
-      if (e != cudaSuccess) {
-        cudaGetLastError();
-        return record_error(RA_ERR_INVALID, "%s=%p: not a CUDA pointer (%s)", label(b_[i].name, b_[i].index), p,
-                            cudaGetErrorName(e));
-      }
-      if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
-        return record_error(RA_ERR_INVALID, "%s=%p: not device memory", label(b_[i].name, b_[i].index), p);
-      if (at.type == cudaMemoryTypeDevice && at.device != device_)
-        return record_error(RA_ERR_INVALID, "%s=%p: memory of device %d, handle is on device %d",
-                            label(b_[i].name, b_[i].index), p, at.device, device_);
-    }
-    register_debug();
-    return RA_OK;
-  }
-
-  // Every row of every buffer so far starts on a 16-byte boundary, and rows
-  // of `row_bytes` hold whole 16-byte vectors.
-  bool aligned(size_t row_bytes) const {
-    uintptr_t bits = row_bytes;
-    for (int i = 0; i < count_; ++i) bits |= b_[i].lo | (b_[i].span > b_[i].width ? b_[i].stride : 0);
-    return bits % 16 == 0;
-  }
-
- private:
-  static constexpr int kMost = 2 * kMaxRanks + 16;
-
-  const char* label(const char* name, int index) {
-    if (index < 0) return name;
-    std::snprintf(text_, sizeof(text_), "%s[%d]", name, index);
-    return text_;
-  }
-
-  static bool overlap(const Buffer& a, const Buffer& b) {
-    if (a.lo >= b.lo + b.span || b.lo >= a.lo + a.span) return false;
-    if (a.output && a.twin && (uintptr_t)a.twin == b.lo && a.lo == b.lo && a.stride == b.stride) return false;
-    if (a.stride == b.stride && a.stride >= a.width + b.width) {
-      // column slices of one matrix: b's columns begin d bytes after a's
-      const size_t s = a.stride;
-      const size_t d = b.lo >= a.lo ? (b.lo - a.lo) % s : (s - (a.lo - b.lo) % s) % s;
-      if (d >= a.width && d + b.width <= s) return false;
-    }
-    return true;
-  }
-
-  void register_debug() {
-#ifdef RA_DEBUG_BOUNDS
-    ra::DebugTable& t = ra::debug_table();
-    t.count = 0;
-    t.report = ra::debug_report();
-    for (int i = 0; i < count_ && t.count < ra::kDebugRanges; ++i, ++t.count) {
-      t.r[t.count].lo = b_[i].lo;
-      t.r[t.count].hi = b_[i].lo + b_[i].span;
-    }
-#endif
-  }
-
-  Buffer b_[kMost];
-  int count_ = 0;
-  int device_;
-  size_t rows_;
-  bool check_pointers_;
-  char text_[32];
-};
-
-#define RA_TRY(call)                       \
-  do {                                     \
-    const ra_status try_status = (call);   \
-    if (try_status != RA_OK) return try_status; \
-  } while (0)
-
-ra_status device_of(int* dev, int* sms) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-  if (e != cudaSuccess) return cuda_error(e, "cudaDeviceGetAttribute");
-  return RA_OK;
-}
-
-ra_status check_rows(size_t rows) {
-  if (rows > (size_t)kMaxRows) return record_error(RA_ERR_INVALID, "rows=%zu too large", rows);
-  return RA_OK;
-}
+using namespace ra;
 
 ra_status check_gate(const void* gate, size_t gate_rows, size_t rows) {
   if (!gate) return RA_OK;
   if (gate_rows < 1 || gate_rows > rows || rows % gate_rows)
     return record_error(RA_ERR_INVALID, "gate_rows=%zu does not divide rows=%zu", gate_rows, rows);
-  return RA_OK;
-}
-
-ra_status check_ranks(const char* name, int count, int R) {
-  if (count != 1 && count != R) return record_error(RA_ERR_INVALID, "%s=%d: 1 or R=%d expected", name, count, R);
   return RA_OK;
 }
 
@@ -686,14 +487,6 @@ static ra_status vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distil
   a.teacher_f32 = g->teacher_dtype == RA_F32;
   const cudaError_t e = ra::launch_vocab_backward(h->dtype, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "distillation's gradient launch");
-}
-
-template <class H> static ra_status set_option(H h, int key, long long value) {
-  if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
-  if (key != RA_OPT_CHECK_POINTERS) return record_error(RA_ERR_INVALID, "option %d: only RA_OPT_CHECK_POINTERS", key);
-  if (value != 0 && value != 1) return record_error(RA_ERR_INVALID, "value %lld: 0 or 1", value);
-  h->check_pointers = value != 0;
-  return RA_OK;
 }
 
 extern "C" {

@@ -1,6 +1,6 @@
 // ra_torch.cpp -- the Python extension _ra_torch: torch tensors checked and
 // marshalled into the argument blocks of the model operators (ra_norm_*,
-// ra_vocab_* of include/ra.h).  A decode step is a few microseconds on the
+// ra_vocab_*, ra_ffn_*, ra_ckpt_* of include/ra.h).  A decode step is a few microseconds on the
 // GPU, so the way to the launch has to be short: about 1 us here for a call
 // of a dozen tensors, 8 to 10 us in interpreted Python.
 //
@@ -28,6 +28,10 @@ struct Api {
   decltype(&ra_vocab_logprobs_backward) logprobs_backward;
   decltype(&ra_vocab_distill) distill;
   decltype(&ra_vocab_distill_backward) distill_backward;
+  decltype(&ra_ffn_forward) ffn_forward;
+  decltype(&ra_ffn_backward) ffn_backward;
+  decltype(&ra_ckpt_store) ckpt_store;
+  decltype(&ra_ckpt_load) ckpt_load;
 } api;
 
 constexpr int kRanks = 32;
@@ -423,8 +427,300 @@ PyObject* distill_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   });
 }
 
+// A list of R tensors, one a rank's shard of `inner` columns (chunk plan: C
+// columns a rank); those of ranks without columns are not looked at.
+struct Shards {
+  void* at[kRanks];
+  size_t strides[kRanks];
+};
+
+// (handle, device, R, dim, inner, dtype, grad_dtype) lead every feed-forward call
+struct FfnConfig {
+  ra_ffn_handle h;
+  Call call;
+  mutable PyObject* made[2 * kRanks];   // lists of what can be gone through once only
+  mutable int made_count = 0;
+  int R;
+  int64_t dim, inner, C;
+  Type type, grad;
+  explicit FfnConfig(Args& a) {
+    h = static_cast<ra_ffn_handle>(a.pointer());
+    call.device = (int)a.number();
+    R = (int)a.number();
+    dim = a.number();
+    inner = a.number();
+    C = (inner + R - 1) / R;
+    type = type_of(a.number());
+    grad = type_of(a.number());
+  }
+  FfnConfig(const FfnConfig&) = delete;
+  ~FfnConfig() {
+    while (made_count) Py_DECREF(made[--made_count]);
+  }
+  PyObject* again(PyObject* o) const {
+    if (o == Py_None || THPVariable_Check(o) || PyList_Check(o) || PyTuple_Check(o) || made_count == 2 * kRanks) return o;
+    PyObject* list = PySequence_List(o);
+    if (!list) PyErr_Clear();
+    if (list) made[made_count++] = list;
+    return list ? list : o;   // what is no sequence is refused where it is looked at
+  }
+  // f(r, width, tensor) for every rank that holds columns
+  template <class F> void each(const char* name, PyObject* o, F&& f) const {
+    PyObject* seq = PySequence_Fast(o, "a sequence of shards is expected");
+    if (!seq) throw std::invalid_argument(std::string(name) + ": a sequence of shards is expected");
+    try {
+      if (PySequence_Fast_GET_SIZE(seq) != R)
+        wrong(name, (std::to_string(R) + " shards are expected, got " + std::to_string(PySequence_Fast_GET_SIZE(seq))).c_str());
+      for (int r = 0; r < R; ++r) {
+        const int64_t width = std::min(C, inner - r * C);
+        if (width > 0) f(r, width, PySequence_Fast_GET_ITEM(seq, r));
+      }
+      Py_DECREF(seq);
+    } catch (...) {
+      Py_DECREF(seq);
+      throw;
+    }
+  }
+  void columns(const char* name, PyObject* o, Type t, int64_t T, Shards* s) const {
+    each(name, o, [&](int r, int64_t width, PyObject* x) { s->at[r] = call.rows(name, x, t, T, width, &s->strides[r]); });
+  }
+  void weights(const char* name, PyObject* o, Type t, Shards* s) const {
+    each(name, o, [&](int r, int64_t width, PyObject* x) { s->at[r] = call.rows(name, x, t, width, dim, &s->strides[r]); });
+  }
+  void scales(const char* name, PyObject* o, int64_t T, float** at) const {
+    each(name, o, [&](int r, int64_t width, PyObject* x) {
+      at[r] = static_cast<float*>(call.flat(name, x, at::kFloat, {T, (width + 127) / 128}));
+    });
+  }
+  // 8 where the shards hold 8-bit codes, 16 where they hold the block's type
+  int bits(PyObject* o) const {
+    int n = 16;
+    each("gate", o, [&](int r, int64_t, PyObject* x) {
+      const at::Tensor* t = strided(x);
+      if (r == 0 && t && t->scalar_type() == at::kChar) n = 8;
+    });
+    return n;
+  }
+};
+
+// Rows of the rank buffers that a call goes by.
+int64_t ranks_rows(const char* name, PyObject* o) {
+  if (THPVariable_Check(o)) return axis(name, o, 3, 1, "rank buffers [rows, dim] are expected");
+  PyObject* seq = PySequence_Fast(o, "a sequence of rank buffers is expected");
+  if (!seq) throw std::invalid_argument(std::string(name) + ": a sequence of rank buffers is expected");
+  PyObject* first = PySequence_Fast_GET_SIZE(seq) ? PySequence_Fast_GET_ITEM(seq, 0) : nullptr;
+  const at::Tensor* t = first ? strided(first) : nullptr;
+  const int64_t n = t && t->dim() == 2 ? t->size(0) : -1;
+  Py_DECREF(seq);
+  if (n < 0) wrong(name, "rank buffers [rows, dim] are expected");
+  return n;
+}
+
+struct Kept {
+  int bits = 0;
+  Shards gate, up;
+  float *gate_scales[kRanks], *up_scales[kRanks];
+  Kept(const FfnConfig& c, PyObject* g, PyObject* u, PyObject* gs, PyObject* us, int64_t T) {
+    if ((g == Py_None) != (u == Py_None)) wrong("gate, up", "they go together");
+    if (g == Py_None) {
+      if (gs != Py_None || us != Py_None) wrong("gate_scales, up_scales", "scales without gate and up");
+      return;
+    }
+    bits = c.bits(g);
+    const Type t = bits == 8 ? at::kChar : c.type;
+    c.columns("gate", g, t, T, &gate);
+    c.columns("up", u, t, T, &up);
+    if (bits == 8) {
+      c.scales("gate_scales", gs, T, gate_scales);
+      c.scales("up_scales", us, T, up_scales);
+    } else if (gs != Py_None || us != Py_None) {
+      wrong("gate_scales, up_scales", "they go with 8-bit codes");
+    }
+  }
+};
+
+PyObject* ffn_forward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  return guarded([&]() -> int {
+    Args a{argv, argv + argc};
+    const FfnConfig c(a);
+    ra_ffn_forward_args g{};
+    void *x[kRanks], *out[kRanks];
+    Shards w[3], hidden;
+    PyObject* xs = c.again(a.next());
+    const int64_t T = ranks_rows("xs", xs);
+    g.rows = (size_t)T;
+    g.xs = c.call.ranks("xs", xs, c.R, true, c.type, T, c.dim, x, &g.x_stride);
+    c.weights("w_gate", c.again(a.next()), c.type, &w[0]);
+    c.weights("w_up", c.again(a.next()), c.type, &w[1]);
+    c.weights("w_down", c.again(a.next()), c.type, &w[2]);
+    c.columns("hidden", c.again(a.next()), c.type, T, &hidden);
+    c.call.ranks("parts", c.again(a.next()), c.R, false, c.type, T, c.dim, out, &g.out_stride);
+    PyObject* kept[4];
+    for (PyObject*& o : kept) o = c.again(a.next());
+    Kept k(c, kept[0], kept[1], kept[2], kept[3], T);
+    g.x = x;
+    g.w_gate = w[0].at;
+    g.w_gate_strides = w[0].strides;
+    g.w_up = w[1].at;
+    g.w_up_strides = w[1].strides;
+    g.w_down = w[2].at;
+    g.w_down_strides = w[2].strides;
+    g.hidden = hidden.at;
+    g.hidden_strides = hidden.strides;
+    g.out = out;
+    g.keep_bits = k.bits;
+    g.gate = k.gate.at;
+    g.gate_strides = k.gate.strides;
+    g.up = k.up.at;
+    g.up_strides = k.up.strides;
+    g.gate_scales = k.gate_scales;
+    g.up_scales = k.up_scales;
+    return api.ffn_forward(c.h, &g, a.pointer());
+  });
+}
+
+PyObject* ffn_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  return guarded([&]() -> int {
+    Args a{argv, argv + argc};
+    const FfnConfig c(a);
+    ra_ffn_backward_args g{};
+    void *dy[kRanks], *x[kRanks], *dx[kRanks];
+    Shards w[3], hidden, pre[2], gw[3];
+    PyObject* grad_parts = c.again(a.next());
+    PyObject* xs = c.again(a.next());
+    PyObject* weights[3];
+    for (PyObject*& o : weights) o = c.again(a.next());
+    PyObject* kept[2];
+    for (PyObject*& o : kept) o = c.again(a.next());
+    PyObject* hid = c.again(a.next());
+    PyObject* pres[2];
+    for (PyObject*& o : pres) o = c.again(a.next());
+    PyObject* grad_xs = c.again(a.next());
+    PyObject* grads[3];
+    for (PyObject*& o : grads) o = c.again(a.next());
+    PyObject* gate_scales = c.again(a.next());
+    PyObject* up_scales = c.again(a.next());
+    const int64_t T = ranks_rows("grad_parts", grad_parts);
+    g.rows = (size_t)T;
+    g.grads = c.call.ranks("grad_parts", grad_parts, c.R, true, c.type, T, c.dim, dy, &g.grad_out_stride);
+    g.grad_out = dy;
+    if (kept[0] == Py_None) wrong("gate", "what forward kept is expected");
+    Kept k(c, kept[0], kept[1], gate_scales, up_scales, T);
+    g.keep_bits = k.bits;
+    g.gate = k.gate.at;
+    g.gate_strides = k.gate.strides;
+    g.up = k.up.at;
+    g.up_strides = k.up.strides;
+    g.gate_scales = k.gate_scales;
+    g.up_scales = k.up_scales;
+    c.weights("w_down", weights[2], c.type, &w[2]);
+    g.w_down = w[2].at;
+    g.w_down_strides = w[2].strides;
+    if (hid != Py_None) {
+      c.columns("hidden", hid, c.type, T, &hidden);
+      g.hidden = hidden.at;
+      g.hidden_strides = hidden.strides;
+    }
+    c.columns("grad_gate", pres[0], c.type, T, &pre[0]);
+    c.columns("grad_up", pres[1], c.type, T, &pre[1]);
+    g.grad_gate = pre[0].at;
+    g.grad_gate_strides = pre[0].strides;
+    g.grad_up = pre[1].at;
+    g.grad_up_strides = pre[1].strides;
+    if (grad_xs != Py_None) {
+      c.weights("w_gate", weights[0], c.type, &w[0]);
+      c.weights("w_up", weights[1], c.type, &w[1]);
+      g.w_gate = w[0].at;
+      g.w_gate_strides = w[0].strides;
+      g.w_up = w[1].at;
+      g.w_up_strides = w[1].strides;
+      c.call.ranks("grad_xs", grad_xs, c.R, false, c.type, T, c.dim, dx, &g.grad_x_stride);
+      g.grad_x = dx;
+    }
+    if (grads[0] != Py_None || grads[1] != Py_None) {
+      g.xs = c.call.ranks("xs", xs, c.R, true, c.type, T, c.dim, x, &g.x_stride);
+      g.x = x;
+    }
+    const char* names[3] = {"grad_w_gate", "grad_w_up", "grad_w_down"};
+    for (int i = 0; i < 3; ++i)
+      if (grads[i] != Py_None) c.weights(names[i], grads[i], c.grad, &gw[i]);
+    if (grads[0] != Py_None) {
+      g.grad_w_gate = gw[0].at;
+      g.grad_w_gate_strides = gw[0].strides;
+    }
+    if (grads[1] != Py_None) {
+      g.grad_w_up = gw[1].at;
+      g.grad_w_up_strides = gw[1].strides;
+    }
+    if (grads[2] != Py_None) {
+      g.grad_w_down = gw[2].at;
+      g.grad_w_down_strides = gw[2].strides;
+    }
+    return api.ffn_backward(c.h, &g, a.pointer());
+  });
+}
+
+// (handle, device, dim, dtype, normed_dtype, param_dtype) lead the calls for kept rows
+struct CkptConfig {
+  ra_ckpt_handle h;
+  Call call;
+  int64_t dim;
+  Type type, normed, param;
+  explicit CkptConfig(Args& a) {
+    h = static_cast<ra_ckpt_handle>(a.pointer());
+    call.device = (int)a.number();
+    dim = a.number();
+    type = type_of(a.number());
+    normed = type_of(a.number());
+    param = type_of(a.number());
+  }
+  float* scales(PyObject* o, int64_t T) const {
+    return static_cast<float*>(call.flat("scales", o, at::kFloat, {T, (dim + 127) / 128}));
+  }
+};
+
+PyObject* ckpt_store(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  return guarded([&]() -> int {
+    Args a{argv, argv + argc};
+    const CkptConfig c(a);
+    ra_ckpt_store_args g{};
+    PyObject* values = a.next();
+    const int64_t T = axis("values", values, 2, 0, "a tensor [rows, dim] is expected");
+    g.rows = (size_t)T;
+    g.values = c.call.rows("values", values, c.type, T, c.dim, &g.stride);
+    g.codes = static_cast<signed char*>(c.call.rows("codes", a.next(), at::kChar, T, c.dim, &g.codes_stride));
+    g.scales = c.scales(a.next(), T);
+    return api.ckpt_store(c.h, &g, a.pointer());
+  });
+}
+
+PyObject* ckpt_load(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  return guarded([&]() -> int {
+    Args a{argv, argv + argc};
+    const CkptConfig c(a);
+    ra_ckpt_load_args g{};
+    PyObject* codes = a.next();
+    const int64_t T = axis("codes", codes, 2, 0, "a tensor [rows, dim] is expected");
+    g.rows = (size_t)T;
+    g.codes = static_cast<signed char*>(c.call.rows("codes", codes, at::kChar, T, c.dim, &g.codes_stride));
+    g.scales = c.scales(a.next(), T);
+    PyObject* values = a.next();
+    if (values != Py_None) g.values = c.call.rows("values", values, c.type, T, c.dim, &g.stride);
+    PyObject* rstd = a.next();
+    PyObject* weight = a.next();
+    PyObject* normed = a.next();
+    if (normed != Py_None) {
+      g.rstd = static_cast<float*>(c.call.flat("rstd", rstd, at::kFloat, {T}));
+      g.weight = c.call.flat("weight", weight, c.param, {c.dim});
+      g.normed = c.call.rows("normed", normed, c.normed, T, c.dim, &g.normed_stride);
+    }
+    return api.ckpt_load(c.h, &g, a.pointer());
+  });
+}
+
 // bind(norm_forward, norm_backward, logprobs, logprobs_backward, distill,
-// distill_backward): the library's functions, by address
+// distill_backward, ffn_forward, ffn_backward, ckpt_store, ckpt_load): the
+// library's functions, by address
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   return guarded([&]() -> int {
     Args a{argv, argv + argc};
@@ -434,6 +730,10 @@ PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     api.logprobs_backward = reinterpret_cast<decltype(api.logprobs_backward)>(a.pointer());
     api.distill = reinterpret_cast<decltype(api.distill)>(a.pointer());
     api.distill_backward = reinterpret_cast<decltype(api.distill_backward)>(a.pointer());
+    api.ffn_forward = reinterpret_cast<decltype(api.ffn_forward)>(a.pointer());
+    api.ffn_backward = reinterpret_cast<decltype(api.ffn_backward)>(a.pointer());
+    api.ckpt_store = reinterpret_cast<decltype(api.ckpt_store)>(a.pointer());
+    api.ckpt_load = reinterpret_cast<decltype(api.ckpt_load)>(a.pointer());
     return 0;
   });
 }
@@ -441,6 +741,7 @@ PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
 #define RA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {RA_METHOD(bind), RA_METHOD(norm_forward), RA_METHOD(norm_backward), RA_METHOD(logprobs),
                          RA_METHOD(logprobs_backward), RA_METHOD(distill), RA_METHOD(distill_backward),
+                         RA_METHOD(ffn_forward), RA_METHOD(ffn_backward), RA_METHOD(ckpt_store), RA_METHOD(ckpt_load),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ra_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,5 +1,5 @@
-"""Model operators around the sums over ranks (``ra_norm_*`` and ``ra_vocab_*``
-of include/ra.h), on torch CUDA tensors.
+"""Model operators around the sums over ranks (``ra_norm_*``, ``ra_vocab_*``,
+``ra_ffn_*`` and ``ra_ckpt_*`` of include/ra.h), on torch CUDA tensors.
 
 ``BlockNorm``: the end of a tensor-parallel block.  The R ranks' partial
 products are summed, normalised, gated, added to the residual stream and
@@ -10,6 +10,15 @@ normalised for the next block, in one pass; and the gradient of that.
 ``ra_chunk_plan(R, V)`` lays them out): log probabilities of given tokens with
 entropy and top alternatives, distillation from a teacher's top logits, and
 the gradients of both.
+
+``FeedForward``: the gated feed-forward block between two block ends.  Its
+input is what BlockNorm.forward normalised, its R partial products are what the
+next one sums; backward takes what BlockNorm.backward gives every partial, and
+gives the R partial gradients that the previous one sums.  Its activations may
+be kept in 8 bits.
+
+``Checkpoint``: rows kept in 8 bits until the backward pass (BlockNorm's total
+and residual stream), and brought back, with the normalised rows.
 
 The caller owns every buffer, outputs included.  Where R rank buffers are
 asked for, a list of R tensors or one tensor with a leading axis of R will do.
@@ -29,9 +38,11 @@ from . import binding
 from . import build as _build
 from .binding import RAError, _lib, _P
 
-__all__ = ["BlockNorm", "VocabHead"]
+__all__ = ["BlockNorm", "VocabHead", "FeedForward", "Checkpoint"]
 
 _CODE = {"f32": 0, "bf16": 1, "f16": 3}     # ra_dtype
+_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+_ACTIVATION = {"silu": 0, "gelu": 1}        # ra_activation
 
 
 def _load():
@@ -43,7 +54,8 @@ def _load():
     ext = importlib.import_module("." + _build.TORCH_EXT, __package__)
     ext.bind(*(ctypes.cast(f, _P).value for f in (
         _lib.ra_norm_forward, _lib.ra_norm_backward, _lib.ra_vocab_logprobs, _lib.ra_vocab_logprobs_backward,
-        _lib.ra_vocab_distill, _lib.ra_vocab_distill_backward)))
+        _lib.ra_vocab_distill, _lib.ra_vocab_distill_backward, _lib.ra_ffn_forward, _lib.ra_ffn_backward,
+        _lib.ra_ckpt_store, _lib.ra_ckpt_load)))
     return ext
 
 
@@ -59,11 +71,11 @@ class _Handle:
         _code("dtype", dtype)
         self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
 
-    def _opened(self, h, R, *config):
+    def _opened(self, h, *config):
         """The handle and what the extension's checks go by."""
         # the extension has seen every tensor to be on the device
         binding._check(self._set_option(h, binding.Option.CHECK_POINTERS, 0))
-        self._config = (h.value, self.device, R, *config)
+        self._config = (h.value, self.device, *config)
 
     def _call(self, fn, stream, *args):
         if self._config is None:
@@ -224,3 +236,115 @@ class VocabHead(_Handle):
         """grads (R shards, may be the logits' own) = the logits' gradient of
         sum(grad_loss * loss); lse is what distill wrote."""
         self._call(_ext.distill_backward, stream, shards, teacher_ids, teacher_logits, lse, grad_loss, grads)
+
+
+class FeedForward(_Handle):
+    """A gated feed-forward block of `dim` columns outside and `inner` inside, over R ranks.
+
+    Rank r holds the inner columns of chunk r of ``ra_chunk_plan(R, inner)``
+    (`widths`), and of each weight the rows [width, dim] for them.  dtype:
+    "bf16" or "f16"; activation: "silu" (a / (1 + e^-a)) or "gelu"
+    (a (1 + erf(a / sqrt 2)) / 2); grad_dtype: the weights' gradients', "f32" or
+    dtype, which is the default.
+
+    Products run on the tensor cores where the rows of their operands start on
+    16-byte boundaries: `dim` a multiple of 8 (or padded rows), and hidden,
+    grad_gate and grad_up as ``rows`` makes them.  Others take some thirty
+    times as long."""
+
+    _destroy, _set_option = staticmethod(_lib.ra_ffn_destroy), staticmethod(_lib.ra_ffn_set_option)
+
+    def __init__(self, R, dim, inner, dtype="bf16", activation="silu", grad_dtype=None):
+        super().__init__(dtype)
+        self.R, self.dim, self.inner, self.dtype = int(R), int(dim), int(inner), dtype
+        if self.inner < 0:
+            raise ValueError(f"inner {inner}")
+        if activation not in _ACTIVATION:
+            raise ValueError(f"activation {activation!r}: one of {sorted(_ACTIVATION)} is expected")
+        codes = _code("dtype", dtype), _code("grad_dtype", grad_dtype or dtype)
+        h = _P()
+        binding._check(_lib.ra_ffn_create(self.R, self.dim, self.inner, codes[0], _ACTIVATION[activation], codes[1],
+                                          ctypes.byref(h)))
+        self._opened(h, self.R, self.dim, self.inner, *codes)
+        #: inner columns of each rank
+        self.widths = [n for _, n in binding.ra_chunk_plan(self.R, self.inner)]
+
+    def rows(self, T, dtype=None):
+        """R new tensors [T, width] of dtype (default: the block's) whose rows start on 16-byte boundaries."""
+        dtype = dtype or _TORCH[self.dtype]
+        to = 16 // dtype.itemsize
+        return [torch.empty((T, (n + to - 1) // to * to), dtype=dtype, device=f"cuda:{self.device}")[:, :n]
+                for n in self.widths]
+
+    def codes(self, T):
+        """What keeps one projection in 8 bits: R new tensors [T, width] of codes, and R [T, ceil(width / 128)] of scales."""
+        return self.rows(T, torch.int8), [torch.empty((T, (n + 127) // 128), device=f"cuda:{self.device}")
+                                          for n in self.widths]
+
+    def forward(self, xs, w_gate, w_up, w_down, hidden, parts, gate=None, up=None, gate_scales=None, up_scales=None,
+                stream=None):
+        """Per rank: a = x w_gate^T, b = x w_up^T; hidden = activation(a) b; parts = hidden w_down.
+
+        xs: 1 or R x [T, dim]; weights: R x [width, dim]; hidden: R x [T, width];
+        parts: R x [T, dim].  gate, up: R x [T, width] each, keep a and b for
+        backward: in the block's type, or, as int8 with gate_scales and
+        up_scales (R x [T, ceil(width / 128)], float32), in 8 bits (see ``codes``)."""
+        self._call(_ext.ffn_forward, stream, xs, w_gate, w_up, w_down, hidden, parts, gate, up, gate_scales, up_scales)
+
+    def backward(self, grad_parts, xs, w_gate, w_up, w_down, gate, up, hidden, grad_gate, grad_up, grad_xs=None,
+                 grad_w_gate=None, grad_w_up=None, grad_w_down=None, gate_scales=None, up_scales=None, stream=None):
+        """The gradient of forward, from the kept gate and up.
+
+        grad_parts: 1 or R x [T, dim], the gradient of every rank's partial
+        product.  Writes grad_gate and grad_up (R x [T, width], the gradients
+        of a and b), hidden (as forward wrote it, from the kept a and b; None
+        where grad_w_down is), grad_xs (R x [T, dim], the ranks' partial
+        gradients of x) and the weights' gradients (R x [width, dim] of
+        grad_dtype), each None where it is not wanted.  16-bit gate and up may be overwritten by grad_gate and
+        grad_up."""
+        self._call(_ext.ffn_backward, stream, grad_parts, xs, w_gate, w_up, w_down, gate, up, hidden, grad_gate,
+                   grad_up, grad_xs, grad_w_gate, grad_w_up, grad_w_down, gate_scales, up_scales)
+
+    def device_status(self, stream=None):
+        """(Status, DeviceError) after synchronising the stream: whether a bounded wait of a product on this device gave up."""
+        err = binding.DeviceError()
+        if self._config is None:
+            raise ValueError("the handle is closed")
+        raw = _current_stream(self.device) if stream is None else binding._stream(stream)
+        status = _lib.ra_ffn_get_device_status(self._config[0], raw, ctypes.byref(err))
+        if status not in (binding.Status.OK, binding.Status.ERR_TIMEOUT):
+            raise RAError(status, binding.ra_last_error())
+        return binding.Status(status), err
+
+
+class Checkpoint(_Handle):
+    """Rows of `dim` columns kept in 8 bits: int8 codes, and a float32 scale for every 128 columns of a row.
+
+    A code stands for code * scale, at most half a scale (a 254th of the
+    group's largest magnitude) from the value.  A group with an infinity or a
+    NaN comes back as NaN, one with nothing above 2^-110 as zeros.  dtype:
+    the rows'; normed_dtype, param_dtype: those of the normalised rows that
+    load gives and of their weight (default: dtype; normed_dtype).
+    BlockNorm's total and residual_out, kept so, come back for its backward
+    pass; the normalised rows, for the products that took them, need not be
+    kept at all."""
+
+    _destroy, _set_option = staticmethod(_lib.ra_ckpt_destroy), staticmethod(_lib.ra_ckpt_set_option)
+
+    def __init__(self, dim, dtype="bf16", normed_dtype=None, param_dtype=None):
+        super().__init__(dtype)
+        self.dim = int(dim)
+        codes = [_code("dtype", dtype), _code("normed_dtype", normed_dtype or dtype)]
+        codes.append(_code("param_dtype", param_dtype or normed_dtype or dtype))
+        h = _P()
+        binding._check(_lib.ra_ckpt_create(self.dim, *codes, ctypes.byref(h)))
+        self._opened(h, self.dim, *codes)
+
+    def store(self, values, codes, scales, stream=None):
+        """values [T, dim] into codes [T, dim] (int8) and scales [T, ceil(dim / 128)] (float32)."""
+        self._call(_ext.ckpt_store, stream, values, codes, scales)
+
+    def load(self, codes, scales, values=None, rstd=None, weight=None, normed=None, stream=None):
+        """values [T, dim] = codes * scales; normed [T, dim] = codes * scales * rstd * weight, with rstd [T]
+        (row 1 of what BlockNorm.forward wrote) and weight [dim].  Either may be None, not both."""
+        self._call(_ext.ckpt_load, stream, codes, scales, values, rstd, weight, normed)
