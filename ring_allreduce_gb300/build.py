@@ -41,6 +41,7 @@ DTYPES = ["RA_F32", "RA_BF16", "RA_I32", "RA_F16", "RA_F64", "RA_I64"]
 NORM_TYPES = [("DF32", "DF32"), ("DBF16", "DBF16"), ("DBF16", "DF32"), ("DF16", "DF16"), ("DF16", "DF32")]
 UNITS = ([(src, os.path.splitext(src)[0], {}) for src in SOURCES] +
          [("ra_direct_inst.cu", "ra_direct_" + dt[3:].lower(), {"RA_INST_DTYPE": dt}) for dt in DTYPES] +
+         [("ra_ffn_mma_inst.cu", "ra_ffn_mma_" + dt[3:].lower(), {"RA_INST_DTYPE": dt}) for dt in ("RA_BF16", "RA_F16")] +
          [("ra_norm_inst.cu", f"ra_norm_{d}_{rd}".lower(), {"RA_INST_D": d, "RA_INST_RD": rd})
           for d, rd in NORM_TYPES])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -75,7 +76,8 @@ KERNEL_SOURCES = {
     "ll": ["ra_ll.cu", "ra_ll.h", "ra_device.cuh", "ra_internal.h"],
     "norm": ["ra_norm.cu", "ra_norm.cuh", "ra_norm_inst.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
     "vocab": ["ra_vocab.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
-    "ffn": ["ra_ffn_simple.cu", "ra_ffn.cuh", "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
+    "ffn": ["ra_ffn_mma_inst.cu", "ra_ffn_mma.cuh", "ra_ffn_mma.h", "ra_tensor.cuh", "ra_ffn_simple.cu", "ra_ffn.cuh",
+            "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
     "ckpt": ["ra_ckpt.cu", "ra_ffn.cuh", "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
 }
 

@@ -1,7 +1,10 @@
 // ra_ffn_host.cpp -- host side of the feed-forward block and of rows kept in 8
-// bits (ra_ffn_*, ra_ckpt_* of include/ra.h): handles, argument checks, and
-// which kernel runs.
+// bits (ra_ffn_*, ra_ckpt_* of include/ra.h): handles, argument checks, the
+// tensor maps of a call's operands, and which kernel runs.
+#include <cuda.h>
+
 #include "ra_ffn.h"
+#include "ra_ffn_mma.h"
 #include "ra_ops_host.h"
 
 struct ra_ffn_ctx {
@@ -9,6 +12,7 @@ struct ra_ffn_ctx {
   ra_dtype dtype, grad_dtype;
   int act;
   bool check_pointers = true;
+  ra_device_error* err;   // the device's record of waits that gave up
 };
 
 struct ra_ckpt_ctx {
@@ -110,8 +114,141 @@ ra_status check_ffn_rows(size_t rows) {
   return RA_OK;
 }
 
-ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& a, cudaStream_t st) {
-  const cudaError_t e = launch_ffn_simple(h->dtype, stage, a, h->sms, st);
+// A matrix operand [rows][columns] of a product; no columns: there is none.
+struct Operand {
+  const void* p;
+  int64_t rows, columns, stride;
+  bool aligned() const { return (uintptr_t)p % 16 == 0 && (rows <= 1 || stride * 2 % 16 == 0); }
+};
+
+using Encode = decltype(&cuTensorMapEncodeTiled);
+
+Encode encoder() {
+  static const Encode f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return Encode(nullptr);
+    return reinterpret_cast<Encode>(p);
+  }();
+  return f;
+}
+
+// The map that fetches boxes of 64 columns and `box_rows` rows of an operand, swizzled.
+bool encode(CUtensorMap* map, ra_dtype dtype, const Operand& o, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)o.columns, (cuuint64_t)o.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.stride * 2 : (o.columns * 2 + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
+  return encoder()(map, dtype == RA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                   const_cast<void*>(o.p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The operands of a stage for rank r: `a[i]` and `b[i]` as MmaArgs has them.
+struct Operands {
+  Operand a[3] = {}, b[2] = {};
+  int as = 1, bs = 1;
+  Operands(FfnStage stage, const FfnArgs& f, int r) {
+    const int64_t width = f.width(r), T = f.rows, D = f.dim;
+    const Operand x{f.x[r], T, D, f.x_stride}, dy{f.grad_out[r], T, D, f.grad_out_stride},
+        hidden{f.hidden[r], T, width, f.hidden_stride[r]};
+    Operand w[3], pre[2];
+    for (int k = 0; k < 3; ++k) w[k] = {f.w[k][r], width, D, f.w_stride[k][r]};
+    for (int k = 0; k < 2; ++k) pre[k] = {f.grad_pre[k][r], T, width, f.grad_pre_stride[k][r]};
+    switch (stage) {
+      case kFfnHidden:
+        a[0] = x;
+        b[0] = w[0];
+        b[1] = w[1];
+        bs = 2;
+        break;
+      case kFfnOut:
+        a[0] = hidden;
+        b[0] = w[2];
+        break;
+      case kFfnGradHidden:
+        a[0] = dy;
+        b[0] = w[2];
+        break;
+      case kFfnGradX:
+        a[0] = pre[0];
+        a[1] = pre[1];
+        b[0] = w[0];
+        b[1] = w[1];
+        as = bs = 2;
+        break;
+      default:   // what is not wanted has no operands
+        as = 3;
+        bs = 2;
+        for (int k = 0; k < 3; ++k)
+          if (f.grad_w[k][r]) {
+            a[k] = k == 2 ? hidden : pre[k];
+            b[k == 2] = k == 2 ? dy : x;
+          }
+    }
+  }
+};
+
+// Rows of every rank's buffer on 16-byte boundaries.
+bool on_grid(const ra_ffn_ctx* h, void* const* at, const int64_t* strides, int64_t elem, int64_t rows) {
+  uintptr_t bits = 0;
+  for (int r = 0; r < h->ranks; ++r) bits |= (uintptr_t)at[r] | (rows > 1 ? (uintptr_t)(strides[r] * elem) : 0);
+  return bits % 16 == 0;
+}
+
+ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st) {
+  MmaArgs a;
+  bool aligned = true;
+  for (int r = 0; r < h->ranks && aligned; ++r) {
+    const Operands o(stage, f, r);
+    for (int i = 0; i < o.as; ++i) aligned = aligned && o.a[i].aligned();
+    for (int i = 0; i < o.bs; ++i) aligned = aligned && o.b[i].aligned();
+  }
+  if (!aligned) {
+    const cudaError_t e = launch_ffn_simple(h->dtype, stage, f, h->sms, st);
+    return e == cudaSuccess ? RA_OK : cuda_error(e, "feed-forward launch");
+  }
+  if (!encoder()) return record_error(RA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+  // rows across the terms of a sum are fetched 64 of them at a time
+  const bool a_mn = stage == kFfnGradW, b_mn = stage == kFfnOut || stage == kFfnGradX || stage == kFfnGradW;
+  for (int r = 0; r < h->ranks; ++r) {
+    const Operands o(stage, f, r);
+    bool ok = true;
+    for (int i = 0; i < o.as; ++i)
+      if (o.a[i].p && f.rows) ok = ok && encode(&a.a[i][r], h->dtype, o.a[i], a_mn ? 64 : 128);
+    for (int i = 0; i < o.bs; ++i)
+      if (o.b[i].p && o.b[i].rows) ok = ok && encode(&a.b[i][r], h->dtype, o.b[i], b_mn ? 64 : 128);
+    if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  }
+  a.f = f;
+  a.err = h->err;
+  a.segments = stage == kFfnGradX ? 2 : 1;
+  const int64_t gb = f.grad_f32 ? 4 : 2;
+  a.vec = 0;
+  if (f.hidden[0] && on_grid(h, f.hidden, f.hidden_stride, 2, f.rows)) a.vec |= kVecHidden;
+  if (f.keep_bits && on_grid(h, f.kept[0], f.kept_stride[0], f.keep_bits / 8, f.rows) &&
+      on_grid(h, f.kept[1], f.kept_stride[1], f.keep_bits / 8, f.rows))
+    a.vec |= kVecKept;
+  if (f.grad_pre[0][0] && on_grid(h, f.grad_pre[0], f.grad_pre_stride[0], 2, f.rows) &&
+      on_grid(h, f.grad_pre[1], f.grad_pre_stride[1], 2, f.rows))
+    a.vec |= kVecPre;
+  uintptr_t out = f.rows > 1 ? (uintptr_t)f.out_stride * 2 : 0;
+  for (int r = 0; r < h->R; ++r) out |= (uintptr_t)f.out[r];
+  if (out % 16 == 0) a.vec |= kVecOut;
+  bool grads = true;
+  for (int k = 0; k < 3; ++k)
+    if (f.grad_w[k][0]) grads = grads && on_grid(h, f.grad_w[k], f.grad_w_stride[k], gb, h->C);
+  if (grads) a.vec |= kVecGradW;
+  const bool wide = stage == kFfnHidden;
+  const int64_t M = stage == kFfnGradW ? h->C : f.rows, N = wide || stage == kFfnGradHidden ? h->C : h->dim;
+  a.tiles_m = (int)((M + 255) / 256);
+  a.tiles_n = (int)(wide ? (N + 127) / 128 : (N + 255) / 256);
+  a.tiles = (int64_t)a.tiles_m * a.tiles_n * (stage == kFfnGradW ? 3 * h->R : h->R);
+  const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
+  const cudaError_t e = h->dtype == RA_BF16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st)
+                                            : launch_ffn_mma<RA_F16>(as, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "feed-forward launch");
 }
 
@@ -128,8 +265,12 @@ ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_d
   if (act != RA_SILU && act != RA_GELU) return record_error(RA_ERR_INVALID, "activation %d", act);
   int dev = -1, sms = 0;
   RA_TRY(device_of(&dev, &sms));
+  ra_device_error* err = nullptr;
+  const cudaError_t e = ffn_error_record(&err);
+  if (e != cudaSuccess) return cuda_error(e, "error record");
   ra_ffn_ctx* h = new (std::nothrow) ra_ffn_ctx();
   if (!h) return record_error(RA_ERR_OOM, "host allocation failed");
+  h->err = err;
   h->R = R;
   h->dim = dim;
   h->inner = (int)inner;
@@ -356,7 +497,12 @@ ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_erro
     if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
     const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
-    if (err) std::memset(err, 0, sizeof(*err));
+    ra_device_error got;
+    cudaError_t c = cudaMemcpy(&got, h->err, sizeof(got), cudaMemcpyDeviceToHost);
+    if (c == cudaSuccess && got.code) c = cudaMemset(h->err, 0, sizeof(got));
+    if (c != cudaSuccess) return cuda_error(c, "error record");
+    if (err) *err = got;
+    if (got.code) return record_error(RA_ERR_TIMEOUT, "a device wait of a feed-forward product gave up");
     return RA_OK;
   });
 }

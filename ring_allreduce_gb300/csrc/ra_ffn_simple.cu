@@ -7,6 +7,7 @@
 // (the gated projections: two sets), columns 16 apart, so that its half warp
 // holds the 128 columns that share a scale.
 #include "ra_ffn.cuh"
+#include "ra_ffn_mma.h"
 
 namespace ra {
 
@@ -182,6 +183,12 @@ template <class D> cudaError_t by_stage(FfnStage stage, const FfnArgs& a, int sm
 }
 
 }  // namespace
+
+__device__ ra_device_error g_ffn_error;
+
+cudaError_t ffn_error_record(ra_device_error** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_ffn_error);
+}
 
 cudaError_t launch_ffn_simple(int dtype, FfnStage stage, const FfnArgs& a, int sms, cudaStream_t st) {
   const cudaError_t e = debug_upload(st);
