@@ -114,11 +114,12 @@ ra_status check_ffn_rows(size_t rows) {
   return RA_OK;
 }
 
-// A matrix operand [rows][columns] of a product; no columns: there is none.
-struct Operand {
+// A matrix of a product, [rows][columns] of `elem` bytes; NULL: there is none.
+struct Matrix {
   const void* p;
-  int64_t rows, columns, stride;
-  bool aligned() const { return (uintptr_t)p % 16 == 0 && (rows <= 1 || stride * 2 % 16 == 0); }
+  int64_t rows, columns, stride;   // in elements
+  int elem;
+  uintptr_t bits() const { return (uintptr_t)p | (rows > 1 ? (uintptr_t)(stride * elem) : 0); }
 };
 
 using Encode = decltype(&cuTensorMapEncodeTiled);
@@ -135,121 +136,124 @@ Encode encoder() {
   return f;
 }
 
-// The map that fetches boxes of 64 columns and `box_rows` rows of an operand, swizzled.
-bool encode(CUtensorMap* map, ra_dtype dtype, const Operand& o, int box_rows) {
+// The map that copies boxes of `box_bytes` (64 or 128, swizzled over as many) of `box_rows` rows.
+bool encode(CUtensorMap* map, ra_dtype dtype, const Matrix& o, int box_bytes, int box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)o.columns, (cuuint64_t)o.rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.stride * 2 : (o.columns * 2 + 15) / 16 * 16)};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, steps[2] = {1, 1};
-  return encoder()(map, dtype == RA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                   const_cast<void*>(o.p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t strides[1] = {(cuuint64_t)(o.rows > 1 ? o.stride * o.elem : (o.columns * o.elem + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / o.elem), (cuuint32_t)box_rows}, steps[2] = {1, 1};
+  const CUtensorMapDataType type = o.elem == 4        ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : o.elem == 1      ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == RA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encoder()(map, type, 2, const_cast<void*>(o.p), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The operands of a stage for rank r: `a[i]` and `b[i]` as MmaArgs has them.
-struct Operands {
-  Operand a[3] = {}, b[2] = {};
-  int as = 1, bs = 1;
-  Operands(FfnStage stage, const FfnArgs& f, int r) {
+// A stage's matrices for rank r, laid out as MmaArgs has them.
+struct Matrices {
+  Matrix in[5] = {};    // operands
+  Matrix out[5] = {};   // rows written, and kept rows read
+  int outs = 0;         // written
+  Matrices(FfnStage stage, const FfnArgs& f, int r) {
     const int64_t width = f.width(r), T = f.rows, D = f.dim;
-    const Operand x{f.x[r], T, D, f.x_stride}, dy{f.grad_out[r], T, D, f.grad_out_stride},
-        hidden{f.hidden[r], T, width, f.hidden_stride[r]};
-    Operand w[3], pre[2];
-    for (int k = 0; k < 3; ++k) w[k] = {f.w[k][r], width, D, f.w_stride[k][r]};
-    for (int k = 0; k < 2; ++k) pre[k] = {f.grad_pre[k][r], T, width, f.grad_pre_stride[k][r]};
+    const int ke = f.keep_bits / 8, ge = f.grad_f32 ? 4 : 2;
+    const Matrix x{f.x[r], T, D, f.x_stride, 2}, dy{f.grad_out[r], T, D, f.grad_out_stride, 2},
+        hidden{f.hidden[r], T, width, f.hidden_stride[r], 2}, product{f.out[r], T, D, f.out_stride, 2};
+    Matrix w[3], pre[2], kept[2];
+    for (int k = 0; k < 3; ++k) w[k] = {f.w[k][r], width, D, f.w_stride[k][r], 2};
+    for (int k = 0; k < 2; ++k) pre[k] = {f.grad_pre[k][r], T, width, f.grad_pre_stride[k][r], 2};
+    for (int k = 0; k < 2; ++k) kept[k] = {f.kept[k][r], T, width, f.kept_stride[k][r], ke};
     switch (stage) {
       case kFfnHidden:
-        a[0] = x;
-        b[0] = w[0];
-        b[1] = w[1];
-        bs = 2;
+        in[0] = x, in[1] = w[0], in[2] = w[1];
+        out[0] = hidden, out[1] = kept[0], out[2] = kept[1];
+        outs = 3;
         break;
       case kFfnOut:
-        a[0] = hidden;
-        b[0] = w[2];
+        in[0] = hidden, in[2] = w[2];
+        out[0] = product;
+        outs = 1;
         break;
       case kFfnGradHidden:
-        a[0] = dy;
-        b[0] = w[2];
+        in[0] = dy, in[1] = w[2];
+        out[0] = pre[0], out[1] = pre[1], out[2] = hidden, out[3] = kept[0], out[4] = kept[1];
+        outs = 3;
         break;
       case kFfnGradX:
-        a[0] = pre[0];
-        a[1] = pre[1];
-        b[0] = w[0];
-        b[1] = w[1];
-        as = bs = 2;
+        in[0] = pre[0], in[1] = pre[1], in[2] = w[0], in[3] = w[1];
+        out[0] = product;
+        outs = 1;
         break;
       default:   // what is not wanted has no operands
-        as = 3;
-        bs = 2;
+        outs = 3;
         for (int k = 0; k < 3; ++k)
           if (f.grad_w[k][r]) {
-            a[k] = k == 2 ? hidden : pre[k];
-            b[k == 2] = k == 2 ? dy : x;
+            in[k] = k == 2 ? hidden : pre[k];
+            in[k == 2 ? 4 : 3] = k == 2 ? dy : x;
+            out[k] = {f.grad_w[k][r], width, D, f.grad_w_stride[k][r], ge};
           }
     }
   }
 };
 
-// Rows of every rank's buffer on 16-byte boundaries.
-bool on_grid(const ra_ffn_ctx* h, void* const* at, const int64_t* strides, int64_t elem, int64_t rows) {
-  uintptr_t bits = 0;
-  for (int r = 0; r < h->ranks; ++r) bits |= (uintptr_t)at[r] | (rows > 1 ? (uintptr_t)(strides[r] * elem) : 0);
-  return bits % 16 == 0;
-}
-
 ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st) {
-  MmaArgs a;
-  bool aligned = true;
-  for (int r = 0; r < h->ranks && aligned; ++r) {
-    const Operands o(stage, f, r);
-    for (int i = 0; i < o.as; ++i) aligned = aligned && o.a[i].aligned();
-    for (int i = 0; i < o.bs; ++i) aligned = aligned && o.b[i].aligned();
+  uintptr_t operands = 0;
+  for (int r = 0; r < h->ranks; ++r) {
+    const Matrices m(stage, f, r);
+    for (const Matrix& o : m.in)
+      if (o.p) operands |= o.bits();
   }
-  if (!aligned) {
+  if (operands % 16) {
     const cudaError_t e = launch_ffn_simple(h->dtype, stage, f, h->sms, st);
     return e == cudaSuccess ? RA_OK : cuda_error(e, "feed-forward launch");
   }
   if (!encoder()) return record_error(RA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-  // rows across the terms of a sum are fetched 64 of them at a time
-  const bool a_mn = stage == kFfnGradW, b_mn = stage == kFfnOut || stage == kFfnGradX || stage == kFfnGradW;
-  for (int r = 0; r < h->ranks; ++r) {
-    const Operands o(stage, f, r);
-    bool ok = true;
-    for (int i = 0; i < o.as; ++i)
-      if (o.a[i].p && f.rows) ok = ok && encode(&a.a[i][r], h->dtype, o.a[i], a_mn ? 64 : 128);
-    for (int i = 0; i < o.bs; ++i)
-      if (o.b[i].p && o.b[i].rows) ok = ok && encode(&a.b[i][r], h->dtype, o.b[i], b_mn ? 64 : 128);
-    if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-  }
-  a.f = f;
-  a.err = h->err;
+  MmaArgs a;
+  a.tokens = f.rows;
   a.segments = stage == kFfnGradX ? 2 : 1;
-  const int64_t gb = f.grad_f32 ? 4 : 2;
-  a.vec = 0;
-  if (f.hidden[0] && on_grid(h, f.hidden, f.hidden_stride, 2, f.rows)) a.vec |= kVecHidden;
-  if (f.keep_bits && on_grid(h, f.kept[0], f.kept_stride[0], f.keep_bits / 8, f.rows) &&
-      on_grid(h, f.kept[1], f.kept_stride[1], f.keep_bits / 8, f.rows))
-    a.vec |= kVecKept;
-  if (f.grad_pre[0][0] && on_grid(h, f.grad_pre[0], f.grad_pre_stride[0], 2, f.rows) &&
-      on_grid(h, f.grad_pre[1], f.grad_pre_stride[1], 2, f.rows))
-    a.vec |= kVecPre;
-  uintptr_t out = f.rows > 1 ? (uintptr_t)f.out_stride * 2 : 0;
-  for (int r = 0; r < h->R; ++r) out |= (uintptr_t)f.out[r];
-  if (out % 16 == 0) a.vec |= kVecOut;
-  bool grads = true;
-  for (int k = 0; k < 3; ++k)
-    if (f.grad_w[k][0]) grads = grads && on_grid(h, f.grad_w[k], f.grad_w_stride[k], gb, h->C);
-  if (grads) a.vec |= kVecGradW;
-  const bool wide = stage == kFfnHidden;
-  const int64_t M = stage == kFfnGradW ? h->C : f.rows, N = wide || stage == kFfnGradHidden ? h->C : h->dim;
+  a.dim = f.dim;
+  a.keep_bits = f.keep_bits;
+  a.act = f.act;
+  a.grad_f32 = f.grad_f32;
+  a.err = h->err;
+  const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
+  const bool wide = stage == kFfnHidden, grads = stage == kFfnGradW;
+  const int64_t M = grads ? h->C : f.rows, N = wide || stage == kFfnGradHidden ? h->C : h->dim;
   a.tiles_m = (int)((M + 255) / 256);
   a.tiles_n = (int)(wide ? (N + 127) / 128 : (N + 255) / 256);
-  a.tiles = (int64_t)a.tiles_m * a.tiles_n * (stage == kFfnGradW ? 3 * h->R : h->R);
-  const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
-  const cudaError_t e = h->dtype == RA_BF16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st)
-                                            : launch_ffn_mma<RA_F16>(as, a, h->sms, st);
-  return e == cudaSuccess ? RA_OK : cuda_error(e, "feed-forward launch");
+  // rows of operands that run along the terms come 128 at a time, rows across them one a term, 64 at a time
+  const auto in_rows = [&](int k) { return grads || (as == kFfnOut && k >= 2) ? 64 : 128; };
+  for (int r0 = 0; r0 < h->R; r0 += kLaunchRanks) {
+    const int ranks = h->R - r0 < kLaunchRanks ? h->R - r0 : kLaunchRanks;
+    for (MmaRows& t : a.rows) t.level = 3;
+    for (int i = 0; i < ranks; ++i) {
+      const int r = r0 + i;
+      const Matrices m(stage, f, r);
+      bool ok = true;
+      a.width[i] = f.width(r);
+      for (int k = 0; k < 2; ++k) a.scales[k][i] = f.scales[k][r];
+      for (int k = 0; k < 5; ++k)
+        if (m.in[k].p && m.in[k].rows && m.in[k].columns) ok = ok && encode(&a.map[k][i], h->dtype, m.in[k], 128, in_rows(k));
+      for (int k = 0; k < 5; ++k) {
+        const Matrix& o = m.out[k];
+        a.rows[k].p[i] = static_cast<char*>(const_cast<void*>(o.p));
+        a.rows[k].stride[i] = o.stride * o.elem;
+        if (!o.p) continue;
+        const uintptr_t bits = o.bits();
+        const int level = bits % 32 == 0 ? 3 : bits % 16 == 0 ? 2 : bits % 8 == 0 ? 1 : 0;
+        if (level < a.rows[k].level) a.rows[k].level = level;
+        if (k < m.outs && level >= 2 && o.rows && o.columns)
+          ok = ok && encode(&a.map[first_rows(as) + k][i], h->dtype, o, 64, 32);
+      }
+      if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    }
+    a.tiles = (int64_t)a.tiles_m * a.tiles_n * (grads ? 3 * ranks : ranks);
+    const cudaError_t e = h->dtype == RA_BF16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st)
+                                              : launch_ffn_mma<RA_F16>(as, a, h->sms, st);
+    if (e != cudaSuccess) return cuda_error(e, "feed-forward launch");
+  }
+  return RA_OK;
 }
 
 ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_dtype grad_dtype, ra_ffn_handle* out) {

@@ -11,15 +11,24 @@
 //
 // Roles in a CTA of 320 threads, one CTA an SM, tiles taken by turns:
 //   warp 8   one thread copies operand tiles by tensor map into a ring of
-//            kStages stages (out of range: zeros), the pair's bytes counted on
+//            stages (out of range: zeros), the pair's bytes counted on
 //            the first CTA's barrier
 //   warp 9   of the first CTA: one thread issues the products, and frees
 //            stages and hands over sums by commits to both CTAs' barriers
-//   warps 0-3, 4-7  epilogue of the tiles whose sums lie in the first and in
-//            the second 256 columns of tensor memory: the products of the next tile
-//            run while one is written out; thread = row
+//   warps 0-7  epilogue: thread = row, the second four warps the second half
+//            of the columns.  Tensor memory holds two tiles' sums, so the products
+//            of the next tile run while one is written out
 // Operands are taken as they lie: rows along the terms (projections, dh) or
 // across them (everything else); nothing is transposed or laid out anew.
+//
+// The products keep the shared memory's path busy (a tile's 64 terms: 16 KB
+// written and 16 KB read an SM in 512 cycles), and whatever the epilogue sends
+// through it costs them its time.  A store to global memory by lanes that each
+// hold a row takes a cycle of it a row and 16 bytes; so the epilogue lays its
+// outputs down in shared memory, 64 bytes of 32 rows at a time, and has them
+// stored by tensor map, which also cuts them off at the last row and column
+// (dh of 4096 x 8192 from 2048 columns: 120 -> 112 us; the projections
+// of 8192 x 16384 from 4096: 1108 -> 1079 us).
 #pragma once
 
 #include "ra_ffn.cuh"
@@ -31,16 +40,22 @@ namespace ra {
 namespace {
 
 constexpr int kBlockM = 128, kBlockN = 128, kBlockK = 64;   // of one CTA's operands
-constexpr int kStages = 6;
 constexpr int kOperandBytes = kBlockM * kBlockK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMmaThreads = 320;
 constexpr int kTileN = 2 * kBlockN;
 constexpr uint32_t kTmemColumns = 2 * kTileN;
-constexpr int kMmaShared = kStages * kStageBytes + 1024;   // and up to 1024 to align
+constexpr int kUnitBytes = 32 * 64;   // 64 bytes of a warp's 32 rows
+
+// dh's epilogue writes three outputs: more room for them, one stage less.
+__host__ __device__ constexpr int stages(int stage) { return stage == kFfnGradHidden ? 5 : 6; }
+__host__ __device__ constexpr int units(int stage) { return stage == kFfnGradHidden ? 4 : 2; }
+__host__ __device__ constexpr int mma_shared(int stage) {
+  return stages(stage) * kStageBytes + 8 * units(stage) * kUnitBytes + 1024;   // and up to 1024 to align
+}
 
 struct MmaShared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[6], empty[6];
   uint64_t sums_full[2], sums_empty[2];
   uint32_t tmem;
   int gave_up;
@@ -64,210 +79,315 @@ template <int Stage> __device__ __forceinline__ bool tile_at(const MmaArgs& a, i
   const int band = u / (8 * a.tiles_n), top = band * 8, high = min(8, a.tiles_m - top);
   const int v = u - band * 8 * a.tiles_n;
   p->m0 = (top + v % high) * 256;
-  constexpr int cols = Stage == kFfnHidden ? kBlockN : kTileN;
-  p->n0 = v / high * cols;
-  const FfnArgs& f = a.f;
-  const int width = f.width(p->r);
+  p->n0 = v / high * (Stage == kFfnHidden ? kBlockN : kTileN);
+  const int width = a.width[p->r];
   if constexpr (Stage == kFfnHidden || Stage == kFfnGradHidden) {
-    p->m = (int)f.rows;
+    p->m = (int)a.tokens;
     p->n = width;
-    p->steps = (f.dim + kBlockK - 1) / kBlockK;
+    p->steps = (a.dim + kBlockK - 1) / kBlockK;
   } else if constexpr (Stage == kFfnOut) {
-    p->m = (int)f.rows;
-    p->n = f.dim;
+    p->m = (int)a.tokens;
+    p->n = a.dim;
     p->half = (width + kBlockK - 1) / kBlockK;
     p->steps = p->half * a.segments;
   } else {
     p->m = width;
-    p->n = f.dim;
-    p->steps = (int)((f.rows + kBlockK - 1) / kBlockK);
-    if (!f.grad_w[p->which][p->r]) return false;
+    p->n = a.dim;
+    p->steps = (int)((a.tokens + kBlockK - 1) / kBlockK);
+    if (!a.rows[p->which].p[p->r]) return false;
   }
   return p->m0 < p->m && p->n0 < p->n;
 }
 
-// 32 columns of a row from `v`, of which `left` exist.  vec: 16-byte stores fit.
-template <class D>
-__device__ __forceinline__ void put_chunk(typename D::T* to, const float* v, int left, bool vec) {
-  constexpr int kVec = D::kVec;
-#pragma unroll
-  for (int q = 0; q < 32 / kVec; ++q) {
-    if (vec && left >= (q + 1) * kVec) {
-      uint4* p = reinterpret_cast<uint4*>(to + q * kVec);
-      if (RA_ACCESS_OK(p, 16u, 2u)) *p = pack<D>(v + q * kVec);
-    } else {
-#pragma unroll
-      for (int j = q * kVec; j < (q + 1) * kVec; ++j)
-        if (j < left) st_g(to + j, narrow<D>(v[j]));
-    }
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 32 bytes of this lane's row, `left` of the rows' bytes still to come.
+__device__ __forceinline__ void get_words(const char* p, uint32_t* w, int left, int level) {
+  if (left >= 32 && level == 3) {
+    if (RA_ACCESS_OK(p, 32u, 1u))
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p)
+                   : "memory");
+    return;
   }
-}
-
-__device__ __forceinline__ void put_codes(int8_t* to, const float* v, float by, int left, bool vec) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    if (vec && left >= (q + 1) * 16) {
-      uint4* p = reinterpret_cast<uint4*>(to + q * 16);
-      const float* x = v + q * 16;
-      if (RA_ACCESS_OK(p, 16u, 2u))
-        *p = make_uint4(codes4(x, by), codes4(x + 4, by), codes4(x + 8, by), codes4(x + 12, by));
+  for (int j = 0; j < 8; j += 2) {
+    if (level && left >= 4 * j + 8) {
+      const uint2 x = ld_g(reinterpret_cast<const uint2*>(p) + j / 2);
+      w[j] = x.x;
+      w[j + 1] = x.y;
     } else {
-#pragma unroll
-      for (int j = q * 16; j < (q + 1) * 16; ++j)
-        if (j < left) st_g(to + j, code_of(v[j], by));
-    }
-  }
-}
-
-__device__ __forceinline__ void get_codes(const int8_t* from, float scale, int left, bool vec, float* v) {
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t w[4] = {};
-    if (vec && left >= (q + 1) * 16) {
-      const uint4 x = ld_plain(reinterpret_cast<const uint4*>(from + q * 16));
-      w[0] = x.x;
-      w[1] = x.y;
-      w[2] = x.z;
-      w[3] = x.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (q * 16 + j < left) w[j / 4] |= (uint32_t)(uint8_t)ld_g(from + q * 16 + j) << (8 * (j % 4));
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[q * 16 + j] = code_value(bias_codes(w[j / 4]), j % 4) * scale;
-  }
-}
-
-template <class D>
-__device__ __forceinline__ void get_chunk(const typename D::T* from, int left, bool vec, float* v) {
-  constexpr int kVec = D::kVec;
-#pragma unroll
-  for (int q = 0; q < 32 / kVec; ++q) {
-    if (vec && left >= (q + 1) * kVec) {
-      unpack<D>(ld_plain(reinterpret_cast<const uint4*>(from + q * kVec)), v + q * kVec);
-    } else {
-#pragma unroll
-      for (int j = q * kVec; j < (q + 1) * kVec; ++j) v[j] = j < left ? widen<D>(ld_g(from + j)) : 0.0f;
-    }
-  }
-}
-
-// A chunk of 32 sums of this thread's row.
-__device__ __forceinline__ void get_sums(uint32_t tmem, float* v) {
-  __syncwarp();   // lanes beyond the last row have left the chunk before early
-  tmem_load32(tmem, reinterpret_cast<uint32_t*>(v));
-}
-
-// One row of a finished tile.  `tmem`: its sums in this warp's lanes.
-template <class D, int Stage, int Act>
-__device__ void write_row(const MmaArgs& a, const Tile& p, uint32_t tmem, int64_t row) {
-  using T = typename D::T;
-  const FfnArgs& f = a.f;
-  const int r = p.r;
-  const bool in = row < p.m;
-  if constexpr (Stage == kFfnHidden) {
-    const int groups = (p.n + kGroup - 1) / kGroup;
-    float by[2] = {};
-    if (f.keep_bits == 8) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float most = 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < kBlockN; c += 32) {
-          float v[32];
-          get_sums(tmem + b * kBlockN + c, v);
-          tmem_wait_loads();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) most = max_nan(most, fabsf(v[j]));
-        }
-        float scale;
-        group_scale(most, &scale, &by[b]);
-        if (in) st_g(f.scales[b][r] + row * groups + p.n0 / kGroup, scale);
+      for (int i = 0; i < 8 && 4 * j + i < left; ++i) {
+        const uint32_t x = (uint32_t)ld_g(reinterpret_cast<const uint8_t*>(p) + 4 * j + i) << (8 * (i % 4));
+        if (i < 4) w[j] |= x;
+        else w[j + 1] |= x;
       }
     }
-    // a row of a vector of heads' worth of columns: 32 at a time
+  }
+}
+
+// The epilogue of a tile in one of eight warps.
+template <int Stage> struct Epilogue {
+  static constexpr int kUnits = units(Stage);
+  const MmaArgs& a;
+  uint32_t staging;        // kUnits units of this warp's, 512-byte aligned
+  uint32_t next;           // the unit that is written next
+  int half, lane;
+  // of the tile
+  uint32_t tmem;           // the warp's lanes of its sums
+  int r;
+  int64_t row0;            // the first lane's row
+  int rows;                // how many of the lanes' exist
+  uint32_t sums_empty;     // where the sums are handed back
+
+  __device__ __forceinline__ int64_t row() const { return row0 + lane; }
+  __device__ __forceinline__ bool in() const { return lane < rows; }
+  // 32 columns of this thread's row
+  __device__ __forceinline__ void sums(int column, float* v) const {
+    __syncwarp();
+    tmem_load32(tmem + column, reinterpret_cast<uint32_t*>(v));
+  }
+  // Every lane's loads from tensor memory have returned.
+  __device__ __forceinline__ void release() const {
+    tensor_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster_relaxed(sums_empty);
+  }
+  // Bytes [16 q, 16 q + 16) of this lane's row of a unit, swizzled as its copy by tensor map expects.
+  __device__ __forceinline__ uint32_t piece(uint32_t unit, int q) const {
+    return staging + unit * kUnitBytes + (uint32_t)lane * 64u + (((uint32_t)q ^ ((uint32_t)lane >> 1 & 3u)) << 4);
+  }
+  // The next unit, free to be written: all but the last kUnits - 1 copies have read theirs.
+  __device__ __forceinline__ uint32_t take() {
+    const uint32_t u = next;
+    next = next + 1 == kUnits ? 0 : next + 1;
+    if (lane == 0) bulk_wait_read<kUnits - 1>();
+    __syncwarp();
+    return u;
+  }
+  __device__ __forceinline__ void fill(uint32_t unit, const uint32_t* w) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) st_shared16(piece(unit, q), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  }
+  // A filled unit to the columns from `column` on of rows `k`, elements of `elem` bytes, `left` columns to come.
+  __device__ __forceinline__ void store(uint32_t unit, int k, int column, int left, int elem) const {
+    const MmaRows& t = a.rows[k];
+    // (a copy is cut off to 16 bytes, not to the element)
+    if (t.level >= 2 && (left * elem >= 64 || left * elem % 16 == 0)) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (left > 0 && rows > 0)
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                           &a.map[first_rows(Stage) + k][r]),
+                       "r"(column), "r"((int)row0), "r"(staging + unit * kUnitBytes)
+                       : "memory");
+        bulk_commit();
+      }
+    } else {   // rows off the 16-byte grid, or that end on none: element by element, side by side
+      __syncwarp();
+      const int columns = min(left, 64 / elem), n = max(columns, 0) * rows;
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) {
+        const int y = i / columns, x = i - y * columns;
+        char* const to = t.p[r] + (row0 + y) * t.stride[r] + (int64_t)(column + x) * elem;
+        const uint32_t b = (uint32_t)(x * elem);
+        const uint32_t from = staging + unit * kUnitBytes + (uint32_t)y * 64u + ((b >> 4 ^ ((uint32_t)y >> 1 & 3u)) << 4) + (b & 15u);
+        uint32_t v;
+        if (elem == 4) {
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+          st_g(reinterpret_cast<uint32_t*>(to), v);
+        } else if (elem == 2) {
+          asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(from) : "memory");
+          st_g(reinterpret_cast<uint16_t*>(to), (uint16_t)v);
+        } else {
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+          st_g(reinterpret_cast<uint8_t*>(to), (uint8_t)v);
+        }
+      }
+      if (lane == 0) bulk_commit();   // of nothing: take() counts one a unit
+      __syncwarp();
+    }
+  }
+  // 32 values of a row, rounded to the block's type
+  template <class D> __device__ __forceinline__ void put(int k, int column, const float* v, int left) {
+    const uint32_t u = take();
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2<D>(v[2 * j], v[2 * j + 1]);
+    fill(u, w);
+    store(u, k, column, left, 2);
+  }
+  __device__ __forceinline__ const char* at(int k, int64_t column, int elem) const {
+    return a.rows[k].p[r] + row() * a.rows[k].stride[r] + column * elem;
+  }
+};
+
+// 64 gated columns of a row.  Kept in 8 bits, the 128 columns that share a scale
+// belong to two warps; each looks all of them through for the largest magnitude.
+template <class D, int Act>
+__device__ __forceinline__ void write_hidden(const MmaArgs& a, const Tile& p, Epilogue<kFfnHidden>& e) {
+  const int r = p.r, first = p.n0 + e.half * 64, gate = e.half * 64, up = kBlockN + gate;
+  if (a.keep_bits == 8) {
+    float m[2] = {}, by[2], scale[2];
 #pragma unroll 1
     for (int c = 0; c < kBlockN; c += 32) {
-      const int col = p.n0 + c, left = p.n - col;
-      if (left <= 0) break;
-      float g[32], u[32], h[32];
-      get_sums(tmem + c, g);
-      get_sums(tmem + kBlockN + c, u);
+      float g[32], u[32];
+      e.sums(c, g);
+      e.sums(kBlockN + c, u);
       tmem_wait_loads();
-      if (!in) continue;
-      if (f.keep_bits == 8) {
-        put_codes((int8_t*)f.kept[0][r] + row * f.kept_stride[0][r] + col, g, by[0], left, a.vec & kVecKept);
-        put_codes((int8_t*)f.kept[1][r] + row * f.kept_stride[1][r] + col, u, by[1], left, a.vec & kVecKept);
-      } else if (f.keep_bits == 16) {
-        put_chunk<D>((T*)f.kept[0][r] + row * f.kept_stride[0][r] + col, g, left, a.vec & kVecKept);
-        put_chunk<D>((T*)f.kept[1][r] + row * f.kept_stride[1][r] + col, u, left, a.vec & kVecKept);
-      }
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        float act, slope;
-        activate<Act, false>(g[j], &act, &slope);
-        h[j] = act * u[j];
+        m[0] = max_nan(m[0], fabsf(g[j]));
+        m[1] = max_nan(m[1], fabsf(u[j]));
       }
-      put_chunk<D>((T*)f.hidden[r] + row * f.hidden_stride[r] + col, h, left, a.vec & kVecHidden);
     }
-  } else if constexpr (Stage == kFfnGradHidden) {
-    const int groups = (p.n + kGroup - 1) / kGroup;
+    group_scale(m[0], &scale[0], &by[0]);
+    group_scale(m[1], &scale[1], &by[1]);
+    if (e.in())
+      st_g(a.scales[e.half][r] + e.row() * ((p.n + kGroup - 1) / kGroup) + p.n0 / kGroup, e.half ? scale[1] : scale[0]);
 #pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
-      const int col = p.n0 + c, left = p.n - col;
-      if (left <= 0) break;
-      float dh[32], g[32], u[32];
-      get_sums(tmem + c, dh);
-      if (in) {
-        if (f.keep_bits == 8) {
-          const int64_t at = row * groups + col / kGroup;
-          get_codes((const int8_t*)f.kept[0][r] + row * f.kept_stride[0][r] + col, ld_g(f.scales[0][r] + at), left,
-                    a.vec & kVecKept, g);
-          get_codes((const int8_t*)f.kept[1][r] + row * f.kept_stride[1][r] + col, ld_g(f.scales[1][r] + at), left,
-                    a.vec & kVecKept, u);
-        } else {
-          get_chunk<D>((const T*)f.kept[0][r] + row * f.kept_stride[0][r] + col, left, a.vec & kVecKept, g);
-          get_chunk<D>((const T*)f.kept[1][r] + row * f.kept_stride[1][r] + col, left, a.vec & kVecKept, u);
-        }
-      }
-      tmem_wait_loads();
-      if (!in) continue;
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t unit = e.take();
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        float act, slope;
-        activate<Act, true>(g[j], &act, &slope);
-        g[j] = dh[j] * u[j] * slope;
-        u[j] = act * u[j];
-        dh[j] = dh[j] * act;
+      for (int c = 0; c < 64; c += 32) {
+        float v[32];
+        e.sums((b ? up : gate) + c, v);
+        tmem_wait_loads();
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = codes4(v + 4 * j, b ? by[1] : by[0]);
+        st_shared16(e.piece(unit, c / 16), w[0], w[1], w[2], w[3]);
+        st_shared16(e.piece(unit, c / 16 + 1), w[4], w[5], w[6], w[7]);
       }
-      put_chunk<D>((T*)f.grad_pre[0][r] + row * f.grad_pre_stride[0][r] + col, g, left, a.vec & kVecPre);
-      put_chunk<D>((T*)f.grad_pre[1][r] + row * f.grad_pre_stride[1][r] + col, dh, left, a.vec & kVecPre);
-      if (f.hidden[r])
-        put_chunk<D>((T*)f.hidden[r] + row * f.hidden_stride[r] + col, u, left, a.vec & kVecHidden);
+      e.store(unit, 1 + b, first, p.n - first, 1);
     }
-  } else {
+  }
 #pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
-      const int col = p.n0 + c, left = p.n - col;
-      if (left <= 0) break;
-      float v[32];
-      get_sums(tmem + c, v);
-      tmem_wait_loads();
-      if (p.steps == 0) {   // a sum of nothing: the columns hold what an earlier tile left
+  for (int c = 0; c < 64; c += 32) {
+    const int col = first + c, left = p.n - col;
+    float g[32], u[32];
+    e.sums(gate + c, g);
+    e.sums(up + c, u);
+    tmem_wait_loads();
+    if (c == 32) e.release();
+    if (a.keep_bits == 16) {
+      e.put<D>(1, col, g, left);
+      e.put<D>(2, col, u, left);
+    }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+    for (int j = 0; j < 32; j += 2) {
+      float2 act, slope;
+      activate<Act, false>(make_float2(g[j], g[j + 1]), &act, &slope);
+      const float2 h = __fmul2_rn(act, make_float2(u[j], u[j + 1]));
+      g[j] = h.x;
+      g[j + 1] = h.y;
+    }
+    e.put<D>(0, col, g, left);
+  }
+}
+
+// 128 columns of a row of dh, from which the gradients of a and b are made, 32
+// at a time.  What was kept of them is fetched a chunk ahead, of the first while the products still run.
+template <class D, int Act, bool Coded, class W>
+__device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& p, Epilogue<kFfnGradHidden>& e,
+                                                  const W& wait, uint64_t* full, uint32_t parity) {
+  const int r = p.r, first = p.n0 + e.half * kBlockN;
+  constexpr int kWords = Coded ? 8 : 16, kElem = Coded ? 1 : 2;
+  float scale[2] = {};
+  uint32_t next[2][kWords] = {};
+  const auto fetch = [&](int col) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < kWords; k += 8)
+        get_words(e.at(3 + b, col, kElem) + 4 * k, next[b] + k, (p.n - col) * kElem - 4 * k, a.rows[3 + b].level);
+  };
+  if (e.in() && first < p.n) {
+    fetch(first);
+    if (Coded) {
+      const int64_t at = e.row() * ((p.n + kGroup - 1) / kGroup) + first / kGroup;
+      scale[0] = ld_g(a.scales[0][r] + at);
+      scale[1] = ld_g(a.scales[1][r] + at);
+    }
+  }
+  if (!wait(full, parity, 4)) return false;
+  tensor_fence_after();
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int col = first + 32 * c, left = p.n - col;
+    uint32_t now[2][kWords];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        now[b][k] = next[b][k];
+        next[b][k] = 0u;
       }
-      if (!in) continue;
-      if constexpr (Stage == kFfnGradW) {
-        const int64_t at = row * f.grad_w_stride[p.which][r] + col;
-        if (f.grad_f32)
-          put_chunk<DF32>((float*)f.grad_w[p.which][r] + at, v, left, a.vec & kVecGradW);
-        else
-          put_chunk<D>((T*)f.grad_w[p.which][r] + at, v, left, a.vec & kVecGradW);
+    float dh[32];
+    e.sums(e.half * kBlockN + 32 * c, dh);
+    if (c < 3 && left > 32 && e.in()) fetch(col + 32);
+    tmem_wait_loads();
+    if (c == 3) e.release();
+    if (left <= 0) continue;
+    uint32_t w[3][16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float2 g, u;
+      if constexpr (Coded) {
+        g = __fmul2_rn(code_pair(bias_codes(now[0][j / 2]), 2 * (j % 2)), both(scale[0]));
+        u = __fmul2_rn(code_pair(bias_codes(now[1][j / 2]), 2 * (j % 2)), both(scale[1]));
       } else {
-        put_chunk<D>((T*)f.out[r] + row * f.out_stride + col, v, left, a.vec & kVecOut);
+        unpack2<D>(now[0][j], reinterpret_cast<float*>(&g));
+        unpack2<D>(now[1][j], reinterpret_cast<float*>(&u));
       }
+      const float2 d = make_float2(dh[2 * j], dh[2 * j + 1]);
+      float2 act, slope;
+      activate<Act, true>(g, &act, &slope);
+      const float2 da = __fmul2_rn(__fmul2_rn(d, u), slope), db = __fmul2_rn(d, act), h = __fmul2_rn(act, u);
+      w[0][j] = pack2<D>(da.x, da.y);
+      w[1][j] = pack2<D>(db.x, db.y);
+      w[2][j] = pack2<D>(h.x, h.y);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (k == 2 && !a.rows[2].p[r]) continue;
+      const uint32_t unit = e.take();
+      e.fill(unit, w[k]);
+      e.store(unit, k, col, left, 2);
+    }
+  }
+  return true;
+}
+
+// 128 columns of a row, rounded.
+template <class D, int Stage>
+__device__ __forceinline__ void write_plain(const MmaArgs& a, const Tile& p, Epilogue<Stage>& e) {
+  const int first = p.n0 + e.half * kBlockN;
+#pragma unroll 1
+  for (int c = 0; c < kBlockN; c += 32) {
+    const int col = first + c, left = p.n - col;
+    float v[32];
+    e.sums(e.half * kBlockN + c, v);
+    tmem_wait_loads();
+    if (c == kBlockN - 32) e.release();
+    if (p.steps == 0) {   // a sum of nothing: the columns hold what an earlier tile left
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+    }
+    if (Stage == kFfnGradW && a.grad_f32) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t unit = e.take();
+        e.fill(unit, reinterpret_cast<const uint32_t*>(v + 16 * q));
+        e.store(unit, p.which, col + 16 * q, left - 16 * q, 4);
+      }
+    } else {
+      e.template put<D>(p.which, col, v, left);
     }
   }
 }
@@ -279,6 +399,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
   // operands whose rows run across the terms: 64 terms of 64 elements a box, two boxes
   constexpr bool kAMn = Stage == kFfnGradW, kBMn = Stage == kFfnOut || Stage == kFfnGradW;
   constexpr uint32_t kDesc = product_desc(std::is_same<D, DBF16>::value, kAMn, kBMn, 2 * kBlockM, kTileN);
+  constexpr int kStages = stages(Stage);
   extern __shared__ uint8_t dynamic[];
   __shared__ MmaShared sh;
   const uint32_t ring = (smem_addr(dynamic) + 1023u) & ~1023u;
@@ -291,7 +412,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.sums_full[b], 1);
-      mbar_init(&sh.sums_empty[b], 8);   // four warps of each CTA
+      mbar_init(&sh.sums_empty[b], 16);   // eight warps of each CTA
     }
     sh.gave_up = 0;
     fence_mbar_init();
@@ -319,23 +440,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
         for (int k = 0; k < p.steps; ++k) {
           ok = wait(&sh.empty[s], (round & 1) ^ 1, 0);
           if (!ok) break;
-          const CUtensorMap *ma, *mb;
-          int at = k * kBlockK;
+          int ia = 0, ib = 1, at = k * kBlockK;
           if constexpr (Stage == kFfnHidden) {
-            ma = &a.a[0][p.r];
-            mb = &a.b[cta][p.r];
+            ib = 1 + (int)cta;
           } else if constexpr (Stage == kFfnOut) {
-            const int seg = k >= p.half;
-            ma = &a.a[seg][p.r];
-            mb = &a.b[seg][p.r];
-            at -= seg * p.half * kBlockK;
-          } else if constexpr (Stage == kFfnGradHidden) {
-            ma = &a.a[0][p.r];
-            mb = &a.b[0][p.r];
-          } else {
-            ma = &a.a[p.which][p.r];
-            mb = &a.b[p.which == 2][p.r];
+            ia = k >= p.half;
+            ib = 2 + ia;
+            at -= ia * p.half * kBlockK;
+          } else if constexpr (Stage == kFfnGradW) {
+            ia = p.which;
+            ib = p.which == 2 ? 4 : 3;
           }
+          const CUtensorMap *const ma = &a.map[ia][p.r], *const mb = &a.map[ib][p.r];
           if (cta == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
           const uint32_t bar = in_cta(smem_addr(&sh.full[s]), 0);
           const uint32_t to = ring + s * kStageBytes;
@@ -399,19 +515,32 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
       }
     }
   } else {
-    const uint32_t b = warp / 4;
+    Epilogue<Stage> e{a, ring + kStages * kStageBytes + (uint32_t)warp * (units(Stage) * kUnitBytes), 0, warp / 4, lane};
     uint32_t it = 0;
-    for (int64_t t = blockIdx.x / 2; t < tiles; t += step) {
+    bool ok = true;
+    for (int64_t t = blockIdx.x / 2; ok && t < tiles; t += step) {
       if (!tile_at<Stage>(a, t, &p)) continue;
-      if ((it++ & 1) != b) continue;
-      if (!wait(&sh.sums_full[b], ((it - 1) >> 1) & 1, 4)) break;
-      tensor_fence_after();
-      const int64_t row = p.m0 + (int)cta * kBlockM + (warp % 4) * 32 + lane;
-      write_row<D, Stage, Act>(a, p, tmem + b * kTileN + ((uint32_t)(warp % 4) * 32u << 16), row);
-      tensor_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(in_cta(smem_addr(&sh.sums_empty[b]), 0));
+      const uint32_t b = it & 1, parity = (it >> 1) & 1;
+      e.tmem = tmem + b * kTileN + ((uint32_t)(warp % 4) * 32u << 16);
+      e.r = p.r;
+      e.row0 = p.m0 + (int)cta * kBlockM + (warp % 4) * 32;
+      e.rows = (int)max((int64_t)0, min((int64_t)32, p.m - e.row0));
+      e.sums_empty = in_cta(smem_addr(&sh.sums_empty[b]), 0);
+      if constexpr (Stage == kFfnGradHidden) {
+        ok = a.keep_bits == 8 ? write_grad_hidden<D, Act, true>(a, p, e, wait, &sh.sums_full[b], parity)
+                              : write_grad_hidden<D, Act, false>(a, p, e, wait, &sh.sums_full[b], parity);
+      } else {
+        ok = wait(&sh.sums_full[b], parity, 4);
+        if (!ok) break;
+        tensor_fence_after();
+        if constexpr (Stage == kFfnHidden)
+          write_hidden<D, Act>(a, p, e);
+        else
+          write_plain<D, Stage>(a, p, e);
+      }
+      ++it;
     }
+    if (lane == 0) bulk_wait_all();   // what is stored by tensor map has been
   }
   __syncwarp();
   __syncthreads();

@@ -9,13 +9,13 @@ namespace ra {
 namespace {
 
 // Each kernel is opted in to its shared memory once a device.
-template <class K> cudaError_t opt_in(K kernel, std::atomic<uint64_t>* done) {
+template <class K> cudaError_t opt_in(K kernel, int shared, std::atomic<uint64_t>* done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaShared);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
   if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
   return e;
 }
@@ -23,10 +23,10 @@ template <class K> cudaError_t opt_in(K kernel, std::atomic<uint64_t>* done) {
 template <class D, int Stage, int Act> cudaError_t launch(const MmaArgs& a, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const auto kernel = ffn_mma_kernel<D, Stage, Act>;
-  const cudaError_t e = opt_in(kernel, &opted);
+  const cudaError_t e = opt_in(kernel, mma_shared(Stage), &opted);
   if (e != cudaSuccess) return e;
   const int64_t pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
-  return launch_after(kernel, dim3((unsigned)(2 * pairs)), dim3(kMmaThreads), kMmaShared, st, 2, a);
+  return launch_after(kernel, dim3((unsigned)(2 * pairs)), dim3(kMmaThreads), mma_shared(Stage), st, 2, a);
 }
 
 }  // namespace
@@ -35,7 +35,7 @@ template <> cudaError_t launch_ffn_mma<RA_INST_DTYPE>(FfnStage stage, const MmaA
   using D = DTypeOf<RA_INST_DTYPE>::type;
   const cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
-  const bool silu = a.f.act == RA_SILU;
+  const bool silu = a.act == RA_SILU;
   switch (stage) {
     case kFfnHidden:
       return silu ? launch<D, kFfnHidden, RA_SILU>(a, sms, st) : launch<D, kFfnHidden, RA_GELU>(a, sms, st);

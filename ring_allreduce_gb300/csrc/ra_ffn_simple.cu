@@ -124,9 +124,9 @@ __global__ void __launch_bounds__(kThreads) ffn_simple_kernel(const __grid_const
         const float v = acc[0][i][j];
         if constexpr (Stage == kFfnHidden) {
           const float u = acc[1 % (kDual ? 2 : 1)][i][j];
-          float act, slope;
-          activate<Act, false>(v, &act, &slope);
-          st_g((T*)a.hidden[r] + row * a.hidden_stride[r] + col, narrow<D>(act * u));
+          float2 act, slope;
+          activate<Act, false>(both(v), &act, &slope);
+          st_g((T*)a.hidden[r] + row * a.hidden_stride[r] + col, narrow<D>(act.x * u));
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const int64_t at = row * a.kept_stride[b][r] + col;
@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(kThreads) ffn_simple_kernel(const __grid_const
             else
               kept[b] = widen<D>(ld_g((const T*)a.kept[b][r] + at));
           }
-          float act, slope;
-          activate<Act, true>(kept[0], &act, &slope);
-          st_g((T*)a.grad_pre[0][r] + row * a.grad_pre_stride[0][r] + col, narrow<D>(v * kept[1] * slope));
-          st_g((T*)a.grad_pre[1][r] + row * a.grad_pre_stride[1][r] + col, narrow<D>(v * act));
-          if (a.hidden[r]) st_g((T*)a.hidden[r] + row * a.hidden_stride[r] + col, narrow<D>(act * kept[1]));
+          float2 act, slope;
+          activate<Act, true>(both(kept[0]), &act, &slope);
+          st_g((T*)a.grad_pre[0][r] + row * a.grad_pre_stride[0][r] + col, narrow<D>(v * kept[1] * slope.x));
+          st_g((T*)a.grad_pre[1][r] + row * a.grad_pre_stride[1][r] + col, narrow<D>(v * act.x));
+          if (a.hidden[r]) st_g((T*)a.hidden[r] + row * a.hidden_stride[r] + col, narrow<D>(act.x * kept[1]));
         } else if constexpr (Stage == kFfnGradW) {
           const int64_t at = row * a.grad_w_stride[which][r] + col;
           if (a.grad_f32)
