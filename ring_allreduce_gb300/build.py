@@ -76,7 +76,7 @@ KERNEL_SOURCES = {
     "ll": ["ra_ll.cu", "ra_ll.h", "ra_device.cuh", "ra_internal.h"],
     "norm": ["ra_norm.cu", "ra_norm.cuh", "ra_norm_inst.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
     "vocab": ["ra_vocab.cu", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
-    "ffn": ["ra_ffn_mma_inst.cu", "ra_ffn_mma.cuh", "ra_ffn_mma.h", "ra_tensor.cuh", "ra_ffn_simple.cu", "ra_ffn.cuh",
+    "ffn": ["ra_ffn_mma_inst.cu", "ra_ffn_few.cuh", "ra_ffn_mma.cuh", "ra_ffn_mma.h", "ra_tensor.cuh", "ra_ffn_simple.cu", "ra_ffn.cuh",
             "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
     "ckpt": ["ra_ckpt.cu", "ra_ffn.cuh", "ra_ffn.h", "ra_ops.cuh", "ra_ops.h", "ra_device.cuh", "ra_internal.h"],
 }

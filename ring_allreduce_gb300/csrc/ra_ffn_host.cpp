@@ -197,6 +197,26 @@ struct Matrices {
   }
 };
 
+// Which kernel a product runs on.
+struct Plan {
+  bool few;
+  int nt, split;
+};
+
+#ifdef RA_FFN_PROBE
+int g_probe[3] = {-1, 0, 0};
+}
+extern "C" void ra_ffn_probe(int few, int nt, int split) { g_probe[0] = few, g_probe[1] = nt, g_probe[2] = split; }
+namespace {
+#endif
+
+Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens) {
+#ifdef RA_FFN_PROBE
+  if (g_probe[0] >= 0) return {g_probe[0] && stage != kFfnGradW, g_probe[1], g_probe[2]};
+#endif
+  return {false, 0, 0};
+}
+
 ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st) {
   uintptr_t operands = 0;
   for (int r = 0; r < h->ranks; ++r) {
@@ -220,37 +240,54 @@ ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st
   const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
   const bool wide = stage == kFfnHidden, grads = stage == kFfnGradW;
   const int64_t M = grads ? h->C : f.rows, N = wide || stage == kFfnGradHidden ? h->C : h->dim;
-  a.tiles_m = (int)((M + 255) / 256);
-  a.tiles_n = (int)(wide ? (N + 127) / 128 : (N + 255) / 256);
+  const Plan plan = plan_of(h, stage, f.rows);
+  a.nt = plan.nt;
+  a.split = plan.split;
+  a.early = stage == kFfnOut || stage == kFfnGradX;
+  if (plan.few) {
+    a.tiles_m = (int)((N + 127) / 128);
+    a.tiles_n = (int)((f.rows + plan.nt - 1) / plan.nt);
+  } else {
+    a.tiles_m = (int)((M + 255) / 256);
+    a.tiles_n = (int)(wide ? (N + 127) / 128 : (N + 255) / 256);
+  }
   // rows of operands that run along the terms come 128 at a time, rows across them one a term, 64 at a time
-  const auto in_rows = [&](int k) { return grads || (as == kFfnOut && k >= 2) ? 64 : 128; };
+  // (for few tokens, theirs as many as a tile has)
+  const auto in_rows = [&](int k) {
+    const bool tokens = as == kFfnOut ? k < 2 : k == 0;
+    return plan.few && tokens ? plan.nt : grads || (as == kFfnOut && k >= 2) ? 64 : 128;
+  };
   for (int r0 = 0; r0 < h->R; r0 += kLaunchRanks) {
     const int ranks = h->R - r0 < kLaunchRanks ? h->R - r0 : kLaunchRanks;
-    for (MmaRows& t : a.rows) t.level = 3;
+    for (int& level : a.level) level = 3;
     for (int i = 0; i < ranks; ++i) {
       const int r = r0 + i;
       const Matrices m(stage, f, r);
       bool ok = true;
-      a.width[i] = f.width(r);
-      for (int k = 0; k < 2; ++k) a.scales[k][i] = f.scales[k][r];
+      MmaRank& to = a.rank[i];
+      to.width = f.width(r);
+      for (int k = 0; k < 2; ++k) to.scales[k] = f.scales[k][r];
       for (int k = 0; k < 5; ++k)
-        if (m.in[k].p && m.in[k].rows && m.in[k].columns) ok = ok && encode(&a.map[k][i], h->dtype, m.in[k], 128, in_rows(k));
+        if (m.in[k].p && m.in[k].rows && m.in[k].columns) ok = ok && encode(&to.map[k], h->dtype, m.in[k], 128, in_rows(k));
       for (int k = 0; k < 5; ++k) {
         const Matrix& o = m.out[k];
-        a.rows[k].p[i] = static_cast<char*>(const_cast<void*>(o.p));
-        a.rows[k].stride[i] = o.stride * o.elem;
+        to.rows[k] = static_cast<char*>(const_cast<void*>(o.p));
+        to.stride[k] = o.stride * o.elem;
         if (!o.p) continue;
         const uintptr_t bits = o.bits();
         const int level = bits % 32 == 0 ? 3 : bits % 16 == 0 ? 2 : bits % 8 == 0 ? 1 : 0;
-        if (level < a.rows[k].level) a.rows[k].level = level;
-        if (k < m.outs && level >= 2 && o.rows && o.columns)
-          ok = ok && encode(&a.map[first_rows(as) + k][i], h->dtype, o, 64, 32);
+        if (level < a.level[k]) a.level[k] = level;
+        if (!plan.few && k < m.outs && level >= 2 && o.rows && o.columns)
+          ok = ok && encode(&to.map[first_rows(as) + k], h->dtype, o, 64, 32);
       }
       if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     }
     a.tiles = (int64_t)a.tiles_m * a.tiles_n * (grads ? 3 * ranks : ranks);
-    const cudaError_t e = h->dtype == RA_BF16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st)
-                                              : launch_ffn_mma<RA_F16>(as, a, h->sms, st);
+    a.ring = a.tiles * (plan.few ? plan.split : 0) <= h->sms ? kFewRingAlone : kFewRing;
+    const bool bf16 = h->dtype == RA_BF16;
+    const cudaError_t e = plan.few ? (bf16 ? launch_ffn_few<RA_BF16>(as, a, st) : launch_ffn_few<RA_F16>(as, a, st))
+                                   : (bf16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st)
+                                           : launch_ffn_mma<RA_F16>(as, a, h->sms, st));
     if (e != cudaSuccess) return cuda_error(e, "feed-forward launch");
   }
   return RA_OK;

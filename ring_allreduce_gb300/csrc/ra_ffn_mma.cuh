@@ -80,7 +80,7 @@ template <int Stage> __device__ __forceinline__ bool tile_at(const MmaArgs& a, i
   const int v = u - band * 8 * a.tiles_n;
   p->m0 = (top + v % high) * 256;
   p->n0 = v / high * (Stage == kFfnHidden ? kBlockN : kTileN);
-  const int width = a.width[p->r];
+  const int width = a.rank[p->r].width;
   if constexpr (Stage == kFfnHidden || Stage == kFfnGradHidden) {
     p->m = (int)a.tokens;
     p->n = width;
@@ -94,9 +94,15 @@ template <int Stage> __device__ __forceinline__ bool tile_at(const MmaArgs& a, i
     p->m = width;
     p->n = a.dim;
     p->steps = (int)((a.tokens + kBlockK - 1) / kBlockK);
-    if (!a.rows[p->which].p[p->r]) return false;
+    if (!a.rank[p->r].rows[p->which]) return false;
   }
   return p->m0 < p->m && p->n0 < p->n;
+}
+
+// The maps of a tile's operands, as bits.
+template <int Stage> __device__ __forceinline__ int operand_maps(const MmaArgs& a, const Tile& p) {
+  if (Stage == kFfnGradW) return 1 << p.which | (p.which == 2 ? 16 : 8);
+  return Stage == kFfnHidden ? 7 : Stage == kFfnGradHidden ? 3 : a.segments == 2 ? 15 : 5;
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -175,15 +181,15 @@ template <int Stage> struct Epilogue {
   }
   // A filled unit to the columns from `column` on of rows `k`, elements of `elem` bytes, `left` columns to come.
   __device__ __forceinline__ void store(uint32_t unit, int k, int column, int left, int elem) const {
-    const MmaRows& t = a.rows[k];
+    const MmaRank& t = a.rank[r];
     // (a copy is cut off to 16 bytes, not to the element)
-    if (t.level >= 2 && (left * elem >= 64 || left * elem % 16 == 0)) {
+    if (a.level[k] >= 2 && (left * elem >= 64 || left * elem % 16 == 0)) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         if (left > 0 && rows > 0)
           asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                           &a.map[first_rows(Stage) + k][r]),
+                           &t.map[first_rows(Stage) + k]),
                        "r"(column), "r"((int)row0), "r"(staging + unit * kUnitBytes)
                        : "memory");
         bulk_commit();
@@ -194,7 +200,7 @@ template <int Stage> struct Epilogue {
 #pragma unroll 1
       for (int i = lane; i < n; i += 32) {
         const int y = i / columns, x = i - y * columns;
-        char* const to = t.p[r] + (row0 + y) * t.stride[r] + (int64_t)(column + x) * elem;
+        char* const to = t.rows[k] + (row0 + y) * t.stride[k] + (int64_t)(column + x) * elem;
         const uint32_t b = (uint32_t)(x * elem);
         const uint32_t from = staging + unit * kUnitBytes + (uint32_t)y * 64u + ((b >> 4 ^ ((uint32_t)y >> 1 & 3u)) << 4) + (b & 15u);
         uint32_t v;
@@ -223,7 +229,7 @@ template <int Stage> struct Epilogue {
     store(u, k, column, left, 2);
   }
   __device__ __forceinline__ const char* at(int k, int64_t column, int elem) const {
-    return a.rows[k].p[r] + row() * a.rows[k].stride[r] + column * elem;
+    return a.rank[r].rows[k] + row() * a.rank[r].stride[k] + column * elem;
   }
 };
 
@@ -249,7 +255,7 @@ __device__ __forceinline__ void write_hidden(const MmaArgs& a, const Tile& p, Ep
     group_scale(m[0], &scale[0], &by[0]);
     group_scale(m[1], &scale[1], &by[1]);
     if (e.in())
-      st_g(a.scales[e.half][r] + e.row() * ((p.n + kGroup - 1) / kGroup) + p.n0 / kGroup, e.half ? scale[1] : scale[0]);
+      st_g(a.rank[r].scales[e.half] + e.row() * ((p.n + kGroup - 1) / kGroup) + p.n0 / kGroup, e.half ? scale[1] : scale[0]);
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
       const uint32_t unit = e.take();
@@ -305,14 +311,14 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int k = 0; k < kWords; k += 8)
-        get_words(e.at(3 + b, col, kElem) + 4 * k, next[b] + k, (p.n - col) * kElem - 4 * k, a.rows[3 + b].level);
+        get_words(e.at(3 + b, col, kElem) + 4 * k, next[b] + k, (p.n - col) * kElem - 4 * k, a.level[3 + b]);
   };
   if (e.in() && first < p.n) {
     fetch(first);
     if (Coded) {
       const int64_t at = e.row() * ((p.n + kGroup - 1) / kGroup) + first / kGroup;
-      scale[0] = ld_g(a.scales[0][r] + at);
-      scale[1] = ld_g(a.scales[1][r] + at);
+      scale[0] = ld_g(a.rank[r].scales[0] + at);
+      scale[1] = ld_g(a.rank[r].scales[1] + at);
     }
   }
   if (!wait(full, parity, 4)) return false;
@@ -355,7 +361,7 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      if (k == 2 && !a.rows[2].p[r]) continue;
+      if (k == 2 && !a.rank[r].rows[2]) continue;
       const uint32_t unit = e.take();
       e.fill(unit, w[k]);
       e.store(unit, k, col, left, 2);
@@ -417,17 +423,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
     sh.gave_up = 0;
     fence_mbar_init();
   }
-  after_predecessor();
+  // (one CTA an SM, by its shared memory: the columns are free, and nothing is waited for)
   if (warp == 9) tmem_alloc<2>(&sh.tmem, kTmemColumns);
+  Tile p;
+  if (warp == 8 && lane < 8 && blockIdx.x / 2 < a.tiles && tile_at<Stage>(a, blockIdx.x / 2, &p) && p.steps > 0 &&
+      operand_maps<Stage>(a, p) >> lane & 1)
+    prefetch_map(&a.rank[p.r].map[lane]);
   tensor_fence_before();
   __syncthreads();
   cluster_arrive();
   cluster_wait();
   tensor_fence_after();
   const uint32_t tmem = sh.tmem;
+  after_predecessor();   // what came before ran on beside all this
   const Waits wait{&sh.gave_up, a.err, Stage};
   const int64_t tiles = a.tiles, step = gridDim.x / 2;
-  Tile p;
 
   if (warp == 8) {
     if (lane == 0) {
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
             ia = p.which;
             ib = p.which == 2 ? 4 : 3;
           }
-          const CUtensorMap *const ma = &a.map[ia][p.r], *const mb = &a.map[ib][p.r];
+          const CUtensorMap *const ma = &a.rank[p.r].map[ia], *const mb = &a.rank[p.r].map[ib];
           if (cta == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kStageBytes);
           const uint32_t bar = in_cta(smem_addr(&sh.full[s]), 0);
           const uint32_t to = ring + s * kStageBytes;

@@ -11,12 +11,12 @@ namespace ra {
 // One launch's ranks: with more, maps and addresses outgrow a kernel's arguments.
 constexpr int kLaunchRanks = 16;
 
-// Buffers of a launch by stage.  Operands, in MmaArgs::map alone (x and grad_out the same for all ranks, or not):
+// Buffers of a launch by stage.  Operands, by their maps alone (x and grad_out the same for all ranks, or not):
 //   hidden       0 x, 1 gate, 2 up
 //   out, grad_x  0, 1 hidden, or grad_gate and grad_up; 2, 3 their weights
 //   grad_hidden  0 grad_out, 1 down
 //   grad_w       0 grad_gate, 1 grad_up, 2 hidden; 3 x, 4 grad_out
-// Rows written (and kept rows read), in MmaArgs::rows, and their maps from first_rows(stage) on:
+// Rows written (and kept rows read), and their maps from first_rows(stage) on:
 //   hidden       0 hidden, 1 gate, 2 up
 //   out, grad_x  0 out
 //   grad_hidden  0 grad_gate, 1 grad_up, 2 hidden; 3 gate, 4 up
@@ -25,29 +25,42 @@ __host__ __device__ constexpr int first_rows(int stage) {
   return stage == kFfnHidden ? 3 : stage == kFfnGradHidden ? 2 : stage == kFfnGradW ? 5 : 4;
 }
 
-struct MmaRows {
-  char* p[kLaunchRanks];         // NULL: absent
-  int64_t stride[kLaunchRanks];  // bytes
-  int level;                     // every rank's rows on multiples of: 3, 32 bytes; 2, 16; 1, 8; 0, less
+// What a launch knows of a rank, in one place: a CTA reads one rank's alone.
+struct MmaRank {
+  CUtensorMap map[8];
+  char* rows[5];         // NULL: absent
+  int64_t stride[5];     // bytes
+  float* scales[2];
+  int width;
 };
 
 struct MmaArgs {
-  CUtensorMap map[8][kLaunchRanks];
-  MmaRows rows[5];
-  float* scales[2][kLaunchRanks];
-  int width[kLaunchRanks];
   int64_t tokens;
   int64_t tiles;          // of all jobs
-  int tiles_m, tiles_n;   // of one
+  int tiles_m, tiles_n;   // of one; for few tokens: of the weights' rows, of the tokens
   int segments;           // products that are summed (grad_x: two)
   int dim, keep_bits;
   int act;                // ra_activation
   int grad_f32;
+  int level[5];           // rows of every rank on multiples of: 3, 32 bytes; 2, 16; 1, 8; 0, less
+  // for few tokens alone
+  int nt;                 // tokens of a tile, a multiple of 16, at most 128
+  int split;              // CTAs that share the terms of a tile's sums: 1, 2, 4 or 8
+  int early;              // the stream's kernel before this one is the call's own
+  int ring;               // bytes of the operands' ring
   ra_device_error* err;   // where a wait that gives up says so
+  MmaRank rank[kLaunchRanks];
 };
 
 // Dtype: RA_BF16 or RA_F16.  kFfnGradX runs as kFfnOut with two segments.
 template <int Dtype> cudaError_t launch_ffn_mma(FfnStage stage, const MmaArgs& a, int sms, cudaStream_t st);
+// All but kFfnGradW, for few tokens; the operands' maps of the tokens have boxes of a.nt rows.
+template <int Dtype> cudaError_t launch_ffn_few(FfnStage stage, const MmaArgs& a, cudaStream_t st);
+// Rings for few tokens: for one CTA an SM, or two.
+constexpr int kFewRing = 104 * 1024, kFewRingAlone = 208 * 1024;
+constexpr int kFewABytes = 128 * 64 * 2, kFewMostStages = 12;
+__host__ __device__ constexpr int few_sums(int stage) { return stage == kFfnHidden ? 2 : 1; }   // accumulators
+__host__ __device__ constexpr int few_stage_bytes(int stage, int nt) { return few_sums(stage) * kFewABytes + nt * 128; }
 // The current device's record of waits that gave up (device memory).
 cudaError_t ffn_error_record(ra_device_error** at);
 
