@@ -197,24 +197,55 @@ struct Matrices {
   }
 };
 
-// Which kernel a product runs on.
+// Which kernel a product runs on: pairs of CTAs with tiles of 256 x 256, or
+// CTAs with 128 of the weights' rows against `nt` tokens, `split` to a tile's sums.
 struct Plan {
   bool few;
   int nt, split;
 };
 
-#ifdef RA_FFN_PROBE
-int g_probe[3] = {-1, 0, 0};
-}
-extern "C" void ra_ffn_probe(int few, int nt, int split) { g_probe[0] = few, g_probe[1] = nt, g_probe[2] = split; }
-namespace {
-#endif
-
-Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens) {
-#ifdef RA_FFN_PROBE
-  if (g_probe[0] >= 0) return {g_probe[0] && stage != kFfnGradW, g_probe[1], g_probe[2]};
-#endif
-  return {false, 0, 0};
+// The plan with the shortest estimate, in microseconds.  The estimates' form is
+// what bounds either kernel -- steps of 64 terms, one after another, in as
+// many rounds as there are tiles for the SMs; the bytes of an SM's steps; a turn
+// of the ring, whose copies take some 1.8 us; the weights' bytes -- and their
+// constants were fitted to 44 shapes (1 to 1200 tokens, 64 to 8192 by 64 to
+// 28000 columns, 1 to 8 ranks) times five products, every plan of each measured.
+// On these the plan chosen takes 5 % longer than the fastest on average, and
+// the large tiles alone would take 42 %.  (The projections of 37 tokens, 4096 x
+// 16384 in 8 ranks: 54 us large, 46 few; of 777, 1544 x 5005 in 3: 26 and 48.)
+Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens, int keep_bits) {
+  if (stage == kFfnGradW) return {false, 0, 0};   // sums over the tokens: nothing to split
+  const bool dual = stage == kFfnHidden, back = stage == kFfnGradHidden;
+  const int64_t N = dual || back ? h->C : h->dim, K = dual || back ? h->dim : h->C;
+  const auto up = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+  const double steps = (double)up(K, 64) * (stage == kFfnGradX ? 2 : 1);
+  const double memory = 2.0 * h->inner * h->dim * (dual || stage == kFfnGradX ? 2 : 1) / 6.6e6;
+  const double waves = (double)up(up(tokens, 256) * up(N, dual ? 128 : 256) * h->R, h->sms / 2);
+  Plan best{false, 0, 0};
+  double least = 4.4 + std::max(waves * steps * 0.277, memory) + 1.8 * (waves - 1) +
+                 (back ? 7.1 : !dual ? 1.1 : keep_bits == 8 ? 4.5 : 1.7);
+  const double token = back ? 0.15 : !dual ? 0.07 : keep_bits == 8 ? 0.21 : 0.025;   // a token's outputs
+  for (const int most : {16, 32, 64, 96, 128}) {
+    const int nt = (int)std::min<int64_t>(most, up(tokens, 16) * 16);
+    for (int split = 1; split <= 8 && (split == 1 || nt <= 96); split *= 2) {
+      const double ctas = (double)(up(N, 128) * up(tokens, nt) * h->R * split);
+      const double rounds = std::ceil(ctas / (2 * h->sms)), on_sm = ctas > h->sms ? 2 : 1;
+      const int stage_bytes = few_stage_bytes(stage, nt);
+      const int ring = std::min((on_sm > 1 ? kFewRing : kFewRingAlone) / stage_bytes, kFewMostStages);
+      const double step = std::max(stage_bytes / 1024.0 * on_sm * 0.0117, 1.76 / ring);
+      const int live = (int)std::min<int64_t>(nt, tokens);
+      const double estimate =
+          1.25 + std::max(rounds * steps / split * step, memory) +
+          rounds * (3.3 + (split > 1 ? 0.33 + 0.07 * live + 0.144 * split : 0.0) + 8.0 * up(up(live, split), 8) * token +
+                    (dual && keep_bits == 8 ? 2.0 : 0.0));
+      if (estimate < least) {
+        least = estimate;
+        best = {true, nt, split};
+      }
+    }
+    if (nt < most) break;
+  }
+  return best;
 }
 
 ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st) {
@@ -240,10 +271,11 @@ ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st
   const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
   const bool wide = stage == kFfnHidden, grads = stage == kFfnGradW;
   const int64_t M = grads ? h->C : f.rows, N = wide || stage == kFfnGradHidden ? h->C : h->dim;
-  const Plan plan = plan_of(h, stage, f.rows);
+  const Plan plan = plan_of(h, stage, f.rows, f.keep_bits);
   a.nt = plan.nt;
   a.split = plan.split;
   a.early = stage == kFfnOut || stage == kFfnGradX;
+  a.late = grads && f.out[0];
   if (plan.few) {
     a.tiles_m = (int)((N + 127) / 128);
     a.tiles_n = (int)((f.rows + plan.nt - 1) / plan.nt);

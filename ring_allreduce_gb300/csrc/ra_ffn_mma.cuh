@@ -196,10 +196,11 @@ template <int Stage> struct Epilogue {
       }
     } else {   // rows off the 16-byte grid, or that end on none: element by element, side by side
       __syncwarp();
-      const int columns = min(left, 64 / elem), n = max(columns, 0) * rows;
-#pragma unroll 1
+      const int columns = max(min(left, 64 / elem), 1), n = left > 0 ? columns * rows : 0;
+      const int down = 32 / columns, across = 32 - down * columns;   // 32 elements on
+      int y = lane / columns, x = lane - y * columns;
+#pragma unroll 2
       for (int i = lane; i < n; i += 32) {
-        const int y = i / columns, x = i - y * columns;
         char* const to = t.rows[k] + (row0 + y) * t.stride[k] + (int64_t)(column + x) * elem;
         const uint32_t b = (uint32_t)(x * elem);
         const uint32_t from = staging + unit * kUnitBytes + (uint32_t)y * 64u + ((b >> 4 ^ ((uint32_t)y >> 1 & 3u)) << 4) + (b & 15u);
@@ -213,6 +214,12 @@ template <int Stage> struct Epilogue {
         } else {
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
           st_g(reinterpret_cast<uint8_t*>(to), (uint8_t)v);
+        }
+        x += across;
+        y += down;
+        if (x >= columns) {
+          x -= columns;
+          ++y;
         }
       }
       if (lane == 0) bulk_commit();   // of nothing: take() counts one a unit
@@ -435,7 +442,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
   cluster_wait();
   tensor_fence_after();
   const uint32_t tmem = sh.tmem;
-  after_predecessor();   // what came before ran on beside all this
+  // what came before ran on beside all this.  Late: the kernel before this one is
+  // the call's own and gives it nothing; what it takes was whole when that one began
+  if (!a.late) after_predecessor();
   const Waits wait{&sh.gave_up, a.err, Stage};
   const int64_t tiles = a.tiles, step = gridDim.x / 2;
 
@@ -559,6 +568,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
   cluster_arrive();
   cluster_wait();
   if (warp == 9) tmem_free<2>(tmem, kTmemColumns);
+  if (a.late) after_predecessor();   // who waits for this kernel waits for that one too
 }
 
 }  // namespace ra
