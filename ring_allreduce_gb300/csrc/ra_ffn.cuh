@@ -74,14 +74,21 @@ __device__ __forceinline__ void group_scale(float most, float* scale, float* by)
 
 // v * by to the nearest whole number: adding 1.5 * 2^23 leaves it, to even, in
 // the low bits (|v * by| < 128).  0 * infinity, NaN, leaves whatever: the scale is NaN then.
-__device__ __forceinline__ uint32_t code_bits(float v, float by) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(v, by), 12582912.0f)) & 0xFFu;
+// (Products one by one: of two at a time the compiler makes one operation with
+// the sums, and a product that is not rounded before goes the other way at a half.)
+__device__ __forceinline__ float2 code_sum(float2 v, float by) {
+  return __fadd2_rn(make_float2(__fmul_rn(v.x, by), __fmul_rn(v.y, by)), both(12582912.0f));
 }
-__device__ __forceinline__ int8_t code_of(float v, float by) { return (int8_t)code_bits(v, by); }
-
+__device__ __forceinline__ int8_t code_of(float v, float by) {
+  return (int8_t)(__float_as_uint(__fadd_rn(__fmul_rn(v, by), 12582912.0f)) & 0xFFu);
+}
+// Four of them as a word.
+__device__ __forceinline__ uint32_t codes4(float2 x, float2 y) {
+  return __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                     __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
+}
 __device__ __forceinline__ uint32_t codes4(const float* v, float by) {
-  return __byte_perm(__byte_perm(code_bits(v[0], by), code_bits(v[1], by), 0x0040),
-                     __byte_perm(code_bits(v[2], by), code_bits(v[3], by), 0x0040), 0x5410);
+  return codes4(code_sum(make_float2(v[0], v[1]), by), code_sum(make_float2(v[2], v[3]), by));
 }
 
 // Code k of four in a word, as a number: the biased byte as the low bits of 2^23 + ...

@@ -64,7 +64,16 @@ struct CkptArgs {
   void* normed;         // may be NULL
   int64_t rows, stride, codes_stride, normed_stride;
   int dim;
-  int param_f32;        // else the weight has the normalised rows' type
+  uint32_t by;          // n / groups = (mulhi(n, by) + n) >> shift for n below 2^31
+  int shift;
+  // Groups of a row, and by and shift for them.
+  int set_groups() {
+    const int groups = (dim + kGroup - 1) / kGroup;
+    shift = 0;
+    while (((int64_t)1 << shift) < groups) ++shift;
+    by = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - (uint64_t)groups)) / (uint64_t)groups + 1);
+    return groups;
+  }
 };
 // wide: rows of every buffer start on 16-byte boundaries (codes: 8) and hold whole groups of 8 columns
 cudaError_t launch_ckpt_store(int dtype, bool wide, const CkptArgs& a, int sms, cudaStream_t st);

@@ -275,7 +275,6 @@ ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st
   a.nt = plan.nt;
   a.split = plan.split;
   a.early = stage == kFfnOut || stage == kFfnGradX;
-  a.late = grads && f.out[0];
   if (plan.few) {
     a.tiles_m = (int)((N + 127) / 128);
     a.tiles_n = (int)((f.rows + plan.nt - 1) / plan.nt);
@@ -496,6 +495,7 @@ ra_status ckpt_store(ra_ckpt_handle h, const ra_ckpt_store_args* g, cudaStream_t
   a.stride = (int64_t)stride;
   a.codes_stride = (int64_t)codes_stride;
   a.dim = h->dim;
+  a.set_groups();
   const bool wide = dim % 8 == 0 && rows_wide(g->values, stride * b, g->rows, 16) &&
                     rows_wide(g->codes, codes_stride, g->rows, 8);
   const cudaError_t e = launch_ckpt_store(h->dtype, wide, a, h->sms, st);
@@ -540,7 +540,7 @@ ra_status ckpt_load(ra_ckpt_handle h, const ra_ckpt_load_args* g, cudaStream_t s
   a.codes_stride = (int64_t)codes_stride;
   a.normed_stride = (int64_t)normed_stride;
   a.dim = h->dim;
-  a.param_f32 = h->param_dtype == RA_F32;
+  a.set_groups();
   const cudaError_t e = launch_ckpt_load(h->dtype, h->normed_dtype, h->param_dtype, wide, a, h->sms, st);
   return e == cudaSuccess ? RA_OK : cuda_error(e, "checkpoint load launch");
 }

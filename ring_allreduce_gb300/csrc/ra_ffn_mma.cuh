@@ -442,9 +442,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
   cluster_wait();
   tensor_fence_after();
   const uint32_t tmem = sh.tmem;
-  // what came before ran on beside all this.  Late: the kernel before this one is
-  // the call's own and gives it nothing; what it takes was whole when that one began
-  if (!a.late) after_predecessor();
+  after_predecessor();   // what came before ran on beside all this
   const Waits wait{&sh.gave_up, a.err, Stage};
   const int64_t tiles = a.tiles, step = gridDim.x / 2;
 
@@ -568,7 +566,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
   cluster_arrive();
   cluster_wait();
   if (warp == 9) tmem_free<2>(tmem, kTmemColumns);
-  if (a.late) after_predecessor();   // who waits for this kernel waits for that one too
 }
 
 }  // namespace ra

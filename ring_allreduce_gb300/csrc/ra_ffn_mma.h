@@ -43,7 +43,6 @@ struct MmaArgs {
   int act;                // ra_activation
   int grad_f32;
   int level[5];           // rows of every rank on multiples of: 3, 32 bytes; 2, 16; 1, 8; 0, less
-  int late;               // grad_w: runs beside the rest of the kernel before it, the call's grad_x
   // for few tokens alone
   int nt;                 // tokens of a tile, a multiple of 16, at most 128
   int split;              // CTAs that share the terms of a tile's sums: 1, 2, 4 or 8
