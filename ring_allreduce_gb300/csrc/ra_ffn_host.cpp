@@ -3,6 +3,8 @@
 // tensor maps of a call's operands, and which kernel runs.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "ra_ffn.h"
 #include "ra_ffn_mma.h"
 #include "ra_ops_host.h"
@@ -248,6 +250,75 @@ Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens, int keep_bits)
   return best;
 }
 
+// One product on the tensor cores, in as few launches as its ranks fit into.
+template <class Args> ra_status run_planned(ra_ffn_handle h, FfnStage stage, const Plan& plan, const FfnArgs& f,
+                                            cudaStream_t st) {
+  constexpr bool kFew = std::is_same<Args, FewArgs>::value;
+  Args a;
+  a.tokens = f.rows;
+  a.segments = stage == kFfnGradX ? 2 : 1;
+  a.dim = f.dim;
+  a.keep_bits = f.keep_bits;
+  a.act = f.act;
+  a.grad_f32 = f.grad_f32;
+  a.err = h->err;
+  a.nt = plan.nt;
+  a.split = plan.split;
+  a.early = stage == kFfnOut || stage == kFfnGradX;
+  const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
+  const bool wide = stage == kFfnHidden, grads = stage == kFfnGradW;
+  const int64_t N = wide || stage == kFfnGradHidden ? h->C : h->dim;   // columns of the product
+  if (kFew) {
+    a.tiles_m = (int)((N + 127) / 128);
+    a.tiles_n = (int)((f.rows + plan.nt - 1) / plan.nt);
+  } else {
+    a.tiles_m = (int)(((grads ? h->C : f.rows) + 255) / 256);
+    a.tiles_n = (int)(wide ? (N + 127) / 128 : (N + 255) / 256);
+  }
+  // rows of operands that run along the terms come 128 at a time, rows across them one a term, 64 at a time
+  // (for few tokens, theirs as many as a tile has)
+  const auto in_rows = [&](int k) {
+    const bool tokens = as == kFfnOut ? k < 2 : k == 0;
+    return grads ? 64 : kFew && tokens ? plan.nt : as == kFfnOut && k >= 2 ? 64 : 128;
+  };
+  const int launches = (h->R + Args::kRanks - 1) / Args::kRanks, most = (h->R + launches - 1) / launches;
+  for (int r0 = 0; r0 < h->R; r0 += most) {
+    const int ranks = h->R - r0 < most ? h->R - r0 : most;
+    for (int& level : a.level) level = 3;
+    for (int i = 0; i < ranks; ++i) {
+      const int r = r0 + i;
+      const Matrices m(stage, f, r);
+      bool ok = true;
+      MmaRank<Args::kMaps>& to = a.rank[i];
+      to.width = f.width(r);
+      for (int k = 0; k < 2; ++k) to.scales[k] = f.scales[k][r];
+      for (int k = 0; k < (kFew ? 4 : 5); ++k)
+        if (m.in[k].p && m.in[k].rows && m.in[k].columns) ok = ok && encode(&to.map[k], h->dtype, m.in[k], 128, in_rows(k));
+      for (int k = 0; k < 5; ++k) {
+        const Matrix& o = m.out[k];
+        to.rows[k] = static_cast<char*>(const_cast<void*>(o.p));
+        to.stride[k] = o.stride * o.elem;
+        if (!o.p) continue;
+        const uintptr_t bits = o.bits();
+        const int level = bits % 32 == 0 ? 3 : bits % 16 == 0 ? 2 : bits % 8 == 0 ? 1 : 0;
+        if (level < a.level[k]) a.level[k] = level;
+        if constexpr (!kFew)
+          if (k < m.outs && level >= 2 && o.rows && o.columns)
+            ok = ok && encode(&to.map[first_rows(as) + k], h->dtype, o, 64, 32);
+      }
+      if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    }
+    a.tiles = (int64_t)a.tiles_m * a.tiles_n * (grads ? 3 * ranks : ranks);
+    a.ring = a.tiles * plan.split <= h->sms ? kFewRingAlone : kFewRing;
+    const bool bf16 = h->dtype == RA_BF16;
+    cudaError_t e;
+    if constexpr (kFew) e = bf16 ? launch_ffn_few<RA_BF16>(as, a, st) : launch_ffn_few<RA_F16>(as, a, st);
+    else e = bf16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st) : launch_ffn_mma<RA_F16>(as, a, h->sms, st);
+    if (e != cudaSuccess) return cuda_error(e, "feed-forward launch");
+  }
+  return RA_OK;
+}
+
 ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st) {
   uintptr_t operands = 0;
   for (int r = 0; r < h->ranks; ++r) {
@@ -260,68 +331,8 @@ ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st
     return e == cudaSuccess ? RA_OK : cuda_error(e, "feed-forward launch");
   }
   if (!encoder()) return record_error(RA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-  MmaArgs a;
-  a.tokens = f.rows;
-  a.segments = stage == kFfnGradX ? 2 : 1;
-  a.dim = f.dim;
-  a.keep_bits = f.keep_bits;
-  a.act = f.act;
-  a.grad_f32 = f.grad_f32;
-  a.err = h->err;
-  const FfnStage as = stage == kFfnGradX ? kFfnOut : stage;
-  const bool wide = stage == kFfnHidden, grads = stage == kFfnGradW;
-  const int64_t M = grads ? h->C : f.rows, N = wide || stage == kFfnGradHidden ? h->C : h->dim;
   const Plan plan = plan_of(h, stage, f.rows, f.keep_bits);
-  a.nt = plan.nt;
-  a.split = plan.split;
-  a.early = stage == kFfnOut || stage == kFfnGradX;
-  if (plan.few) {
-    a.tiles_m = (int)((N + 127) / 128);
-    a.tiles_n = (int)((f.rows + plan.nt - 1) / plan.nt);
-  } else {
-    a.tiles_m = (int)((M + 255) / 256);
-    a.tiles_n = (int)(wide ? (N + 127) / 128 : (N + 255) / 256);
-  }
-  // rows of operands that run along the terms come 128 at a time, rows across them one a term, 64 at a time
-  // (for few tokens, theirs as many as a tile has)
-  const auto in_rows = [&](int k) {
-    const bool tokens = as == kFfnOut ? k < 2 : k == 0;
-    return plan.few && tokens ? plan.nt : grads || (as == kFfnOut && k >= 2) ? 64 : 128;
-  };
-  for (int r0 = 0; r0 < h->R; r0 += kLaunchRanks) {
-    const int ranks = h->R - r0 < kLaunchRanks ? h->R - r0 : kLaunchRanks;
-    for (int& level : a.level) level = 3;
-    for (int i = 0; i < ranks; ++i) {
-      const int r = r0 + i;
-      const Matrices m(stage, f, r);
-      bool ok = true;
-      MmaRank& to = a.rank[i];
-      to.width = f.width(r);
-      for (int k = 0; k < 2; ++k) to.scales[k] = f.scales[k][r];
-      for (int k = 0; k < 5; ++k)
-        if (m.in[k].p && m.in[k].rows && m.in[k].columns) ok = ok && encode(&to.map[k], h->dtype, m.in[k], 128, in_rows(k));
-      for (int k = 0; k < 5; ++k) {
-        const Matrix& o = m.out[k];
-        to.rows[k] = static_cast<char*>(const_cast<void*>(o.p));
-        to.stride[k] = o.stride * o.elem;
-        if (!o.p) continue;
-        const uintptr_t bits = o.bits();
-        const int level = bits % 32 == 0 ? 3 : bits % 16 == 0 ? 2 : bits % 8 == 0 ? 1 : 0;
-        if (level < a.level[k]) a.level[k] = level;
-        if (!plan.few && k < m.outs && level >= 2 && o.rows && o.columns)
-          ok = ok && encode(&to.map[first_rows(as) + k], h->dtype, o, 64, 32);
-      }
-      if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    }
-    a.tiles = (int64_t)a.tiles_m * a.tiles_n * (grads ? 3 * ranks : ranks);
-    a.ring = a.tiles * (plan.few ? plan.split : 0) <= h->sms ? kFewRingAlone : kFewRing;
-    const bool bf16 = h->dtype == RA_BF16;
-    const cudaError_t e = plan.few ? (bf16 ? launch_ffn_few<RA_BF16>(as, a, st) : launch_ffn_few<RA_F16>(as, a, st))
-                                   : (bf16 ? launch_ffn_mma<RA_BF16>(as, a, h->sms, st)
-                                           : launch_ffn_mma<RA_F16>(as, a, h->sms, st));
-    if (e != cudaSuccess) return cuda_error(e, "feed-forward launch");
-  }
-  return RA_OK;
+  return plan.few ? run_planned<FewArgs>(h, stage, plan, f, st) : run_planned<MmaArgs>(h, stage, plan, f, st);
 }
 
 ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_dtype grad_dtype, ra_ffn_handle* out) {

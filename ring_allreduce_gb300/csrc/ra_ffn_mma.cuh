@@ -181,7 +181,7 @@ template <int Stage> struct Epilogue {
   }
   // A filled unit to the columns from `column` on of rows `k`, elements of `elem` bytes, `left` columns to come.
   __device__ __forceinline__ void store(uint32_t unit, int k, int column, int left, int elem) const {
-    const MmaRank& t = a.rank[r];
+    const MmaRank<MmaArgs::kMaps>& t = a.rank[r];
     // (a copy is cut off to 16 bytes, not to the element)
     if (a.level[k] >= 2 && (left * elem >= 64 || left * elem % 16 == 0)) {
       fence_proxy_async_smem();

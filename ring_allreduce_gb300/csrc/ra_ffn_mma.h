@@ -8,9 +8,6 @@
 
 namespace ra {
 
-// One launch's ranks: with more, maps and addresses outgrow a kernel's arguments.
-constexpr int kLaunchRanks = 16;
-
 // Buffers of a launch by stage.  Operands, by their maps alone (x and grad_out the same for all ranks, or not):
 //   hidden       0 x, 1 gate, 2 up
 //   out, grad_x  0, 1 hidden, or grad_gate and grad_up; 2, 3 their weights
@@ -26,15 +23,18 @@ __host__ __device__ constexpr int first_rows(int stage) {
 }
 
 // What a launch knows of a rank, in one place: a CTA reads one rank's alone.
-struct MmaRank {
-  CUtensorMap map[8];
+template <int Maps> struct MmaRank {
+  CUtensorMap map[Maps];
   char* rows[5];         // NULL: absent
   int64_t stride[5];     // bytes
   float* scales[2];
   int width;
 };
 
-struct MmaArgs {
+// Ranks of one launch, `Ranks` at most: with more, maps and addresses outgrow a kernel's arguments.
+template <int Maps, int Ranks>
+struct MmaArgsOf {
+  static constexpr int kMaps = Maps, kRanks = Ranks;
   int64_t tokens;
   int64_t tiles;          // of all jobs
   int tiles_m, tiles_n;   // of one; for few tokens: of the weights' rows, of the tokens
@@ -49,13 +49,15 @@ struct MmaArgs {
   int early;              // the stream's kernel before this one is the call's own
   int ring;               // bytes of the operands' ring
   ra_device_error* err;   // where a wait that gives up says so
-  MmaRank rank[kLaunchRanks];
+  MmaRank<Maps> rank[Ranks];
 };
+using MmaArgs = MmaArgsOf<8, 16>;
+using FewArgs = MmaArgsOf<4, kMaxRanks>;   // operands alone have maps
 
 // Dtype: RA_BF16 or RA_F16.  kFfnGradX runs as kFfnOut with two segments.
 template <int Dtype> cudaError_t launch_ffn_mma(FfnStage stage, const MmaArgs& a, int sms, cudaStream_t st);
 // All but kFfnGradW, for few tokens; the operands' maps of the tokens have boxes of a.nt rows.
-template <int Dtype> cudaError_t launch_ffn_few(FfnStage stage, const MmaArgs& a, cudaStream_t st);
+template <int Dtype> cudaError_t launch_ffn_few(FfnStage stage, const FewArgs& a, cudaStream_t st);
 // Rings for few tokens: for one CTA an SM, or two.
 constexpr int kFewRing = 104 * 1024, kFewRingAlone = 208 * 1024;
 constexpr int kFewABytes = 128 * 64 * 2, kFewMostStages = 12;

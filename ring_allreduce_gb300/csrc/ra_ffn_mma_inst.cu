@@ -30,7 +30,7 @@ template <class D, int Stage, int Act> cudaError_t launch(const MmaArgs& a, int 
   return launch_after(kernel, dim3((unsigned)(2 * pairs)), dim3(kMmaThreads), mma_shared(Stage), st, 2, a);
 }
 
-template <class D, int Stage, int Act> cudaError_t launch_few(const MmaArgs& a, cudaStream_t st) {
+template <class D, int Stage, int Act> cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> opted{0};
   const auto kernel = ffn_few_kernel<D, Stage, Act>;
   const cudaError_t e = opt_in(kernel, kFewRingAlone + 1024, &opted);
@@ -40,7 +40,7 @@ template <class D, int Stage, int Act> cudaError_t launch_few(const MmaArgs& a, 
 
 }  // namespace
 
-template <> cudaError_t launch_ffn_few<RA_INST_DTYPE>(FfnStage stage, const MmaArgs& a, cudaStream_t st) {
+template <> cudaError_t launch_ffn_few<RA_INST_DTYPE>(FfnStage stage, const FewArgs& a, cudaStream_t st) {
   using D = DTypeOf<RA_INST_DTYPE>::type;
   const cudaError_t e = debug_upload(st);
   if (e != cudaSuccess) return e;
