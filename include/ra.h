@@ -690,9 +690,11 @@ ra_status ra_vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distill_ba
  * Buffers may start on any element and have any stride, as for the operators
  * above, but products run on the tensor cores only where the rows of both
  * their operands start on 16-byte boundaries; otherwise on the CUDA cores,
- * some thirty times slower.  (`dim` a multiple of 8, or padded rows: the
+ * thirty to a hundred times slower.  (`dim` a multiple of 8, or padded rows: the
  * inner width and the number of rows do not matter, as hidden, grad_gate and
- * grad_up may have padded rows.) */
+ * grad_up may have padded rows.)  The tensor cores take 16-bit operands, so what one product
+ * gives the next -- hidden, grad_gate, grad_up -- is rounded to dtype in
+ * between; every sum is held in binary32. */
 typedef struct ra_ffn_ctx* ra_ffn_handle;
 typedef enum ra_activation { RA_SILU = 0, RA_GELU = 1 } ra_activation;   /* a / (1 + e^-a); a (1 + erf(a / sqrt 2)) / 2 */
 ra_status ra_ffn_create(int R, int dim, size_t inner, ra_dtype dtype, ra_activation activation, ra_dtype grad_dtype,

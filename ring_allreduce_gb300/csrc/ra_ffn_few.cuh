@@ -16,6 +16,12 @@
 // warps every other eight tokens; warp 8 copies; warp 9 issues the products.  A product whose predecessor in
 // the stream is the call's own, which writes no weights, fetches its first weights
 // before that has ended.
+//
+// What bounds it is DRAM where the weights are large: one token of 4096 x 16384
+// in 8 ranks takes 67 us for 403 MB, 0.88 of the copy bandwidth, 37 tokens 75
+// us (large tiles: 103 and 82).  Where they are not, a chain of steps: the
+// predecessor's end 1 us, the first copy 1.5, the terms, a cluster's exchange
+// 2 to 3, the epilogue 1: 7 us for a product of 1024 x 2048 a rank.
 #pragma once
 
 #include "ra_ffn.cuh"

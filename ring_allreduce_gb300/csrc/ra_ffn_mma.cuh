@@ -27,8 +27,17 @@
 // hold a row takes a cycle of it a row and 16 bytes; so the epilogue lays its
 // outputs down in shared memory, 64 bytes of 32 rows at a time, and has them
 // stored by tensor map, which also cuts them off at the last row and column
-// (dh of 4096 x 8192 from 2048 columns: 120 -> 112 us; the projections
-// of 8192 x 16384 from 4096: 1108 -> 1079 us).
+// (the projections of 8192 tokens, 4096 x 16384: 1108 -> 1079 us; their
+// gradients' kernel, 4096 x 8192 from 2048 columns: 120 -> 112).
+//
+// Measured one by one, bf16: the projections of 8192 tokens, 4096 x 16384 in
+// four ranks, at 2.04 PFLOP/s, the product back at 2.03; both together, over
+// and over, 1.91 ms, 1.73 PFLOP/s, where the power limit holds a plain library
+// product of that size to the same.  What bounds them beside the tensor cores is the way from L2: 64
+// bytes a cycle and SM, 15 TB/s together.  The weights' gradients reach 1.8 to
+// 1.9 PFLOP/s (their rows lie across the terms), the gradients of a and b 1.2
+// to 1.6: of them the epilogue, which reads kept rows 32 bytes at a time and
+// writes three outputs, takes 12.8 us a tile, as long as the products of some 2900 columns.
 #pragma once
 
 #include "ra_ffn.cuh"

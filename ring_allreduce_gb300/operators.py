@@ -249,8 +249,8 @@ class FeedForward(_Handle):
 
     Products run on the tensor cores where the rows of their operands start on
     16-byte boundaries: `dim` a multiple of 8 (or padded rows), and hidden,
-    grad_gate and grad_up as ``rows`` makes them.  Others take some thirty
-    times as long."""
+    grad_gate and grad_up as ``rows`` makes them.  Others take thirty to a
+    hundred times as long."""
 
     _destroy, _set_option = staticmethod(_lib.ra_ffn_destroy), staticmethod(_lib.ra_ffn_set_option)
 
