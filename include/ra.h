@@ -685,7 +685,7 @@ ra_status ra_vocab_distill_backward(ra_vocab_handle h, const ra_vocab_distill_ba
  * ra_chunk_plan(R, inner), [r C, min((r+1) C, inner)), C = ceil(inner / R); its
  * three weights are [width_r][dim], and the pointers of ranks without columns
  * are not looked at.  dtype: RA_BF16 or RA_F16.  grad_dtype, the weights'
- * gradients': dtype or RA_F32.
+ * gradients': dtype or RA_F32.  A call takes at most 2^27 rows.
  *
  * Buffers may start on any element and have any stride, as for the operators
  * above, but products run on the tensor cores only where the rows of both

@@ -28,7 +28,7 @@ namespace {
 using namespace ra;
 
 constexpr int kMaxDim = 1 << 20, kMaxInner = 1 << 24;
-constexpr size_t kMaxFfnRows = (size_t)1 << 30;
+constexpr size_t kMaxFfnRows = (size_t)1 << 27;   // sums over more would come near the waits' limit
 
 using FfnBuffers = BuffersOf<17 * kMaxRanks>;
 
@@ -112,7 +112,7 @@ ra_status check_ffn(ra_ffn_handle h, const void* args) {
 }
 
 ra_status check_ffn_rows(size_t rows) {
-  if (rows > kMaxFfnRows) return record_error(RA_ERR_INVALID, "rows=%zu above 2^30", rows);
+  if (rows > kMaxFfnRows) return record_error(RA_ERR_INVALID, "rows=%zu above 2^27", rows);
   return RA_OK;
 }
 

@@ -1,5 +1,6 @@
 """How FeedForward may be called: buffers that lie in other ways, several host threads, far rows."""
 
+import ctypes
 import threading
 
 import pytest
@@ -152,3 +153,52 @@ def test_long_sums(ops):
     """Ten thousand columns against a rank's hundred, and the other way about."""
     both_ways(ops.FeedForward(2, 10000, 200, grad_dtype="f32"), f.Block(38, 2, 37, 10000, 200, grad_dtype="f32"))
     both_ways(ops.FeedForward(1, 72, 20011), f.Block(39, 1, 130, 72, 20011))
+
+
+def test_refusals_at_the_c_boundary(ops):
+    """What only a C caller can ask for."""
+    lib = ops._lib
+
+    class ForwardArgs(ctypes.Structure):   # ra_ffn_forward_args
+        _fields_ = [(n, ctypes.c_int if n in ("xs", "keep_bits") else
+                     ctypes.c_size_t if n in ("rows", "x_stride", "out_stride") else ctypes.c_void_p) for n in
+                    ("rows x x_stride xs w_gate w_gate_strides w_up w_up_strides w_down w_down_strides hidden "
+                     "hidden_strides out out_stride keep_bits gate gate_strides up up_strides gate_scales up_scales").split()]
+
+    h = ctypes.c_void_p()
+    assert lib.ra_ffn_create(2, 64, 256, 1, 0, 1, ctypes.byref(h)) == 0
+
+    def call(**kw):
+        args = ForwardArgs(**{**dict(rows=4, xs=1), **kw})
+        return lib.ra_ffn_forward(h, ctypes.addressof(args), None)
+
+    assert call(rows=0) == 0
+    for bad in (dict(rows=2 ** 27 + 1), dict(xs=3), dict(xs=0), dict(keep_bits=4), dict(), dict(rows=2 ** 63)):
+        assert call(**bad) == 1
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    host = torch.zeros((4, 64), dtype=torch.bfloat16)
+    w = torch.zeros((128, 64), dtype=torch.bfloat16, device="cuda")
+    hid, out = torch.zeros((2, 4, 128), dtype=torch.bfloat16, device="cuda"), torch.full((2, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    held = []
+
+    def array(kind, values):
+        held.append((kind * len(values))(*values))
+        return ctypes.addressof(held[-1])
+
+    arr, sizes = (lambda *v: array(ctypes.c_void_p, v)), (lambda *v: array(ctypes.c_size_t, v))
+    ok = dict(x=arr(x.data_ptr()), x_stride=64, w_gate=arr(w.data_ptr(), w.data_ptr()), w_gate_strides=sizes(64, 64),
+              out=arr(out[0].data_ptr(), out[1].data_ptr()), out_stride=64, hidden=arr(hid[0].data_ptr(), hid[1].data_ptr()),
+              hidden_strides=sizes(128, 128))
+    ok.update(w_up=ok["w_gate"], w_up_strides=ok["w_gate_strides"], w_down=ok["w_gate"], w_down_strides=ok["w_gate_strides"])
+    for bad in (dict(x=arr(host.data_ptr())), dict(x_stride=63), dict(hidden=arr(hid[0].data_ptr(), 0)),
+                dict(hidden=arr(hid[0].data_ptr(), hid[0].data_ptr())), dict(w_up=None), dict(out=arr(x.data_ptr(), out[1].data_ptr())),
+                dict(x=arr(x.data_ptr() + 1)), dict(keep_bits=8), dict(hidden_strides=sizes(128, 2 ** 50))):
+        assert call(**{**ok, **bad}) == 1
+        assert lib.ra_last_error()
+    torch.cuda.synchronize()
+    assert (out == 9).all()
+    assert call(**ok) == 0
+    torch.cuda.synchronize()
+    assert (out == 0).all()
+    assert lib.ra_ffn_set_option(h, 4, 2) == 1 and lib.ra_ffn_set_option(h, 1, 1) == 1 and lib.ra_ffn_set_option(h, 4, 0) == 0
+    assert lib.ra_ffn_destroy(h) == 0
