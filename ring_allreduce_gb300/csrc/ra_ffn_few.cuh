@@ -48,8 +48,8 @@ __device__ __forceinline__ void st_cluster(uint32_t at, float v) {
 
 }  // namespace
 
-template <class D, int Stage, int Act>
-__global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_constant__ FewArgs a) {
+template <class D, int Stage, int Act, int Ranks>
+__global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_constant__ FewArgs<Ranks> a) {
   using T = typename D::T;
   constexpr bool kAMn = Stage == kFfnOut;   // the weights' rows run along the terms
   constexpr int kSums = few_sums(Stage);
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
   const int per = a.tiles_m * a.tiles_n;
   const int r = (int)(tile / per), u = (int)(tile - (int64_t)r * per);
   const int m0 = u / a.tiles_n * kFewRows, t0 = u % a.tiles_n * nt;
-  const MmaRank<FewArgs::kMaps>& k = a.rank[r];
+  const auto& k = a.rank[r];
   const int width = k.width;
   const int m = Stage == kFfnOut ? a.dim : width;   // weight rows there are
   const int half = ((Stage == kFfnOut ? width : a.dim) + kFewK - 1) / kFewK;

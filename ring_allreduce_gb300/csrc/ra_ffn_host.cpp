@@ -253,7 +253,7 @@ Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens, int keep_bits)
 // One product on the tensor cores, in as few launches as its ranks fit into.
 template <class Args> ra_status run_planned(ra_ffn_handle h, FfnStage stage, const Plan& plan, const FfnArgs& f,
                                             cudaStream_t st) {
-  constexpr bool kFew = std::is_same<Args, FewArgs>::value;
+  constexpr bool kFew = !std::is_same<Args, MmaArgs>::value;
   Args a;
   a.tokens = f.rows;
   a.segments = stage == kFfnGradX ? 2 : 1;
@@ -332,7 +332,9 @@ ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st
   }
   if (!encoder()) return record_error(RA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
   const Plan plan = plan_of(h, stage, f.rows, f.keep_bits);
-  return plan.few ? run_planned<FewArgs>(h, stage, plan, f, st) : run_planned<MmaArgs>(h, stage, plan, f, st);
+  if (!plan.few) return run_planned<MmaArgs>(h, stage, plan, f, st);
+  return h->R <= kFewRanks ? run_planned<FewArgs<kFewRanks>>(h, stage, plan, f, st)
+                           : run_planned<FewArgs<kMaxRanks>>(h, stage, plan, f, st);
 }
 
 ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_dtype grad_dtype, ra_ffn_handle* out) {

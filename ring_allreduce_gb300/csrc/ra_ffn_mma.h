@@ -52,12 +52,15 @@ struct MmaArgsOf {
   MmaRank<Maps> rank[Ranks];
 };
 using MmaArgs = MmaArgsOf<8, 16>;
-using FewArgs = MmaArgsOf<4, kMaxRanks>;   // operands alone have maps
+// For few tokens operands alone have maps; and few ranks' arguments are handed over sooner.
+template <int Ranks> using FewArgs = MmaArgsOf<4, Ranks>;
+constexpr int kFewRanks = 8;
 
 // Dtype: RA_BF16 or RA_F16.  kFfnGradX runs as kFfnOut with two segments.
 template <int Dtype> cudaError_t launch_ffn_mma(FfnStage stage, const MmaArgs& a, int sms, cudaStream_t st);
 // All but kFfnGradW, for few tokens; the operands' maps of the tokens have boxes of a.nt rows.
-template <int Dtype> cudaError_t launch_ffn_few(FfnStage stage, const FewArgs& a, cudaStream_t st);
+template <int Dtype> cudaError_t launch_ffn_few(FfnStage stage, const FewArgs<kFewRanks>& a, cudaStream_t st);
+template <int Dtype> cudaError_t launch_ffn_few(FfnStage stage, const FewArgs<kMaxRanks>& a, cudaStream_t st);
 // Rings for few tokens: for one CTA an SM, or two.
 constexpr int kFewRing = 104 * 1024, kFewRingAlone = 208 * 1024;
 constexpr int kFewABytes = 128 * 64 * 2, kFewMostStages = 12;
