@@ -313,75 +313,174 @@ __device__ __forceinline__ void write_hidden(const MmaArgs& a, const Tile& p, Ep
   }
 }
 
+// A warp's 32 rows of 128 kept codes, gate or up: fetched with eight lanes to a
+// row, a line of memory at a time, and handed to the rows' lanes through
+// shared memory.  (A row a lane, 32 bytes at a time, is four requests for the
+// line; they took a third of the epilogue.)
+struct KeptCodes {
+  uint4 q[8];   // of rows lane / 8, lane / 8 + 4, ...: 16 columns
+  __device__ __forceinline__ void fetch(const MmaArgs& a, const Epilogue<kFfnGradHidden>& e, int k, int first, int left) {
+    const int64_t stride = a.rank[e.r].stride[k];
+    const char* const from = a.rank[e.r].rows[k] + e.row0 * stride + first + e.lane % 8 * 16;
+    const int mine = left - e.lane % 8 * 16, level = a.level[k];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int y = e.lane / 8 + 4 * i;
+      const char* const at = from + y * stride;
+      uint32_t w[4] = {};
+      if (y < e.rows && mine > 0) {
+        if (level >= 2 && mine >= 16) {
+          if (RA_ACCESS_OK(at, 16u, 1u)) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            if (level && mine >= 4 * j + 8) {
+              const uint2 x = ld_g(reinterpret_cast<const uint2*>(at) + j / 2);
+              w[j] = x.x, w[j + 1] = x.y;
+            } else {
+#pragma unroll 1
+              for (int n = 0; n < 8 && 4 * j + n < mine; ++n) {
+                const uint32_t x = (uint32_t)ld_g(reinterpret_cast<const uint8_t*>(at) + 4 * j + n) << (8 * (n % 4));
+                if (n < 4) w[j] |= x;
+                else w[j + 1] |= x;
+              }
+            }
+          }
+        }
+      }
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // To `staging`, 4 KB; then this lane's row back from there, 128 columns as they lie.
+  __device__ __forceinline__ void put(uint32_t staging, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t y = (uint32_t)(lane / 8 + 4 * i);
+      st_shared16(staging + y * 128u + ((((uint32_t)lane & 7u) ^ (y & 7u)) << 4), q[i].x, q[i].y, q[i].z, q[i].w);
+    }
+  }
+  __device__ __forceinline__ void get(uint32_t staging, int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                   : "r"(staging + (uint32_t)lane * 128u + (((uint32_t)i ^ ((uint32_t)lane & 7u)) << 4))
+                   : "memory");
+  }
+};
+
+// 16 columns of a row: the gradients of a and b, and hidden, from dh and what was kept.
+template <class D, int Act, class P>
+__device__ __forceinline__ void gradients(const float* dh, const P& pair, uint32_t (*w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 g = pair(0, j), u = pair(1, j), d = make_float2(dh[2 * j], dh[2 * j + 1]);
+    float2 act, slope;
+    activate<Act, true>(g, &act, &slope);
+    const float2 da = __fmul2_rn(__fmul2_rn(d, u), slope), db = __fmul2_rn(d, act), h = __fmul2_rn(act, u);
+    w[0][j] = pack2<D>(da.x, da.y);
+    w[1][j] = pack2<D>(db.x, db.y);
+    w[2][j] = pack2<D>(h.x, h.y);
+  }
+}
+
 // 128 columns of a row of dh, from which the gradients of a and b are made, 32
-// at a time.  What was kept of them is fetched a chunk ahead, of the first while the products still run.
+// at a time.  Kept codes are fetched while the products still run; 16-bit
+// values, for which there are not the registers, a chunk ahead.
 template <class D, int Act, bool Coded, class W>
 __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& p, Epilogue<kFfnGradHidden>& e,
                                                   const W& wait, uint64_t* full, uint32_t parity) {
   const int r = p.r, first = p.n0 + e.half * kBlockN;
-  constexpr int kWords = Coded ? 8 : 16, kElem = Coded ? 1 : 2;
   float scale[2] = {};
-  uint32_t next[2][kWords] = {};
+  KeptCodes codes[Coded ? 2 : 1];
+  uint32_t next[2][Coded ? 1 : 16] = {};
   const auto fetch = [&](int col) {
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < kWords; k += 8)
-        get_words(e.at(3 + b, col, kElem) + 4 * k, next[b] + k, (p.n - col) * kElem - 4 * k, a.level[3 + b]);
+      for (int k = 0; k < 16; k += 8)
+        get_words(e.at(3 + b, col, 2) + 4 * k, next[b] + (Coded ? 0 : k), (p.n - col) * 2 - 4 * k, a.level[3 + b]);
   };
-  if (e.in() && first < p.n) {
-    fetch(first);
-    if (Coded) {
+  if constexpr (Coded) {
+    codes[0].fetch(a, e, 3, first, p.n - first);
+    codes[1].fetch(a, e, 4, first, p.n - first);
+    if (e.in() && first < p.n) {
       const int64_t at = e.row() * ((p.n + kGroup - 1) / kGroup) + first / kGroup;
       scale[0] = ld_g(a.rank[r].scales[0] + at);
       scale[1] = ld_g(a.rank[r].scales[1] + at);
     }
+  } else {
+    if (e.in() && first < p.n) fetch(first);
   }
   if (!wait(full, parity, 4)) return false;
   tensor_fence_after();
-#pragma unroll 1
+  if constexpr (Coded) {
+    if (e.lane == 0) bulk_wait_read<0>();   // the units are free
+    __syncwarp();
+    codes[0].put(e.staging, e.lane);
+    codes[1].put(e.staging + 4096, e.lane);
+    __syncwarp();
+    codes[0].get(e.staging, e.lane);
+    codes[1].get(e.staging + 4096, e.lane);
+    __syncwarp();
+  }
+  // Codes are taken from the registers they were fetched into, which asks for
+  // four copies of the body (moved to the front for one copy instead: 8192
+  // columns of 4096 tokens by 1024, two ranks, 90 -> 98 us); with 16-bit
+  // values one copy is the faster (131 -> 121 us).
+#pragma unroll(Coded ? 4 : 1)
   for (int c = 0; c < 4; ++c) {
     const int col = first + 32 * c, left = p.n - col;
-    uint32_t now[2][kWords];
+    uint32_t now[2][Coded ? 1 : 16];
+    if constexpr (!Coded) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) {
-        now[b][k] = next[b][k];
-        next[b][k] = 0u;
-      }
+        for (int k = 0; k < 16; ++k) {
+          now[b][k] = next[b][k];
+          next[b][k] = 0u;
+        }
+    }
     float dh[32];
     e.sums(e.half * kBlockN + 32 * c, dh);
-    if (c < 3 && left > 32 && e.in()) fetch(col + 32);
+    if (!Coded && c < 3 && left > 32 && e.in()) fetch(col + 32);
     tmem_wait_loads();
     if (c == 3) e.release();
     if (left <= 0) continue;
-    uint32_t w[3][16];
+    // three units at once: what was stored before the last copy has been read
+    uint32_t unit[3];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float2 g, u;
-      if constexpr (Coded) {
-        g = __fmul2_rn(code_pair(bias_codes(now[0][j / 2]), 2 * (j % 2)), both(scale[0]));
-        u = __fmul2_rn(code_pair(bias_codes(now[1][j / 2]), 2 * (j % 2)), both(scale[1]));
-      } else {
-        unpack2<D>(now[0][j], reinterpret_cast<float*>(&g));
-        unpack2<D>(now[1][j], reinterpret_cast<float*>(&u));
+    for (int k = 0; k < 3; ++k) unit[k] = (e.next + k) % e.kUnits;
+    e.next = (e.next + (a.rank[r].rows[2] ? 3 : 2)) % e.kUnits;
+    if (e.lane == 0) bulk_wait_read<e.kUnits - 3>();
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[3][8];
+      gradients<D, Act>(dh + 16 * h, [&](int b, int j) {
+        if constexpr (Coded) {
+          const uint4& x = codes[b].q[2 * c + h];
+          const uint32_t word = j < 2 ? x.x : j < 4 ? x.y : j < 6 ? x.z : x.w;
+          return __fmul2_rn(code_pair(bias_codes(word), 2 * (j % 2)), both(scale[b]));
+        } else {
+          float2 v;
+          unpack2<D>(now[b][8 * h + j], reinterpret_cast<float*>(&v));
+          return v;
+        }
+      }, w);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (k == 2 && !a.rank[r].rows[2]) continue;
+        st_shared16(e.piece(unit[k], 2 * h), w[k][0], w[k][1], w[k][2], w[k][3]);
+        st_shared16(e.piece(unit[k], 2 * h + 1), w[k][4], w[k][5], w[k][6], w[k][7]);
       }
-      const float2 d = make_float2(dh[2 * j], dh[2 * j + 1]);
-      float2 act, slope;
-      activate<Act, true>(g, &act, &slope);
-      const float2 da = __fmul2_rn(__fmul2_rn(d, u), slope), db = __fmul2_rn(d, act), h = __fmul2_rn(act, u);
-      w[0][j] = pack2<D>(da.x, da.y);
-      w[1][j] = pack2<D>(db.x, db.y);
-      w[2][j] = pack2<D>(h.x, h.y);
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      if (k == 2 && !a.rank[r].rows[2]) continue;
-      const uint32_t unit = e.take();
-      e.fill(unit, w[k]);
-      e.store(unit, k, col, left, 2);
-    }
+    for (int k = 0; k < 3; ++k)
+      if (k < 2 || a.rank[r].rows[2]) e.store(unit[k], k, col, left, 2);
   }
   return true;
 }
