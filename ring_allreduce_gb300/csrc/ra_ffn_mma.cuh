@@ -35,9 +35,10 @@
 // and over, 1.91 ms, 1.73 PFLOP/s, where the power limit holds a plain library
 // product of that size to the same.  What bounds them beside the tensor cores is the way from L2: 64
 // bytes a cycle and SM, 15 TB/s together.  The weights' gradients reach 1.8 to
-// 1.9 PFLOP/s (their rows lie across the terms), the gradients of a and b 1.2
-// to 1.6: of them the epilogue, which reads kept rows 32 bytes at a time and
-// writes three outputs, takes 12.8 us a tile, as long as the products of some 2900 columns.
+// 1.9 PFLOP/s (their rows lie across the terms), the gradients of a and b 1.1
+// to 1.6: of them the epilogue, which reads two kept tensors and writes three,
+// takes 11 us a tile from codes and 13.8 from 16-bit values (SiLU; GELU 13.8 and
+// 15.3), as long as the products of some 2600 columns and more.
 #pragma once
 
 #include "ra_ffn.cuh"
@@ -116,33 +117,6 @@ template <int Stage> __device__ __forceinline__ int operand_maps(const MmaArgs& 
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
-// 32 bytes of this lane's row, `left` of the rows' bytes still to come.
-__device__ __forceinline__ void get_words(const char* p, uint32_t* w, int left, int level) {
-  if (left >= 32 && level == 3) {
-    if (RA_ACCESS_OK(p, 32u, 1u))
-      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                   : "l"(p)
-                   : "memory");
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    if (level && left >= 4 * j + 8) {
-      const uint2 x = ld_g(reinterpret_cast<const uint2*>(p) + j / 2);
-      w[j] = x.x;
-      w[j + 1] = x.y;
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < 8 && 4 * j + i < left; ++i) {
-        const uint32_t x = (uint32_t)ld_g(reinterpret_cast<const uint8_t*>(p) + 4 * j + i) << (8 * (i % 4));
-        if (i < 4) w[j] |= x;
-        else w[j + 1] |= x;
-      }
-    }
-  }
 }
 
 // The epilogue of a tile in one of eight warps.
@@ -244,9 +218,6 @@ template <int Stage> struct Epilogue {
     fill(u, w);
     store(u, k, column, left, 2);
   }
-  __device__ __forceinline__ const char* at(int k, int64_t column, int elem) const {
-    return a.rank[r].rows[k] + row() * a.rank[r].stride[k] + column * elem;
-  }
 };
 
 // 64 gated columns of a row.  Kept in 8 bits, the 128 columns that share a scale
@@ -313,19 +284,21 @@ __device__ __forceinline__ void write_hidden(const MmaArgs& a, const Tile& p, Ep
   }
 }
 
-// A warp's 32 rows of 128 kept codes, gate or up: fetched with eight lanes to a
-// row, a line of memory at a time, and handed to the rows' lanes through
-// shared memory.  (A row a lane, 32 bytes at a time, is four requests for the
-// line; they took a third of the epilogue.)
-struct KeptCodes {
-  uint4 q[8];   // of rows lane / 8, lane / 8 + 4, ...: 16 columns
-  __device__ __forceinline__ void fetch(const MmaArgs& a, const Epilogue<kFfnGradHidden>& e, int k, int first, int left) {
+// 16 * kLanes bytes of a warp's 32 kept rows, gate or up: fetched with kLanes
+// lanes to a row, so that a request takes a line of memory or half of one, and
+// handed to the rows' lanes through shared memory.  (A row a lane, 32 bytes at
+// a time, is four requests for a line; they took a third of the epilogue.)
+template <int kLanes> struct KeptRows {
+  static constexpr int kDown = 32 / kLanes;   // rows in a request
+  uint4 q[kLanes];   // of rows lane / kLanes, lane / kLanes + kDown, ...: 16 bytes
+  // From byte `first` of the rows on, of which `left` bytes are to come.
+  __device__ __forceinline__ void fetch(const MmaArgs& a, const Epilogue<kFfnGradHidden>& e, int k, int64_t first, int left) {
     const int64_t stride = a.rank[e.r].stride[k];
-    const char* const from = a.rank[e.r].rows[k] + e.row0 * stride + first + e.lane % 8 * 16;
-    const int mine = left - e.lane % 8 * 16, level = a.level[k];
+    const int mine = left - e.lane % kLanes * 16, level = a.level[k];
+    const char* const from = a.rank[e.r].rows[k] + e.row0 * stride + first + e.lane % kLanes * 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int y = e.lane / 8 + 4 * i;
+    for (int i = 0; i < kLanes; ++i) {
+      const int y = e.lane / kLanes + kDown * i;
       const char* const at = from + y * stride;
       uint32_t w[4] = {};
       if (y < e.rows && mine > 0) {
@@ -354,23 +327,27 @@ struct KeptCodes {
       q[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // To `staging`, 4 KB; then this lane's row back from there, 128 columns as they lie.
+  // Piece x of row y of what lies at `staging`: eight lanes' pieces on different banks, either way.
+  static __device__ __forceinline__ uint32_t place(uint32_t staging, int y, int x) {
+    return staging + (uint32_t)y * (16u * kLanes) + ((uint32_t)(x ^ (y / (8 / kLanes) % kLanes)) << 4);
+  }
   __device__ __forceinline__ void put(uint32_t staging, int lane) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t y = (uint32_t)(lane / 8 + 4 * i);
-      st_shared16(staging + y * 128u + ((((uint32_t)lane & 7u) ^ (y & 7u)) << 4), q[i].x, q[i].y, q[i].z, q[i].w);
-    }
+    for (int i = 0; i < kLanes; ++i)
+      st_shared16(place(staging, lane / kLanes + kDown * i, lane % kLanes), q[i].x, q[i].y, q[i].z, q[i].w);
   }
+  // This lane's row, as it lies.
   __device__ __forceinline__ void get(uint32_t staging, int lane) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kLanes; ++i)
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
-                   : "r"(staging + (uint32_t)lane * 128u + (((uint32_t)i ^ ((uint32_t)lane & 7u)) << 4))
+                   : "r"(place(staging, lane, i))
                    : "memory");
   }
 };
+
+__device__ __forceinline__ uint32_t word_of(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 
 // 16 columns of a row: the gradients of a and b, and hidden, from dh and what was kept.
 template <class D, int Act, class P>
@@ -394,93 +371,98 @@ template <class D, int Act, bool Coded, class W>
 __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& p, Epilogue<kFfnGradHidden>& e,
                                                   const W& wait, uint64_t* full, uint32_t parity) {
   const int r = p.r, first = p.n0 + e.half * kBlockN;
+  constexpr int kLanes = Coded ? 8 : 4;
   float scale[2] = {};
-  KeptCodes codes[Coded ? 2 : 1];
-  uint32_t next[2][Coded ? 1 : 16] = {};
+  KeptRows<kLanes> kept[2];
   const auto fetch = [&](int col) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int k = 0; k < 16; k += 8)
-        get_words(e.at(3 + b, col, 2) + 4 * k, next[b] + (Coded ? 0 : k), (p.n - col) * 2 - 4 * k, a.level[3 + b]);
+    for (int b = 0; b < 2; ++b) kept[b].fetch(a, e, 3 + b, (int64_t)col * (Coded ? 1 : 2), (p.n - col) * (Coded ? 1 : 2));
   };
-  if constexpr (Coded) {
-    codes[0].fetch(a, e, 3, first, p.n - first);
-    codes[1].fetch(a, e, 4, first, p.n - first);
-    if (e.in() && first < p.n) {
-      const int64_t at = e.row() * ((p.n + kGroup - 1) / kGroup) + first / kGroup;
-      scale[0] = ld_g(a.rank[r].scales[0] + at);
-      scale[1] = ld_g(a.rank[r].scales[1] + at);
-    }
-  } else {
-    if (e.in() && first < p.n) fetch(first);
+  fetch(first);
+  if (Coded && e.in() && first < p.n) {
+    const int64_t at = e.row() * ((p.n + kGroup - 1) / kGroup) + first / kGroup;
+    scale[0] = ld_g(a.rank[r].scales[0] + at);
+    scale[1] = ld_g(a.rank[r].scales[1] + at);
   }
   if (!wait(full, parity, 4)) return false;
   tensor_fence_after();
   if constexpr (Coded) {
-    if (e.lane == 0) bulk_wait_read<0>();   // the units are free
+    if (e.lane == 0) bulk_wait_read<0>();   // all units are free
     __syncwarp();
-    codes[0].put(e.staging, e.lane);
-    codes[1].put(e.staging + 4096, e.lane);
+    kept[0].put(e.staging, e.lane);
+    kept[1].put(e.staging + 2 * kUnitBytes, e.lane);
     __syncwarp();
-    codes[0].get(e.staging, e.lane);
-    codes[1].get(e.staging + 4096, e.lane);
+    kept[0].get(e.staging, e.lane);
+    kept[1].get(e.staging + 2 * kUnitBytes, e.lane);
     __syncwarp();
   }
   // Codes are taken from the registers they were fetched into, which asks for
-  // four copies of the body (moved to the front for one copy instead: 8192
-  // columns of 4096 tokens by 1024, two ranks, 90 -> 98 us); with 16-bit
-  // values one copy is the faster (131 -> 121 us).
-#pragma unroll(Coded ? 4 : 1)
-  for (int c = 0; c < 4; ++c) {
-    const int col = first + 32 * c, left = p.n - col;
-    uint32_t now[2][Coded ? 1 : 16];
-    if constexpr (!Coded) {
+  // copies of the body; what is left moves to the front between them, as more
+  // copies than these outgrow the instruction cache.  Two ranks of 8192 columns,
+  // 4096 tokens by 2048, with one copy, two and four: SiLU 121, - and 116 us, GELU
+  // 129, 123 and 131; 16-bit values 146, - and 172.
+  constexpr int kCopies = !Coded ? 1 : Act == RA_SILU ? 4 : 2;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 4; c0 += kCopies) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+    for (int c1 = 0; c1 < kCopies; ++c1) {
+      const int c = c0 + c1, col = first + 32 * c, left = p.n - col;
+      float dh[32];
+      e.sums(e.half * kBlockN + 32 * c, dh);
+      KeptRows<kLanes> now[2] = {kept[0], kept[1]};
+      if constexpr (!Coded) {
+        if (left > 0) {
+          // through the next two units: what was stored before the last two copies has been read
+          if (e.lane == 0) bulk_wait_read<e.kUnits - 2>();
+          __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          now[b][k] = next[b][k];
-          next[b][k] = 0u;
+          for (int b = 0; b < 2; ++b) kept[b].put(e.staging + (e.next + b) % e.kUnits * kUnitBytes, e.lane);
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < 2; ++b) now[b].get(e.staging + (e.next + b) % e.kUnits * kUnitBytes, e.lane);
+          __syncwarp();
+          if (c < 3 && left > 32) fetch(col + 32);
         }
-    }
-    float dh[32];
-    e.sums(e.half * kBlockN + 32 * c, dh);
-    if (!Coded && c < 3 && left > 32 && e.in()) fetch(col + 32);
-    tmem_wait_loads();
-    if (c == 3) e.release();
-    if (left <= 0) continue;
-    // three units at once: what was stored before the last copy has been read
-    uint32_t unit[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) unit[k] = (e.next + k) % e.kUnits;
-    e.next = (e.next + (a.rank[r].rows[2] ? 3 : 2)) % e.kUnits;
-    if (e.lane == 0) bulk_wait_read<e.kUnits - 3>();
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[3][8];
-      gradients<D, Act>(dh + 16 * h, [&](int b, int j) {
-        if constexpr (Coded) {
-          const uint4& x = codes[b].q[2 * c + h];
-          const uint32_t word = j < 2 ? x.x : j < 4 ? x.y : j < 6 ? x.z : x.w;
-          return __fmul2_rn(code_pair(bias_codes(word), 2 * (j % 2)), both(scale[b]));
-        } else {
-          float2 v;
-          unpack2<D>(now[b][8 * h + j], reinterpret_cast<float*>(&v));
-          return v;
-        }
-      }, w);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (k == 2 && !a.rank[r].rows[2]) continue;
-        st_shared16(e.piece(unit[k], 2 * h), w[k][0], w[k][1], w[k][2], w[k][3]);
-        st_shared16(e.piece(unit[k], 2 * h + 1), w[k][4], w[k][5], w[k][6], w[k][7]);
       }
-    }
+      tmem_wait_loads();
+      if (c == 3) e.release();
+      if (left <= 0) continue;
+      // three units at once: what was stored before the last copy has been read
+      uint32_t unit[3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (k < 2 || a.rank[r].rows[2]) e.store(unit[k], k, col, left, 2);
+      for (int k = 0; k < 3; ++k) unit[k] = (e.next + k) % e.kUnits;
+      e.next = (e.next + (a.rank[r].rows[2] ? 3 : 2)) % e.kUnits;
+      if (e.lane == 0) bulk_wait_read<e.kUnits - 3>();
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[3][8];
+        gradients<D, Act>(dh + 16 * h, [&](int b, int j) {
+          if constexpr (Coded) {
+            const uint32_t word = word_of(now[b].q[2 * c1 + h], j / 2);
+            return __fmul2_rn(code_pair(bias_codes(word), 2 * (j % 2)), both(scale[b]));
+          } else {
+            float2 v;
+            unpack2<D>(word_of(now[b].q[2 * h + j / 4], j % 4), reinterpret_cast<float*>(&v));
+            return v;
+          }
+        }, w);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          if (k == 2 && !a.rank[r].rows[2]) continue;
+          st_shared16(e.piece(unit[k], 2 * h), w[k][0], w[k][1], w[k][2], w[k][3]);
+          st_shared16(e.piece(unit[k], 2 * h + 1), w[k][4], w[k][5], w[k][6], w[k][7]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < 2 || a.rank[r].rows[2]) e.store(unit[k], k, col, left, 2);
+    }
+    if constexpr (Coded && kCopies < 4) {
+#pragma unroll
+      for (int i = 0; i < 8 - 2 * kCopies; ++i)
+        kept[0].q[i] = kept[0].q[i + 2 * kCopies], kept[1].q[i] = kept[1].q[i + 2 * kCopies];
+    }
   }
   return true;
 }
