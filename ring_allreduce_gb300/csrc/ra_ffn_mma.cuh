@@ -35,10 +35,10 @@
 // and over, 1.91 ms, 1.73 PFLOP/s, where the power limit holds a plain library
 // product of that size to the same.  What bounds them beside the tensor cores is the way from L2: 64
 // bytes a cycle and SM, 15 TB/s together.  The weights' gradients reach 1.8 to
-// 1.9 PFLOP/s (their rows lie across the terms), the gradients of a and b 1.1
+// 1.9 PFLOP/s (their rows lie across the terms), the gradients of a and b 1.2
 // to 1.6: of them the epilogue, which reads two kept tensors and writes three,
-// takes 11 us a tile from codes and 13.8 from 16-bit values (SiLU; GELU 13.8 and
-// 15.3), as long as the products of some 2600 columns and more.
+// takes 10 us a tile from codes and 13.7 from 16-bit values (SiLU; GELU 13 and
+// 14.5), as long as the products of some 2400 columns and more.
 #pragma once
 
 #include "ra_ffn.cuh"
@@ -397,11 +397,12 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
     __syncwarp();
   }
   // Codes are taken from the registers they were fetched into, which asks for
-  // copies of the body; what is left moves to the front between them, as more
-  // copies than these outgrow the instruction cache.  Two ranks of 8192 columns,
-  // 4096 tokens by 2048, with one copy, two and four: SiLU 121, - and 116 us, GELU
-  // 129, 123 and 131; 16-bit values 146, - and 172.
-  constexpr int kCopies = !Coded ? 1 : Act == RA_SILU ? 4 : 2;
+  // four copies of the body; with one, those that are left move to the front.
+  // SiLU's body is short enough for four; the others outgrow the instruction
+  // cache.  Two ranks of 8192 columns, 4096 tokens by 512 and by 2048, one
+  // copy and four: SiLU 85 and 116 us, 76 and 117; GELU 93 and 117, 103 and 124;
+  // 16-bit values with SiLU 99 and 126, 124 and 146.
+  constexpr int kCopies = Coded && Act == RA_SILU ? 4 : 1;
 #pragma unroll 1
   for (int c0 = 0; c0 < 4; c0 += kCopies) {
 #pragma unroll
@@ -412,14 +413,15 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
       KeptRows<kLanes> now[2] = {kept[0], kept[1]};
       if constexpr (!Coded) {
         if (left > 0) {
-          // through the next two units: what was stored before the last two copies has been read
-          if (e.lane == 0) bulk_wait_read<e.kUnits - 2>();
-          __syncwarp();
+          // through the next unit, one after the other: the last copies' three are still being read
+          if (e.lane == 0) bulk_wait_read<e.kUnits - 1>();
 #pragma unroll
-          for (int b = 0; b < 2; ++b) kept[b].put(e.staging + (e.next + b) % e.kUnits * kUnitBytes, e.lane);
-          __syncwarp();
-#pragma unroll
-          for (int b = 0; b < 2; ++b) now[b].get(e.staging + (e.next + b) % e.kUnits * kUnitBytes, e.lane);
+          for (int b = 0; b < 2; ++b) {
+            __syncwarp();
+            kept[b].put(e.staging + e.next * kUnitBytes, e.lane);
+            __syncwarp();
+            now[b].get(e.staging + e.next * kUnitBytes, e.lane);
+          }
           __syncwarp();
           if (c < 3 && left > 32) fetch(col + 32);
         }
@@ -427,13 +429,10 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
       tmem_wait_loads();
       if (c == 3) e.release();
       if (left <= 0) continue;
-      // three units at once: what was stored before the last copy has been read
       uint32_t unit[3];
 #pragma unroll
       for (int k = 0; k < 3; ++k) unit[k] = (e.next + k) % e.kUnits;
       e.next = (e.next + (a.rank[r].rows[2] ? 3 : 2)) % e.kUnits;
-      if (e.lane == 0) bulk_wait_read<e.kUnits - 3>();
-      __syncwarp();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[3][8];
@@ -447,6 +446,10 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
             return v;
           }
         }, w);
+        if (h == 0) {   // three units at once: what was stored before the last copy has been read
+          if (e.lane == 0) bulk_wait_read<e.kUnits - 3>();
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           if (k == 2 && !a.rank[r].rows[2]) continue;
