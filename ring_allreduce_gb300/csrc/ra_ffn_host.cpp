@@ -292,8 +292,9 @@ template <class Args> ra_status run_planned(ra_ffn_handle h, FfnStage stage, con
       MmaRank<Args::kMaps>& to = a.rank[i];
       to.width = f.width(r);
       for (int k = 0; k < 2; ++k) to.scales[k] = f.scales[k][r];
+      // a rank without columns has no terms: its operands are not looked at, wherever they lie
       for (int k = 0; k < (kFew ? 4 : 5); ++k)
-        if (m.in[k].p && m.in[k].rows && m.in[k].columns) ok = ok && encode(&to.map[k], h->dtype, m.in[k], 128, in_rows(k));
+        if (to.width && m.in[k].p && m.in[k].rows) ok = ok && encode(&to.map[k], h->dtype, m.in[k], 128, in_rows(k));
       for (int k = 0; k < 5; ++k) {
         const Matrix& o = m.out[k];
         to.rows[k] = static_cast<char*>(const_cast<void*>(o.p));
