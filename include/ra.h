@@ -789,8 +789,10 @@ ra_status ra_ffn_backward(ra_ffn_handle h, const ra_ffn_backward_args* args, voi
  * largest magnitude, and whose codes are the values times fl(127 / m), rounded to binary32
  * and then to the nearest whole number (to even).  A code stands for
  * code x scale.  A group with nothing above 2^-110 is kept as zeros; one with
- * an infinity or a NaN comes back as NaN.  dtype: that of the rows; normed_dtype
- * and param_dtype: those of the normalised rows and of their weight. */
+ * an infinity or a NaN comes back as NaN.  (Where m is binary32's largest number
+ * the scale is one unit less, as 127 scales would be infinite.)  dtype: that of
+ * the rows; normed_dtype and param_dtype: those of the normalised rows and of
+ * their weight. */
 typedef struct ra_ckpt_ctx* ra_ckpt_handle;
 ra_status ra_ckpt_create(int dim, ra_dtype dtype, ra_dtype normed_dtype, ra_dtype param_dtype, ra_ckpt_handle* out);
 ra_status ra_ckpt_destroy(ra_ckpt_handle h);

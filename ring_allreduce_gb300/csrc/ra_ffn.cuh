@@ -58,6 +58,10 @@ template <int Act, bool Slope> __device__ __forceinline__ void activate(float2 a
 // Groups with nothing above this are kept as zeros: 127 / m stays finite.
 constexpr float kKeepLowest = 7.703719777548943e-34f;   // 2^-110
 
+// The largest scale whose 127th multiple is a number: that of binary32's largest
+// number would be rounded up to 8454660 * 2^98, and 127 of those are infinite.
+constexpr float kMostScale = 0x1.020406p+121f;   // 8454659 * 2^98
+
 // A group's scale and the factor to its codes, from its largest magnitude (NaN
 // where a value is NaN).  Infinite and NaN groups come back as NaN.
 __device__ __forceinline__ void group_scale(float most, float* scale, float* by) {
@@ -65,7 +69,7 @@ __device__ __forceinline__ void group_scale(float most, float* scale, float* by)
     *scale = __uint_as_float(0x7FC00000u);
     *by = 0.0f;
   } else if (most > kKeepLowest) {
-    *scale = __fdiv_rn(most, 127.0f);
+    *scale = fminf(__fdiv_rn(most, 127.0f), kMostScale);
     *by = __fdiv_rn(127.0f, most);
   } else {
     *scale = *by = 0.0f;
