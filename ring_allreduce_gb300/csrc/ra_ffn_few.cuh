@@ -160,9 +160,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
   }
   // every warp: the sums are whole (or a wait gave up, and what follows is of no use but ends)
   __syncwarp();
-  const bool ok = !some || wait(&sh.done, 0, 2);
-  (void)ok;
-  __syncwarp();
+  if (some) wait.warp(&sh.done, 0, 2);
   tensor_fence_after();
   const uint32_t mine = tmem + ((uint32_t)(warp % 4) * 32u << 16);
   const int row = (warp % 4) * 32 + lane;

@@ -384,7 +384,7 @@ __device__ __forceinline__ bool write_grad_hidden(const MmaArgs& a, const Tile& 
     scale[0] = ld_g(a.rank[r].scales[0] + at);
     scale[1] = ld_g(a.rank[r].scales[1] + at);
   }
-  if (!wait(full, parity, 4)) return false;
+  if (!wait.warp(full, parity, 4)) return false;
   tensor_fence_after();
   if constexpr (Coded) {
     if (e.lane == 0) bulk_wait_read<0>();   // all units are free
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
         ok = a.keep_bits == 8 ? write_grad_hidden<D, Act, true>(a, p, e, wait, &sh.sums_full[b], parity)
                               : write_grad_hidden<D, Act, false>(a, p, e, wait, &sh.sums_full[b], parity);
       } else {
-        ok = wait(&sh.sums_full[b], parity, 4);
+        ok = wait.warp(&sh.sums_full[b], parity, 4);
         if (!ok) break;
         tensor_fence_after();
         if constexpr (Stage == kFfnHidden)

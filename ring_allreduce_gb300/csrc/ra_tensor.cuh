@@ -154,9 +154,16 @@ struct Waits {
   ra_device_error* err;
   int job;
 
+  // For one thread that acts alone.
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity, int what) const {
     if (mbar_try_wait(bar, parity)) return true;
     return slow(bar, parity, what);
+  }
+  // For all lanes of a warp, and the same for each: lanes poll by themselves, and
+  // where one gives up while the barrier completes for another, none goes on
+  // to what the warp does together.
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, int what) const {
+    return __all_sync(0xFFFFFFFFu, (*this)(bar, parity, what));
   }
   __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, int what) const {
     const uint64_t c0 = sm_cycles();
