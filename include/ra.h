@@ -702,10 +702,10 @@ ra_status ra_ffn_create(int R, int dim, size_t inner, ra_dtype dtype, ra_activat
 ra_status ra_ffn_destroy(ra_ffn_handle h);
 ra_status ra_ffn_set_option(ra_ffn_handle h, int key, long long value);   /* as ra_norm_set_option */
 
-/* Whether a bounded device wait of the products gave up since the last call
- * (RA_ERR_TIMEOUT, outputs undefined; one record a device, shared by all
- * ra_ffn handles, and cleared by this call).  Synchronises `stream` first;
- * err may be NULL. */
+/* Whether a bounded device wait of the products gave up since this handle last
+ * asked (RA_ERR_TIMEOUT; calls since then have undefined outputs).  The record is
+ * the device's: a wait of another ra_ffn handle's call counts too, and every
+ * handle is told.  Synchronises `stream` first; err may be NULL. */
 ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_error* err);
 
 /* Per rank r: a = x w_gate_r^T, b = x w_up_r^T (binary32); hidden_r =

@@ -51,6 +51,18 @@ struct FfnArgs {
   }
 };
 
+// Waits of the products that gave up, in device memory, one record a device:
+// the first since the host took it last, and how many there have been.
+struct WaitRecord {
+  ra_device_error first;
+  uint32_t count;
+};
+// The current device's.
+cudaError_t ffn_wait_record(WaitRecord** at);
+#ifdef RA_DEBUG_BOUNDS
+cudaError_t launch_ffn_give_up(WaitRecord* record, cudaStream_t st);   // writes one down
+#endif
+
 // On the CUDA cores: any start and stride.
 cudaError_t launch_ffn_simple(int dtype, FfnStage stage, const FfnArgs& a, int sms, cudaStream_t st);
 

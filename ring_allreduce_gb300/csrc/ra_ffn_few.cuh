@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) ffn_few_kernel(const __grid_co
   tensor_fence_after();
   const uint32_t tmem = sh.tmem;
   if (!a.early) after_predecessor();   // what came before ran on beside all this
-  const Waits wait{&sh.gave_up, a.err, 8 + Stage};
+  const Waits wait{&sh.gave_up, a.record, 8 + Stage};
 
   if (warp == kFewEpilogue) {
     if (lane == 0) {

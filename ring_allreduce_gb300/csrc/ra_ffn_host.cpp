@@ -3,6 +3,7 @@
 // tensor maps of a call's operands, and which kernel runs.
 #include <cuda.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "ra_ffn.h"
@@ -14,7 +15,8 @@ struct ra_ffn_ctx {
   ra_dtype dtype, grad_dtype;
   int act;
   bool check_pointers = true;
-  ra_device_error* err;   // the device's record of waits that gave up
+  ra::WaitRecord* record; // the device's, of waits that gave up
+  uint64_t seen;          // how often something new stood there when this handle last asked
 };
 
 struct ra_ckpt_ctx {
@@ -261,7 +263,7 @@ template <class Args> ra_status run_planned(ra_ffn_handle h, FfnStage stage, con
   a.keep_bits = f.keep_bits;
   a.act = f.act;
   a.grad_f32 = f.grad_f32;
-  a.err = h->err;
+  a.record = h->record;
   a.nt = plan.nt;
   a.split = plan.split;
   a.early = stage == kFfnOut || stage == kFfnGradX;
@@ -338,6 +340,36 @@ ra_status run(ra_ffn_handle h, FfnStage stage, const FfnArgs& f, cudaStream_t st
                            : run_planned<FewArgs<kMaxRanks>>(h, stage, plan, f, st);
 }
 
+// What the handles of a device know of its record.  Whoever asks takes what is
+// new there; every handle is told once.
+struct Reports {
+  std::mutex lock;
+  uint32_t counted = 0;      // the record's count when it was last read
+  uint64_t times = 0;        // how often that was a new one
+  ra_device_error last = {};
+  uint64_t seen_now() {
+    std::lock_guard<std::mutex> hold(lock);
+    return times;
+  }
+  cudaError_t read(WaitRecord* record, cudaStream_t st) {
+    WaitRecord got;
+    cudaError_t e = cudaMemcpyAsync(&got, record, sizeof(got), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess || got.count == counted) return e;
+    counted = got.count;
+    ++times;
+    last = got.first;
+    if (!last.code) last = {2, -1, -1, -1, -1, 0, 0, 0};   // another came between the last reading and its clearing
+    e = cudaMemsetAsync(&record->first, 0, sizeof(record->first), st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+  }
+};
+
+Reports& reports_of(int device) {
+  static Reports all[64];
+  return all[device & 63];
+}
+
 ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_dtype grad_dtype, ra_ffn_handle* out) {
   if (!out) return record_error(RA_ERR_INVALID, "NULL handle pointer");
   if (R < 1 || R > kMaxRanks) return record_error(RA_ERR_INVALID, "R=%d outside [1, %d]", R, kMaxRanks);
@@ -351,12 +383,13 @@ ra_status ffn_create(int R, int dim, size_t inner, ra_dtype dtype, int act, ra_d
   if (act != RA_SILU && act != RA_GELU) return record_error(RA_ERR_INVALID, "activation %d", act);
   int dev = -1, sms = 0;
   RA_TRY(device_of(&dev, &sms));
-  ra_device_error* err = nullptr;
-  const cudaError_t e = ffn_error_record(&err);
+  WaitRecord* record = nullptr;
+  const cudaError_t e = ffn_wait_record(&record);
   if (e != cudaSuccess) return cuda_error(e, "error record");
   ra_ffn_ctx* h = new (std::nothrow) ra_ffn_ctx();
   if (!h) return record_error(RA_ERR_OOM, "host allocation failed");
-  h->err = err;
+  h->record = record;
+  h->seen = reports_of(dev).seen_now();
   h->R = R;
   h->dim = dim;
   h->inner = (int)inner;
@@ -383,6 +416,7 @@ ra_status ffn_forward(ra_ffn_handle h, const ra_ffn_forward_args* g, cudaStream_
   FfnArgs a = args_of(h, g->rows);
   a.keep_bits = g->keep_bits;
   FfnBuffers buf(h->device, h->check_pointers, g->rows);
+  buf.also(h->record, sizeof(*h->record));
   RA_TRY(add_ranks(h, buf, "x", g->x, g->xs, g->x_stride, false, a.x, &a.x_stride));
   const Shards weights[3] = {{"w_gate", g->w_gate, g->w_gate_strides, 2, true, false},
                              {"w_up", g->w_up, g->w_up_strides, 2, true, false},
@@ -417,6 +451,7 @@ ra_status ffn_backward(ra_ffn_handle h, const ra_ffn_backward_args* g, cudaStrea
   a.keep_bits = g->keep_bits;
   const size_t gb = bytes_of(h->grad_dtype);
   FfnBuffers buf(h->device, h->check_pointers, g->rows);
+  buf.also(h->record, sizeof(*h->record));
   const Shards grads[3] = {{"grad_w_gate", (const void* const*)g->grad_w_gate, g->grad_w_gate_strides, gb, true, true},
                            {"grad_w_up", (const void* const*)g->grad_w_up, g->grad_w_up_strides, gb, true, true},
                            {"grad_w_down", (const void* const*)g->grad_w_down, g->grad_w_down_strides, gb, true, true}};
@@ -582,14 +617,14 @@ ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_erro
     if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
     OnDevice on(h->device);
     if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
-    const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_error(e, "cudaStreamSynchronize");
-    ra_device_error got;
-    cudaError_t c = cudaMemcpy(&got, h->err, sizeof(got), cudaMemcpyDeviceToHost);
-    if (c == cudaSuccess && got.code) c = cudaMemset(h->err, 0, sizeof(got));
-    if (c != cudaSuccess) return cuda_error(c, "error record");
-    if (err) *err = got;
-    if (got.code) return record_error(RA_ERR_TIMEOUT, "a device wait of a feed-forward product gave up");
+    Reports& reports = reports_of(h->device);
+    std::lock_guard<std::mutex> hold(reports.lock);
+    const cudaError_t e = reports.read(h->record, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_error(e, "error record");
+    const bool news = h->seen != reports.times;
+    h->seen = reports.times;
+    if (err) *err = news ? reports.last : ra_device_error{};
+    if (news) return record_error(RA_ERR_TIMEOUT, "a device wait of a feed-forward product gave up");
     return RA_OK;
   });
 }
@@ -622,5 +657,18 @@ ra_status ra_ckpt_store(ra_ckpt_handle h, const ra_ckpt_store_args* args, void* 
 ra_status ra_ckpt_load(ra_ckpt_handle h, const ra_ckpt_load_args* args, void* stream) {
   return guarded([&] { return ckpt_load(h, args, static_cast<cudaStream_t>(stream)); });
 }
+
+#ifdef RA_DEBUG_BOUNDS
+// Debug builds: what a wait that gives up in a call of this handle writes down.
+ra_status ra_debug_ffn_give_up(ra_ffn_handle h, void* stream) {
+  return guarded([&]() -> ra_status {
+    FfnBuffers buf(h->device, false, 0);
+    buf.also(h->record, sizeof(*h->record));
+    RA_TRY(buf.check());
+    const cudaError_t e = launch_ffn_give_up(h->record, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RA_OK : cuda_error(e, "give-up launch");
+  });
+}
+#endif
 
 }  // extern "C"

@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) ffn_mma_kernel(const __grid_co
   tensor_fence_after();
   const uint32_t tmem = sh.tmem;
   after_predecessor();   // what came before ran on beside all this
-  const Waits wait{&sh.gave_up, a.err, Stage};
+  const Waits wait{&sh.gave_up, a.record, Stage};
   const int64_t tiles = a.tiles, step = gridDim.x / 2;
 
   if (warp == 8) {

@@ -48,7 +48,7 @@ struct MmaArgsOf {
   int split;              // CTAs that share the terms of a tile's sums: 1, 2, 4 or 8
   int early;              // the stream's kernel before this one is the call's own
   int ring;               // bytes of the operands' ring
-  ra_device_error* err;   // where a wait that gives up says so
+  WaitRecord* record;     // where a wait that gives up says so
   MmaRank<Maps> rank[Ranks];
 };
 using MmaArgs = MmaArgsOf<8, 16>;
@@ -66,7 +66,5 @@ constexpr int kFewRing = 104 * 1024, kFewRingAlone = 208 * 1024;
 constexpr int kFewABytes = 128 * 64 * 2, kFewMostStages = 12;
 __host__ __device__ constexpr int few_sums(int stage) { return stage == kFfnHidden ? 2 : 1; }   // accumulators
 __host__ __device__ constexpr int few_stage_bytes(int stage, int nt) { return few_sums(stage) * kFewABytes + nt * 128; }
-// The current device's record of waits that gave up (device memory).
-cudaError_t ffn_error_record(ra_device_error** at);
 
 }  // namespace ra

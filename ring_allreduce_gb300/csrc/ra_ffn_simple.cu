@@ -11,6 +11,7 @@
 // one token of 4095 x 16383 in eight: 2.0 ms and 0.07).
 #include "ra_ffn.cuh"
 #include "ra_ffn_mma.h"
+#include "ra_tensor.cuh"
 
 namespace ra {
 
@@ -187,11 +188,24 @@ template <class D> cudaError_t by_stage(FfnStage stage, const FfnArgs& a, int sm
 
 }  // namespace
 
-__device__ ra_device_error g_ffn_error;
+__device__ WaitRecord g_ffn_waits;
 
-cudaError_t ffn_error_record(ra_device_error** at) {
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_ffn_error);
+cudaError_t ffn_wait_record(WaitRecord** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_ffn_waits);
 }
+
+#ifdef RA_DEBUG_BOUNDS
+namespace {
+__global__ void give_up_kernel(WaitRecord* record) { record_give_up(record, 0, 0, 1u); }
+}  // namespace
+
+cudaError_t launch_ffn_give_up(WaitRecord* record, cudaStream_t st) {
+  const cudaError_t e = debug_upload(st);
+  if (e != cudaSuccess) return e;
+  give_up_kernel<<<1, 1, 0, st>>>(record);
+  return cudaGetLastError();
+}
+#endif
 
 cudaError_t launch_ffn_simple(int dtype, FfnStage stage, const FfnArgs& a, int sms, cudaStream_t st) {
   const cudaError_t e = debug_upload(st);

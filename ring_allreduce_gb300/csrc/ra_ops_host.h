@@ -106,6 +106,12 @@ template <int Most> class BuffersOf {
     return add(name, -1, p, elem, count, &stride, output, 1);
   }
 
+  // Memory of the library's own that the call's kernels write (bounds checks of debug builds).
+  void also(const void* p, size_t bytes) {
+    own_ = (uintptr_t)p;
+    own_bytes_ = bytes;
+  }
+
   ra_status check() {
     const bool apart = spans_apart();
     for (int i = 0; i < count_; ++i) {
@@ -184,9 +190,11 @@ template <int Most> class BuffersOf {
     ra::DebugTable& t = ra::debug_table();
     t.count = 0;
     t.report = ra::debug_report();
+    if (own_bytes_) t.r[t.count++] = {own_, own_ + own_bytes_};
+    const int room = ra::kDebugRanges - t.count;
     for (int i = 0; i < count_; ++i) {
       ra::DebugRange& d = t.r[t.count < ra::kDebugRanges ? t.count++ : ra::kDebugRanges - 1];
-      const bool more = i >= ra::kDebugRanges;   // what the table has no room for shares its last range
+      const bool more = i >= room;   // what the table has no room for shares its last range
       d.lo = more ? std::min<uint64_t>(d.lo, b_[i].lo) : b_[i].lo;
       d.hi = more ? std::max<uint64_t>(d.hi, b_[i].lo + b_[i].span) : b_[i].lo + b_[i].span;
     }
@@ -198,6 +206,8 @@ template <int Most> class BuffersOf {
   int device_;
   size_t rows_;
   bool check_pointers_;
+  uintptr_t own_ = 0;
+  size_t own_bytes_ = 0;
   char text_[32];
 };
 

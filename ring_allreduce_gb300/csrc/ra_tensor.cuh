@@ -9,6 +9,7 @@
 #include <cuda.h>
 
 #include "ra_device.cuh"
+#include "ra_ffn.h"
 
 namespace ra {
 
@@ -149,9 +150,14 @@ __device__ __forceinline__ void tmem_load8(uint32_t tmem, uint32_t* v) {
 // loops; what is in flight is given time to land before the CTA ends.
 constexpr long long kWaitCycles = 4000000000ll;
 
+__device__ __forceinline__ void record_give_up(WaitRecord* record, int what, int job, uint32_t parity) {
+  record_wait_error(&record->first, 2u, what, job, (int)blockIdx.x, -1, 0u, parity);
+  if (RA_ACCESS_OK(&record->count, sizeof(record->count), 2u)) atomicAdd(&record->count, 1u);
+}
+
 struct Waits {
   volatile int* gave_up;   // in shared memory
-  ra_device_error* err;
+  WaitRecord* record;
   int job;
 
   // For one thread that acts alone.
@@ -171,7 +177,7 @@ struct Waits {
       if (*gave_up) return false;
       if ((long long)(sm_cycles() - c0) > kWaitCycles) {
         *gave_up = 1;
-        record_wait_error(err, 2u, what, job, (int)blockIdx.x, -1, 0u, parity);
+        record_give_up(record, what, job, parity);
         return false;
       }
     }

@@ -306,7 +306,8 @@ class FeedForward(_Handle):
                    grad_up, grad_xs, grad_w_gate, grad_w_up, grad_w_down, gate_scales, up_scales)
 
     def device_status(self, stream=None):
-        """(Status, DeviceError) after synchronising the stream: whether a bounded wait of a product on this device gave up."""
+        """(Status, DeviceError) after synchronising the stream: whether a bounded wait of a product on this device,
+        of whichever FeedForward, gave up since this one last asked."""
         err = binding.DeviceError()
         if self._config is None:
             raise ValueError("the handle is closed")
