@@ -201,12 +201,21 @@ struct Matrices {
   }
 };
 
+// Tokens of a tile whose sums may be split: the CTAs' shares of both projections' sums, as much as this,
+// lie in a ring of kFewRing.
+constexpr int kFewMostSplit = 96;
+static_assert(2 * kFewMostSplit * 128 * 4 <= kFewRing && kFewMostSplit % 8 == 0, "a cluster's sums outgrow the ring");
+
 // Which kernel a product runs on: pairs of CTAs with tiles of 256 x 256, or
 // CTAs with 128 of the weights' rows against `nt` tokens, `split` to a tile's sums.
 struct Plan {
   bool few;
   int nt, split;
 };
+
+#ifdef RA_DEBUG_BOUNDS
+thread_local Plan debug_plan{false, 0, 0};   // split 0: none
+#endif
 
 // The plan with the shortest estimate, in microseconds.  The estimates' form is
 // what bounds either kernel -- steps of 64 terms, one after another, in as
@@ -219,6 +228,10 @@ struct Plan {
 // 16384 in 8 ranks: 54 us large, 46 few; of 777, 1544 x 5005 in 3: 26 and 48.)
 Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens, int keep_bits) {
   if (stage == kFfnGradW) return {false, 0, 0};   // sums over the tokens: nothing to split
+#ifdef RA_DEBUG_BOUNDS
+  if (debug_plan.split)
+    return {debug_plan.few, (int)std::min<int64_t>(debug_plan.nt, (tokens + 15) / 16 * 16), debug_plan.split};
+#endif
   const bool dual = stage == kFfnHidden, back = stage == kFfnGradHidden;
   const int64_t N = dual || back ? h->C : h->dim, K = dual || back ? h->dim : h->C;
   const auto up = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
@@ -231,7 +244,7 @@ Plan plan_of(const ra_ffn_ctx* h, FfnStage stage, int64_t tokens, int keep_bits)
   const double token = back ? 0.15 : !dual ? 0.07 : keep_bits == 8 ? 0.21 : 0.025;   // a token's outputs
   for (const int most : {16, 32, 64, 96, 128}) {
     const int nt = (int)std::min<int64_t>(most, up(tokens, 16) * 16);
-    for (int split = 1; split <= 8 && (split == 1 || nt <= 96); split *= 2) {
+    for (int split = 1; split <= 8 && (split == 1 || nt <= kFewMostSplit); split *= 2) {
       const double ctas = (double)(up(N, 128) * up(tokens, nt) * h->R * split);
       const double rounds = std::ceil(ctas / (2 * h->sms)), on_sm = ctas > h->sms ? 2 : 1;
       const int stage_bytes = few_stage_bytes(stage, nt);
@@ -659,7 +672,18 @@ ra_status ra_ckpt_load(ra_ckpt_handle h, const ra_ckpt_load_args* args, void* st
 }
 
 #ifdef RA_DEBUG_BOUNDS
-// Debug builds: what a wait that gives up in a call of this handle writes down.
+// Debug builds: the plan of this host thread's next calls, but for the weights' gradients, which have one;
+// among those that the estimate can come to. split 0: the estimate's again.
+ra_status ra_debug_ffn_plan(int few, int nt, int split) {
+  const bool valid = split == 0 || (!few && split == 1) ||
+                     (few && nt >= 16 && nt <= 128 && nt % 16 == 0 &&
+                      (split == 1 || ((split == 2 || split == 4 || split == 8) && nt <= kFewMostSplit)));
+  if (!valid) return RA_ERR_INVALID;
+  debug_plan = {few != 0, nt, split};
+  return RA_OK;
+}
+
+// What a wait that gives up in a call of this handle writes down.
 ra_status ra_debug_ffn_give_up(ra_ffn_handle h, void* stream) {
   return guarded([&]() -> ra_status {
     FfnBuffers buf(h->device, false, 0);
