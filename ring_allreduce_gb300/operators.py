@@ -114,6 +114,14 @@ def _code(name, dtype):
     return _CODE[dtype]
 
 
+def _size(name, value, bits=31):
+    """A size as the library's types hold it: what ctypes would cut to fewer bits is refused."""
+    value = int(value)
+    if not -2 ** bits <= value < 2 ** bits:
+        raise ValueError(f"{name} {value} is out of range")
+    return value
+
+
 def _listed(arg):
     """An argument that can be gone through twice."""
     if arg is None or isinstance(arg, (torch.Tensor, list, tuple)):
@@ -157,7 +165,7 @@ class BlockNorm(_Handle):
 
     def __init__(self, R, dim, dtype="bf16", residual_dtype=None, param_dtype=None, eps=1e-6, scale=1.0):
         super().__init__(dtype)
-        self.R, self.dim, self.eps, self.scale = int(R), int(dim), float(eps), float(scale)
+        self.R, self.dim, self.eps, self.scale = _size("R", R), _size("dim", dim), float(eps), float(scale)
         codes = (_code("dtype", dtype), _code("residual_dtype", residual_dtype or dtype),
                  _code("param_dtype", param_dtype or dtype))
         h = _P()
@@ -200,7 +208,7 @@ class VocabHead(_Handle):
 
     def __init__(self, R, vocab, dtype="bf16", temperature=1.0):
         super().__init__(dtype)
-        self.R, self.vocab, self.temperature = int(R), int(vocab), float(temperature)
+        self.R, self.vocab, self.temperature = _size("R", R), _size("vocab", vocab, 63), float(temperature)
         if self.vocab < 0:
             raise ValueError(f"vocab {vocab}")
         code = _code("dtype", dtype)
@@ -256,7 +264,7 @@ class FeedForward(_Handle):
 
     def __init__(self, R, dim, inner, dtype="bf16", activation="silu", grad_dtype=None):
         super().__init__(dtype)
-        self.R, self.dim, self.inner, self.dtype = int(R), int(dim), int(inner), dtype
+        self.R, self.dim, self.inner, self.dtype = _size("R", R), _size("dim", dim), _size("inner", inner, 63), dtype
         if self.inner < 0:
             raise ValueError(f"inner {inner}")
         if activation not in _ACTIVATION:
@@ -334,7 +342,7 @@ class Checkpoint(_Handle):
 
     def __init__(self, dim, dtype="bf16", normed_dtype=None, param_dtype=None):
         super().__init__(dtype)
-        self.dim = int(dim)
+        self.dim = _size("dim", dim)
         codes = [_code("dtype", dtype), _code("normed_dtype", normed_dtype or dtype)]
         codes.append(_code("param_dtype", param_dtype or normed_dtype or dtype))
         h = _P()
