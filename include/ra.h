@@ -740,7 +740,8 @@ ra_status ra_ffn_forward(ra_ffn_handle h, const ra_ffn_forward_args* args, void*
 
 /* The gradient, from the kept a and b.  With dh = grad_out w_down_r^T
  * (binary32): grad_gate_r = dh b activation'(a), grad_up_r = dh activation(a),
- * hidden_r = activation(a) b, each rounded to dtype; and from these, each only
+ * hidden_r = activation(a) b (of codes' a and b: less exact than what forward
+ * wrote), each rounded to dtype; and from these, each only
  * where it is asked for (not NULL), grad_x_r = grad_gate_r w_gate_r + grad_up_r w_up_r,
  * grad_w_gate_r = grad_gate_r^T x, grad_w_up_r = grad_up_r^T x, grad_w_down_r =
  * hidden_r^T grad_out (sums over no rows are zeros).  grad_out is the gradient of every rank's

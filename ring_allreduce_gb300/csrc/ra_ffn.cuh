@@ -14,10 +14,13 @@ namespace ra {
 // P(-z) = e^(-z^2/2) R(z), z >= 0, where R falls smoothly from 1/2: a
 // polynomial of degree 8 in t = 1 / (1 + 0.23 z), fitted to R's values at
 // Chebyshev points by reweighted least squares until its largest relative
-// error (4.7e-8 up to z = 13.3, beyond which e^(-z^2/2) is below binary32's
-// normal numbers) stood still; 7 units of 2^-24 evaluated in binary32.  P keeps its
-// relative accuracy where 1 + erf cancels, for twenty instructions with the
-// derivative, which takes the same exponential.
+// error stood still: 6.2e-8 up to z = 13.3, beyond which e^(-z^2/2) is below
+// binary32's normal numbers (8.0e-8 with binary32's 0.23); 7 units of 2^-24
+// evaluated in binary32.  Nothing cancels, as it does in 1 + erf; but the
+// exponent is rounded twice, so that P is off by up to 7 + 1.2 z^2 units of 2^-24
+// (23 by z = 5, 45 by z = 8): less than a hundredth of the 16-bit outputs' own
+// rounding.  Twenty instructions with the derivative, which takes the same
+// exponential.
 //
 // Arithmetic is on pairs, two binary32 operations an instruction.
 __device__ __forceinline__ float reciprocal(float x) {   // 0 from 2^126 on
@@ -99,7 +102,6 @@ __device__ __forceinline__ uint32_t codes4(const float* v, float by) {
 __device__ __forceinline__ float code_raised(uint32_t biased, int k) {
   return __uint_as_float(__byte_perm(biased, 0x4B000000u, 0x7440u + (uint32_t)k));
 }
-__device__ __forceinline__ float code_value(uint32_t biased, int k) { return code_raised(biased, k) - 8388736.0f; }
 // codes k and k + 1
 __device__ __forceinline__ float2 code_pair(uint32_t biased, int k) {
   return __fadd2_rn(make_float2(code_raised(biased, k), code_raised(biased, k + 1)), both(-8388736.0f));

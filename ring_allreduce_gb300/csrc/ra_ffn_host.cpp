@@ -70,8 +70,8 @@ ra_status add_ranks(const ra_ffn_ctx* h, FfnBuffers& buf, const char* name, cons
   return RA_OK;
 }
 
-ra_status add_scales(const ra_ffn_ctx* h, FfnBuffers& buf, const char* name, size_t rows, const float* const* p,
-                     bool output, float** at) {
+ra_status add_scales(const ra_ffn_ctx* h, FfnBuffers& buf, const char* name, const float* const* p, bool output,
+                     float** at) {
   if (!p) return record_error(RA_ERR_INVALID, "%s: NULL pointer array", name);
   for (int r = 0; r < h->ranks; ++r) {
     const size_t width = (size_t)(r + 1 < h->ranks ? h->C : h->inner - r * h->C);
@@ -89,8 +89,8 @@ ra_status add_kept(const ra_ffn_ctx* h, FfnBuffers& buf, size_t rows, int bits, 
   RA_TRY(add_shards(h, buf, rows, {"gate", gate, gate_strides, elem, false, output}, a->kept[0], a->kept_stride[0]));
   RA_TRY(add_shards(h, buf, rows, {"up", up, up_strides, elem, false, output}, a->kept[1], a->kept_stride[1]));
   if (bits == 8) {
-    RA_TRY(add_scales(h, buf, "gate_scales", rows, gate_scales, output, a->scales[0]));
-    RA_TRY(add_scales(h, buf, "up_scales", rows, up_scales, output, a->scales[1]));
+    RA_TRY(add_scales(h, buf, "gate_scales", gate_scales, output, a->scales[0]));
+    RA_TRY(add_scales(h, buf, "up_scales", up_scales, output, a->scales[1]));
   }
   return RA_OK;
 }
@@ -299,7 +299,7 @@ template <class Args> ra_status run_planned(ra_ffn_handle h, FfnStage stage, con
   const int launches = (h->R + Args::kRanks - 1) / Args::kRanks, most = (h->R + launches - 1) / launches;
   for (int r0 = 0; r0 < h->R; r0 += most) {
     const int ranks = h->R - r0 < most ? h->R - r0 : most;
-    for (int& level : a.level) level = 3;
+    for (int& level : a.level) level = 2;
     for (int i = 0; i < ranks; ++i) {
       const int r = r0 + i;
       const Matrices m(stage, f, r);
@@ -316,10 +316,10 @@ template <class Args> ra_status run_planned(ra_ffn_handle h, FfnStage stage, con
         to.stride[k] = o.stride * o.elem;
         if (!o.p) continue;
         const uintptr_t bits = o.bits();
-        const int level = bits % 32 == 0 ? 3 : bits % 16 == 0 ? 2 : bits % 8 == 0 ? 1 : 0;
+        const int level = bits % 16 == 0 ? 2 : bits % 8 == 0 ? 1 : 0;
         if (level < a.level[k]) a.level[k] = level;
         if constexpr (!kFew)
-          if (k < m.outs && level >= 2 && o.rows && o.columns)
+          if (k < m.outs && level == 2 && o.rows && o.columns)
             ok = ok && encode(&to.map[first_rows(as) + k], h->dtype, o, 64, 32);
       }
       if (!ok) return record_error(RA_ERR_CUDA, "cuTensorMapEncodeTiled failed");

@@ -21,8 +21,8 @@
 // Operands are taken as they lie: rows along the terms (projections, dh) or
 // across them (everything else); nothing is transposed or laid out anew.
 //
-// The products keep the shared memory's path busy (a tile's 64 terms: 16 KB
-// written and 16 KB read an SM in 512 cycles), and whatever the epilogue sends
+// The products keep the shared memory's path busy (a tile's 64 terms: 32 KB
+// written and as much read an SM in 512 cycles), and whatever the epilogue sends
 // through it costs them its time.  A store to global memory by lanes that each
 // hold a row takes a cycle of it a row and 16 bytes; so the epilogue lays its
 // outputs down in shared memory, 64 bytes of 32 rows at a time, and has them
@@ -166,7 +166,7 @@ template <int Stage> struct Epilogue {
   __device__ __forceinline__ void store(uint32_t unit, int k, int column, int left, int elem) const {
     const MmaRank<MmaArgs::kMaps>& t = a.rank[r];
     // (a copy is cut off to 16 bytes, not to the element)
-    if (a.level[k] >= 2 && (left * elem >= 64 || left * elem % 16 == 0)) {
+    if (a.level[k] == 2 && (left * elem >= 64 || left * elem % 16 == 0)) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -302,7 +302,7 @@ template <int kLanes> struct KeptRows {
       const char* const at = from + y * stride;
       uint32_t w[4] = {};
       if (y < e.rows && mine > 0) {
-        if (level >= 2 && mine >= 16) {
+        if (level == 2 && mine >= 16) {
           if (RA_ACCESS_OK(at, 16u, 1u)) {
             const uint4 x = *reinterpret_cast<const uint4*>(at);
             w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;

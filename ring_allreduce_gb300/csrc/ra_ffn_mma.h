@@ -42,7 +42,7 @@ struct MmaArgsOf {
   int dim, keep_bits;
   int act;                // ra_activation
   int grad_f32;
-  int level[5];           // rows of every rank on multiples of: 3, 32 bytes; 2, 16; 1, 8; 0, less
+  int level[5];           // rows of every rank on multiples of: 2, 16 bytes (of tensor maps); 1, 8; 0, less
   // for few tokens alone
   int nt;                 // tokens of a tile, a multiple of 16, at most 128
   int split;              // CTAs that share the terms of a tile's sums: 1, 2, 4 or 8

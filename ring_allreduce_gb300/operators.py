@@ -305,8 +305,9 @@ class FeedForward(_Handle):
 
         grad_parts: 1 or R x [T, dim], the gradient of every rank's partial
         product.  Writes grad_gate and grad_up (R x [T, width], the gradients
-        of a and b), hidden (as forward wrote it, from the kept a and b; None
-        where grad_w_down is), grad_xs (R x [T, dim], the ranks' partial
+        of a and b), hidden (activation(a) b of the kept a and b, from which
+        grad_w_down is made: from codes it is less exact than what forward wrote,
+        which it replaces in the same tensors; None only without grad_w_down), grad_xs (R x [T, dim], the ranks' partial
         gradients of x) and the weights' gradients (R x [width, dim] of
         grad_dtype), each None where it is not wanted.  16-bit gate and up may be overwritten by grad_gate and
         grad_up."""
