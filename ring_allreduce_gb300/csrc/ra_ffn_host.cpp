@@ -630,9 +630,15 @@ ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_erro
     if (!h) return record_error(RA_ERR_INVALID, "NULL handle");
     OnDevice on(h->device);
     if (on.status != cudaSuccess) return cuda_error(on.status, "cudaSetDevice");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &capture);
+    if (e != cudaSuccess) return cuda_error(e, "cudaStreamIsCapturing");
+    if (capture != cudaStreamCaptureStatusNone)   // to wait for it would end the capture
+      return record_error(RA_ERR_UNSUPPORTED, "the status of a stream that is being captured");
     Reports& reports = reports_of(h->device);
     std::lock_guard<std::mutex> hold(reports.lock);
-    const cudaError_t e = reports.read(h->record, static_cast<cudaStream_t>(stream));
+    e = reports.read(h->record, st);
     if (e != cudaSuccess) return cuda_error(e, "error record");
     const bool news = h->seen != reports.times;
     h->seen = reports.times;

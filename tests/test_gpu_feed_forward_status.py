@@ -59,3 +59,26 @@ def test_every_handle_is_told():
                          capture_output=True, text=True, timeout=600)
     assert res.returncode == 0, res.stdout[-2000:] + res.stderr[-4000:]
     assert "stray accesses: 0 0" in res.stdout, res.stdout
+
+
+def test_status_does_not_end_a_capture():
+    """Asked of a stream that is being captured it is refused, and the capture goes on."""
+    from ring_allreduce_gb300 import build
+    build.build()
+    from ring_allreduce_gb300 import operators as ops
+    from ring_allreduce_gb300.binding import Status
+    import test_gpu_feed_forward as f
+    b = f.Block(80, 2, 30, 136, 300)
+    op = ops.FeedForward(2, 136, 300)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.forward(op)
+        with pytest.raises(ops.RAError) as err:
+            op.device_status()
+        b.backward(op)
+    assert err.value.status == Status.ERR_UNSUPPORTED
+    graph.replay()
+    assert op.device_status()[0] == Status.OK
+    b.before = [b.kept(r) for r in range(2)]
+    b.check_forward()
+    b.check_backward()
