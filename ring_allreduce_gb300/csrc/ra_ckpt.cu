@@ -3,11 +3,14 @@
 //
 // A half warp takes a group of 128 columns, a lane eight of them side by side:
 // the group's largest magnitude is found by four shuffles, and every group is
-// read and written once.  DRAM bounds it: 16384 x 8192 f32 kept in 101 us (0.98 of the
+// read and written once.  DRAM bounds it where rows start on 16-byte boundaries: 16384 x 8192 f32 kept in 101 us (0.98 of the
 // copy bandwidth), brought back with bf16 normalised rows in 149 (0.93); 8192 x
 // 5120 bf16 brought back in 21.6 (0.87).  Two groups a half warp in flight and
 // 32 CTAs an SM over the kernel's time: more groups held more registers (eight: 119
 // and 96 us for the 101 and, 16384 x 4096 bf16, 37), fewer CTAs left a tail (eight: 121, 60).
+// Further off: f32 rows brought back without or with f32 normalised rows (131 and 258 us, 0.76 and 0.69: a lane's 32
+// bytes go as two accesses, each of which fills half of its sectors), and rows off the 8-column grid, an element a
+// lane (65536 x 2047 bf16 kept in 108 us, 0.56, brought back in 107, with normalised rows in 179).
 #include "ra_ffn.cuh"
 
 namespace ra {
