@@ -708,7 +708,7 @@ ra_status ra_ffn_set_option(ra_ffn_handle h, int key, long long value);   /* as 
 /* Whether a bounded device wait of the products gave up since this handle last
  * asked (RA_ERR_TIMEOUT; calls since then have undefined outputs).  The record is
  * the device's: a wait of another ra_ffn handle's call counts too, and every
- * handle is told.  Synchronises `stream` first, which may not be one that is
+ * handle is told (a new one also of what nobody has asked about yet).  Synchronises `stream` first, which may not be one that is
  * being captured (RA_ERR_UNSUPPORTED); err may be NULL. */
 ra_status ra_ffn_get_device_status(ra_ffn_handle h, void* stream, ra_device_error* err);
 
